@@ -303,6 +303,140 @@ int gemm_strided_batched_noalloc(int64_t M, int64_t N, int64_t K, const void *A,
 /* Bytes of the static scratch gemm_strided_batched_noalloc splits K through. */
 int64_t gemm_noalloc_scratch_bytes(void);
 
+/* ---- Int8 products and expert routing ------------------------------------------
+ * Element formats of the entry points below (f32, f16 and bf16 as TSM_ROWSUM_*),
+ * and the integer formats of expert ids. */
+#define TSM_F32 0
+#define TSM_F16 1
+#define TSM_BF16 2
+#define TSM_I8 3
+#define TSM_I32 4
+#define TSM_I64 5
+
+/*
+ * quantize_i8 -- rows to int8 codes with one float32 scale each, for gemm_i8:
+ * with m the largest magnitude of row r,
+ *     scale[r] := m / 127,    Q[r][c] := nearest whole number to 127 X[r][c] / m,
+ * ties to even, so X[r][c] is Q[r][c] * scale[r] to within half a step.  The
+ * codes are those of the exact quotient (no intermediate rounding).  A row of
+ * zeros gets scale 0 and codes 0; a row that holds a NaN or an infinity gets
+ * scale NaN and codes 0, so every product with it is NaN.
+ *   R, C       : rows and columns per group, >= 0.  C = 0 writes scales of 0.
+ *   X, ldx     : X[g*strideX + r*ldx + c], format xdtype (TSM_F32, TSM_F16 or
+ *                TSM_BF16), aligned to its element; ldx >= 0 (rows may overlap
+ *                or repeat).
+ *   Q, ldq     : codes, ldq >= C; padding is not written.
+ *   scale      : scale[g*stride_scale + r], stride_scale >= R for several groups.
+ *   rows       : NULL, or a DEVICE array of `groups` int32 counts as gemm_grouped
+ *                takes them: rows at and past rows[g] are neither read nor written.
+ *   groups     : matrices (1 for a single one, whose strides are ignored).
+ * Errors and stream semantics as for gemm; Q and scale must not overlap X or
+ * each other.
+ */
+int quantize_i8(int64_t R, int64_t C, const void *X, int64_t ldx, int64_t strideX, int xdtype, int8_t *Q, int64_t ldq,
+                int64_t strideQ, float *scale, int64_t stride_scale, const int32_t *rows, int64_t groups,
+                void *stream);
+
+/*
+ * gemm_i8 -- product of int8 codes with a scale for each token (row of A) and
+ * each channel (column of B):
+ *     C[i][j] := scale_a[i] * scale_b[j] * sum_k A[i][k] * B[j*ldb + k].
+ * The sum is an exact int32 (so K <= 131071); it is converted to float32 once,
+ * multiplied by scale_a, then by scale_b, and rounded to the output format.
+ *   A, lda     : codes, row-major M x K, lda >= K, any alignment.
+ *   B, ldb     : codes of the weight stored N x K (column-major B), ldb >= K.
+ *   scale_a/_b : device float32, M and N of them; NULL means ones.
+ *   C, ldc     : row-major result, out_dtype TSM_F32, TSM_F16 or TSM_BF16.
+ * K = 0 gives sums of 0 (times the scales).  Errors and stream semantics as for
+ * gemm; C must not overlap an operand or a scale.
+ */
+int gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *scale_a, const int8_t *B,
+            int64_t ldb, const float *scale_b, void *C, int64_t ldc, int out_dtype, void *stream);
+
+/*
+ * gemm_i8_strided_batched -- `batch` such products at element strides (0 shares
+ * an operand or its scales; strideC keeps the outputs disjoint), with the fused
+ * activation of gemm_strided_batched_act applied after the scales.
+ */
+int gemm_i8_strided_batched(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64_t strideA,
+                            const float *scale_a, int64_t stride_sa, const int8_t *B, int64_t ldb, int64_t strideB,
+                            const float *scale_b, int64_t stride_sb, void *C, int64_t ldc, int64_t strideC,
+                            int64_t batch, int out_dtype, int activation, float slope, void *stream);
+
+/*
+ * gemm_i8_grouped -- the same over a mixture of experts' slabs: problem g uses
+ * its first m_g = min(max(rows[g], 0), M) rows, counts in device memory, as
+ * gemm_grouped.  Rows past m_g of A, scale_a and C are neither read nor written.
+ */
+int gemm_i8_grouped(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64_t strideA,
+                    const float *scale_a, int64_t stride_sa, const int8_t *B, int64_t ldb, int64_t strideB,
+                    const float *scale_b, int64_t stride_sb, void *C, int64_t ldc, int64_t strideC,
+                    const int32_t *rows, int64_t groups, int out_dtype, int activation, float slope, void *stream);
+
+/* tsm_gemm_i8_kernel_name -- the kernel a gemm_i8_strided_batched call (rows NULL)
+ * or a gemm_i8_grouped call would launch, or NULL. */
+const char *tsm_gemm_i8_kernel_name(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64_t strideA,
+                                    const int8_t *B, int64_t ldb, int64_t strideB, void *C, int64_t ldc,
+                                    int64_t strideC, int64_t batch, const int32_t *rows, int out_dtype);
+
+/*
+ * moe_sort -- the row of each (token, choice) in its expert's slab.  The slabs
+ * of all experts are one matrix of experts * capacity rows, expert e's from row
+ * e * capacity (what gemm_grouped and gemm_i8_grouped take with
+ * strideA = capacity * lda).  With e = ids[t*ld_ids + j],
+ *     positions[t*topk + j] := e * capacity + r,
+ * r the number of entries before (t, j), in token order, that chose e; -1 when
+ * e is outside [0, experts) (a padded token) or r >= capacity (dropped).
+ *     counts[e] := all entries that chose e (those past capacity among them;
+ * the grouped products clamp to their M).
+ *   ids        : DEVICE expert ids, idtype TSM_I32 or TSM_I64, ld_ids >= topk.
+ *   experts    : at most 512.  experts * capacity and tokens * topk below 2^31.
+ *   workspace  : DEVICE memory of moe_sort_workspace_bytes(...) bytes, 4-byte
+ *                aligned, its contents irrelevant before and after (NULL where
+ *                that is 0).  Calls in flight at once must not share one.
+ * The result is the same on every call.  tokens = 0 or topk = 0 writes counts of 0.
+ */
+int moe_sort(int64_t tokens, int64_t topk, const void *ids, int64_t ld_ids, int idtype, int64_t experts,
+             int64_t capacity, int32_t *positions, int32_t *counts, void *workspace, int64_t workspace_bytes,
+             void *stream);
+int64_t moe_sort_workspace_bytes(int64_t tokens, int64_t topk, int64_t experts);
+
+/*
+ * moe_dispatch -- slabs[positions[t*topk + j]] := X[t], and slab_scale likewise
+ * from scale, for every entry with a position.  Slab rows without an entry keep
+ * what they held.  Positions at or past `slots` count as none; no two entries
+ * may have the same one (moe_sort gives distinct ones).
+ *   X, ldx     : tokens x hidden, dtype TSM_F32, TSM_F16, TSM_BF16 or TSM_I8.
+ *   slabs      : slots x hidden, ld_slabs >= hidden.
+ *   scale, slab_scale : a float32 per token and per slab row (the scales of
+ *                quantize_i8), or both NULL.
+ * Its gradient is moe_combine with weights NULL.
+ */
+int moe_dispatch(int64_t tokens, int64_t topk, int64_t hidden, const void *X, int64_t ldx, int dtype,
+                 const float *scale, const int32_t *positions, int64_t slots, void *slabs, int64_t ld_slabs,
+                 float *slab_scale, void *stream);
+
+/*
+ * moe_combine -- Y[t] := sum_j weights[t*topk + j] * slabs[positions[t*topk + j]],
+ * over the entries with a position (no others are read, so a NaN weight or
+ * stale slab row of one without a position does not matter); float32 sums in
+ * the order of j, rounded once.  weights NULL means ones.  A token without any
+ * gets zeros.  dtype (slabs and Y): TSM_F32, TSM_F16 or TSM_BF16.
+ */
+int moe_combine(int64_t tokens, int64_t topk, int64_t hidden, const void *slabs, int64_t ld_slabs, int64_t slots,
+                int dtype, const int32_t *positions, const float *weights, void *Y, int64_t ldy, void *stream);
+
+/*
+ * moe_combine_backward -- the gradients of moe_combine from dY (tokens x hidden):
+ *     dslabs[positions[t*topk + j]]  := weights[t*topk + j] * dY[t],
+ *     dweights[t*topk + j]           := <dY[t], slabs[positions[t*topk + j]]>,
+ * float32 sums; dweights is 0 where there is no position, and dslabs rows
+ * without an entry keep what they held.  dslabs must not overlap slabs.
+ */
+int moe_combine_backward(int64_t tokens, int64_t topk, int64_t hidden, const void *dY, int64_t lddy, const void *slabs,
+                         int64_t ld_slabs, int64_t slots, int dtype, const int32_t *positions, const float *weights,
+                         void *dslabs, int64_t ld_dslabs, float *dweights, void *stream);
+
 /* Static text for a status code ("success", "invalid value", ...). */
 const char *tsm_status_string(int status);
 

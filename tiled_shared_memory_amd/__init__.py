@@ -9,14 +9,16 @@ HIP kernels.
 
 from __future__ import annotations
 
-from ._lib import (TSM_ACT_LEAKY_RELU, TSM_ACT_NONE, TSM_ACT_RELU, TSM_BF16_BF16, TSM_BF16_F16,  # noqa: F401
-                   TSM_BF16_F32, TSM_COL, TSM_ERROR_INVALID_VALUE, TSM_ERROR_LAUNCH, TSM_ERROR_NOT_SUPPORTED,
-                   TSM_F16_BF16, TSM_F16_F16, TSM_F16_F32, TSM_ROW, TSM_ROWSUM_BF16, TSM_ROWSUM_F16, TSM_ROWSUM_F32,
-                   TSM_SUCCESS, TsmError, gemm, gemm_ex, gemm_grouped, gemm_strided_batched,
-                   gemm_noalloc_scratch_bytes, gemm_strided_batched_act, gemm_strided_batched_ex,
-                   gemm_strided_batched_noalloc, gemm_strided_batched_ws, gemm_workspace_bytes,
-                   load, rowsum, tsm_gemm_grouped_kernel_name, tsm_gemm_kernel_name, tsm_gemm_ws_kernel_name,
-                   tsm_last_error_detail, tsm_rowsum_kernel_name, tsm_status_string)
+from ._lib import (TSM_ACT_LEAKY_RELU, TSM_ACT_NONE, TSM_ACT_RELU, TSM_BF16, TSM_BF16_BF16, TSM_BF16_F16,  # noqa: F401
+                   TSM_BF16_F32, TSM_COL, TSM_ERROR_INVALID_VALUE, TSM_ERROR_LAUNCH, TSM_ERROR_NOT_SUPPORTED, TSM_F16,
+                   TSM_F16_BF16, TSM_F16_F16, TSM_F16_F32, TSM_F32, TSM_I8, TSM_I32, TSM_I64, TSM_ROW, TSM_ROWSUM_BF16,
+                   TSM_ROWSUM_F16, TSM_ROWSUM_F32, TSM_SUCCESS, TsmError, gemm, gemm_ex, gemm_grouped, gemm_i8,
+                   gemm_i8_grouped, gemm_i8_strided_batched, gemm_noalloc_scratch_bytes, gemm_strided_batched,
+                   gemm_strided_batched_act, gemm_strided_batched_ex, gemm_strided_batched_noalloc,
+                   gemm_strided_batched_ws, gemm_workspace_bytes, load, moe_combine, moe_combine_backward,
+                   moe_dispatch, moe_sort, moe_sort_workspace_bytes, quantize_i8, rowsum,
+                   tsm_gemm_grouped_kernel_name, tsm_gemm_i8_kernel_name, tsm_gemm_kernel_name,
+                   tsm_gemm_ws_kernel_name, tsm_last_error_detail, tsm_rowsum_kernel_name, tsm_status_string)
 
 
 def dtype_code(in_dtype, out_dtype) -> int:
@@ -101,3 +103,298 @@ def matmul(a, b, *, out=None, out_dtype=None, activation=None, slope=0.01, works
                             out.stride(0) if out.dim() == 3 else 0, batch, code, _ACTIVATIONS[activation], slope,
                             workspace, ws_bytes, stream)
     return out
+
+
+# ---- int8 products and expert routing --------------------------------------------------------------------------
+
+
+def _bad(text):
+    raise TsmError(TSM_ERROR_INVALID_VALUE, text)
+
+
+_FORMATS = None
+
+
+def _format(t):
+    """The library's code of a tensor's dtype (TSM_F32 .. TSM_I64), or None."""
+    global _FORMATS
+    if _FORMATS is None:
+        import torch
+
+        _FORMATS = {torch.float32: TSM_F32, torch.float16: TSM_F16, torch.bfloat16: TSM_BF16, torch.int8: TSM_I8,
+                    torch.int32: TSM_I32, torch.int64: TSM_I64}
+    return _FORMATS.get(t.dtype)
+
+
+def _wants(what, t, formats, shape=None):
+    """Check a tensor argument: on a GPU, of one of the formats, of the shape.  Returns its format."""
+    if not t.is_cuda:
+        _bad(f"{what} is not on a GPU")
+    f = _format(t)
+    if f not in formats:
+        _bad(f"{what} has dtype {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        _bad(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} wanted")
+    return f
+
+
+def _rows_ld(what, t):
+    """Leading dimension of the last two dims of a tensor whose rows are contiguous."""
+    if t.numel() == 0:
+        return max(1, t.shape[-1])
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        _bad(f"{what}: rows must be contiguous")
+    return t.stride(-2) if t.shape[-2] > 1 else max(1, t.shape[-1])
+
+
+def _packed(what, t):
+    if not t.is_contiguous():
+        _bad(f"{what} must be contiguous")
+
+
+def _launch(stream, fn, first, *others):
+    """fn(stream handle) on the GPU that every tensor is on, on its current stream unless one is given."""
+    import torch
+
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            _bad(f"tensors on {dev} and {t.device}")
+    if dev.index == torch.cuda.current_device():
+        return fn(stream)
+    with torch.cuda.device(dev):
+        return fn(stream)
+
+
+_FLOATS = (TSM_F32, TSM_F16, TSM_BF16)
+
+
+def quantize(x, *, rows=None, out=None, scale=None, stream=None):
+    """(codes, scales) of the rows of ``x`` (..., R, C) in float32, float16 or bfloat16: int8 codes with
+    ``x ~ codes * scales[..., None]``, the scales float32 of shape (..., R).
+
+    2-D or 3-D.  With ``rows`` (int32, one count per matrix of a 3-D ``x``, on the GPU) only the first rows of each
+    are read and written.
+    """
+    import torch
+
+    if x.dim() not in (2, 3):
+        _bad("x must be 2-D or 3-D")
+    f = _wants("x", x, _FLOATS)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _wants("out", out, (TSM_I8,), x.shape)
+    _wants("scale", scale, (TSM_F32,), x.shape[:-1])
+    G = x.shape[0] if x.dim() == 3 else 1
+    if rows is not None:
+        _wants("rows", rows, (TSM_I32,), (G,))
+        _packed("rows", rows)
+    if scale.shape[-1] > 1 and scale.stride(-1) != 1:
+        _bad("scale: rows must be contiguous")
+    ldx, ldq = _rows_ld("x", x), _rows_ld("out", out)
+    sx, sq, ss = (x.stride(0), out.stride(0), scale.stride(0)) if x.dim() == 3 else (0, 0, 0)
+    _launch(stream, lambda s: quantize_i8(x.shape[-2], x.shape[-1], x, ldx, sx, f, out, ldq, sq, scale, ss, rows, G, s),
+            x, out, scale, rows)
+    return out, scale
+
+
+def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, activation=None, slope=0.01, stream=None):
+    """C = act(scale_a[..., None] * scale_b * (A.B)) for int8 CUDA tensors ``a`` (..., M, K) and ``b`` (..., K, N).
+
+    ``a`` has contiguous rows and ``b`` is column-major (``w.t()`` of a weight stored N x K).  ``scale_a`` (..., M) and
+    ``scale_b`` (..., N) are float32 (None: ones).  2-D operands give one product, 3-D ones a strided batch (a batch
+    dim of size 1 broadcasts); with ``rows`` (int32 counts on the GPU, one per problem) the grouped product over a
+    mixture of experts' slabs.  The result is float32 (default), float16 or bfloat16; ``activation`` as for ``matmul``.
+    """
+    import torch
+
+    if a.dim() not in (2, 3) or b.dim() not in (2, 3):
+        _bad("a and b must be 2-D or 3-D")
+    _wants("a", a, (TSM_I8,))
+    _wants("b", b, (TSM_I8,))
+    M, K = a.shape[-2], a.shape[-1]
+    K2, N = b.shape[-2], b.shape[-1]
+    if K != K2:
+        _bad(f"inner sizes differ: {K} vs {K2}")
+    batched = a.dim() == 3 or b.dim() == 3
+    ba, bb = (a.shape[0] if a.dim() == 3 else 1), (b.shape[0] if b.dim() == 3 else 1)
+    if ba != bb and ba != 1 and bb != 1:
+        _bad(f"batch sizes differ: {ba} vs {bb}")
+    batch = ba if bb == 1 else bb
+    shape = (batch, M, N) if batched else (M, N)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or torch.float32, device=a.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        _bad(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
+    f = _wants("out", out, _FLOATS, shape)
+    if activation not in _ACTIVATIONS:
+        _bad(f"unknown activation {activation!r}")
+
+    def scales(what, t, op, n):
+        """Batch stride of an operand's scales."""
+        if t is None:
+            return 0
+        _wants(what, t, (TSM_F32,), (*op.shape[:-2], n))
+        if n > 1 and t.stride(-1) != 1:
+            _bad(f"{what}: scales must be contiguous")
+        return t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else 0
+
+    ssa, ssb = scales("scale_a", scale_a, a, M), scales("scale_b", scale_b, b, N)
+    if N > 0 and K > 1 and b.stride(-2) != 1:
+        _bad("b must be column-major (the transpose of a weight stored N x K)")
+    lda, ldb, ldc = _rows_ld("a", a), _rows_ld("b", b.transpose(-1, -2)), _rows_ld("out", out)
+    sa, sb = (a.stride(0) if ba > 1 else 0), (b.stride(0) if bb > 1 else 0)
+    sc = out.stride(0) if batched else 0
+    act = _ACTIVATIONS[activation]
+    if rows is None:
+        _launch(stream, lambda s: gemm_i8_strided_batched(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb,
+                                                          out, ldc, sc, batch, f, act, slope, s),
+                a, b, out, scale_a, scale_b)
+    else:
+        _wants("rows", rows, (TSM_I32,), (batch,))
+        _packed("rows", rows)
+        _launch(stream, lambda s: gemm_i8_grouped(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb, out, ldc,
+                                                  sc, rows, batch, f, act, slope, s),
+                a, b, out, scale_a, scale_b, rows)
+    return out
+
+
+def sort_workspace_for(ids, experts):
+    """A CUDA tensor for ``sort_tokens(..., workspace=...)``, or None when the sizes need none."""
+    import torch
+
+    n = moe_sort_workspace_bytes(ids.shape[0], ids.shape[1], experts)
+    return torch.empty(n, dtype=torch.uint8, device=ids.device) if n else None
+
+
+def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspace=None, stream=None):
+    """(positions, counts) of the experts' ids (tokens, topk), int32 or int64: the row of each choice in the slabs
+    (experts * capacity rows, expert e's from e * capacity), in token order, -1 for an id outside [0, experts) or past
+    the capacity; and how many choices each expert got (int32, those past the capacity among them).
+
+    A workspace (see ``sort_workspace_for``) is allocated when the sizes need one and none is given.
+    """
+    import torch
+
+    if ids.dim() != 2:
+        _bad("ids must be 2-D")
+    f = _wants("ids", ids, (TSM_I32, TSM_I64))
+    if positions is None:
+        positions = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
+    if counts is None:
+        counts = torch.empty((experts,), dtype=torch.int32, device=ids.device)
+    _wants("positions", positions, (TSM_I32,), ids.shape)
+    _wants("counts", counts, (TSM_I32,), (experts,))
+    _packed("positions", positions)
+    _packed("counts", counts)
+    if workspace is None:
+        workspace = sort_workspace_for(ids, experts)
+    if workspace is not None:
+        if not workspace.is_cuda:
+            _bad("workspace is not on a GPU")
+        _packed("workspace", workspace)
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _launch(stream, lambda s: moe_sort(ids.shape[0], ids.shape[1], ids, _rows_ld("ids", ids), f, experts, capacity,
+                                       positions, counts, workspace, nbytes, s),
+            ids, positions, counts, workspace)
+    return positions, counts
+
+
+def _slab_args(what, slabs, positions, tokens, hidden):
+    """Check 2-D slabs (slots, hidden) and the positions (tokens, topk)."""
+    if slabs.dim() != 2 or (hidden is not None and slabs.shape[1] != hidden):
+        _bad(f"{what} must be 2-D with {hidden} columns")
+    if positions.dim() != 2 or (tokens is not None and positions.shape[0] != tokens):
+        _bad(f"positions must be 2-D with {tokens} rows")
+    _wants("positions", positions, (TSM_I32,))
+    _packed("positions", positions)
+
+
+def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale=None, stream=None):
+    """Token rows ``x`` (tokens, hidden) at their ``positions`` (tokens, topk) in the slabs (slots, hidden), float32,
+    float16, bfloat16 or int8.
+
+    ``out`` keeps its other rows; without it the slabs are allocated with ``slots`` rows (the others unset).  With
+    ``scale`` (float32, one per token) also the slab rows' scales: returns (slabs, scales).
+    """
+    import torch
+
+    if x.dim() != 2:
+        _bad("x must be 2-D")
+    f = _wants("x", x, _FLOATS + (TSM_I8,))
+    if out is None:
+        if slots is None:
+            _bad("slots or out is needed")
+        out = torch.empty((slots, x.shape[1]), dtype=x.dtype, device=x.device)
+    elif slots is not None and out.shape[0] != slots:
+        _bad(f"out has {out.shape[0]} rows, slots is {slots}")
+    _slab_args("out", out, positions, x.shape[0], x.shape[1])
+    _wants("out", out, (f,))
+    if scale is not None:
+        _wants("scale", scale, (TSM_F32,), (x.shape[0],))
+        _packed("scale", scale)
+        if out_scale is None:
+            out_scale = torch.empty((out.shape[0],), dtype=torch.float32, device=x.device)
+        _wants("out_scale", out_scale, (TSM_F32,), (out.shape[0],))
+        _packed("out_scale", out_scale)
+    elif out_scale is not None:
+        _bad("out_scale without scale")
+    _launch(stream, lambda s: moe_dispatch(x.shape[0], positions.shape[1], x.shape[1], x, _rows_ld("x", x), f, scale,
+                                           positions, out.shape[0], out, _rows_ld("out", out), out_scale, s),
+            x, out, positions, scale, out_scale)
+    return out if scale is None else (out, out_scale)
+
+
+def combine_tokens(slabs, positions, weights=None, *, out=None, stream=None):
+    """Y[t] = sum_j weights[t, j] * slabs[positions[t, j]] over the choices with a position, float32 sums in the order
+    of j; ``weights`` float32 (tokens, topk), None for ones.  Y has the slabs' dtype (float32, float16 or bfloat16)."""
+    import torch
+
+    _slab_args("slabs", slabs, positions, None, None)
+    f = _wants("slabs", slabs, _FLOATS)
+    tokens, hidden = positions.shape[0], slabs.shape[1]
+    if out is None:
+        out = torch.empty((tokens, hidden), dtype=slabs.dtype, device=slabs.device)
+    _wants("out", out, (f,), (tokens, hidden))
+    if weights is not None:
+        _wants("weights", weights, (TSM_F32,), positions.shape)
+        _packed("weights", weights)
+    _launch(stream, lambda s: moe_combine(tokens, positions.shape[1], hidden, slabs, _rows_ld("slabs", slabs),
+                                          slabs.shape[0], f, positions, weights, out, _rows_ld("out", out), s),
+            slabs, out, positions, weights)
+    return out
+
+
+def dispatch_tokens_backward(dslabs, positions, *, out=None, stream=None):
+    """Gradient of ``dispatch_tokens`` with respect to ``x``: dX[t] = sum_j dslabs[positions[t, j]]."""
+    return combine_tokens(dslabs, positions, None, out=out, stream=stream)
+
+
+def combine_tokens_backward(dy, slabs, positions, weights=None, *, out=None, dweights=None, stream=None):
+    """(dslabs, dweights) of ``combine_tokens`` from ``dy`` (tokens, hidden): dslabs[positions[t, j]] =
+    weights[t, j] * dy[t] (``out``; its other rows are kept, or zeros where it is allocated here) and
+    dweights[t, j] = <dy[t], slabs[positions[t, j]]> (float32, 0 without a position)."""
+    import torch
+
+    if dy.dim() != 2:
+        _bad("dy must be 2-D")
+    f = _wants("dy", dy, _FLOATS)
+    _slab_args("slabs", slabs, positions, dy.shape[0], dy.shape[1])
+    _wants("slabs", slabs, (f,))
+    if out is None:
+        out = torch.zeros(slabs.shape, dtype=slabs.dtype, device=slabs.device)
+    _wants("out", out, (f,), slabs.shape)
+    if dweights is None:
+        dweights = torch.empty(positions.shape, dtype=torch.float32, device=dy.device)
+    _wants("dweights", dweights, (TSM_F32,), positions.shape)
+    _packed("dweights", dweights)
+    if weights is not None:
+        _wants("weights", weights, (TSM_F32,), positions.shape)
+        _packed("weights", weights)
+    _launch(stream, lambda s: moe_combine_backward(dy.shape[0], positions.shape[1], dy.shape[1], dy,
+                                                   _rows_ld("dy", dy), slabs, _rows_ld("slabs", slabs), slabs.shape[0],
+                                                   f, positions, weights, out, _rows_ld("out", out), dweights, s),
+            dy, slabs, out, positions, weights, dweights)
+    return out, dweights

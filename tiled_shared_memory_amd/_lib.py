@@ -39,6 +39,13 @@ TSM_ROWSUM_F32 = 0
 TSM_ROWSUM_F16 = 1
 TSM_ROWSUM_BF16 = 2
 
+TSM_F32 = 0
+TSM_F16 = 1
+TSM_BF16 = 2
+TSM_I8 = 3
+TSM_I32 = 4
+TSM_I64 = 5
+
 # Every function the header declares, with its ctypes signature.
 _I64, _PTR, _INT = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
 SIGNATURES = {
@@ -68,6 +75,20 @@ SIGNATURES = {
     "gemm_noalloc_scratch_bytes": ([], _I64),
     "tsm_gemm_ws_kernel_name": ([_I64, _I64, _I64, _PTR, _I64, _INT, _I64, _PTR, _I64, _INT, _I64, _PTR, _I64, _I64,
                                  _I64, _INT, _PTR, _I64], ctypes.c_char_p),
+    "quantize_i8": ([_I64, _I64, _PTR, _I64, _I64, _INT, _PTR, _I64, _I64, _PTR, _I64, _PTR, _I64, _PTR], _INT),
+    "gemm_i8": ([_I64, _I64, _I64, _PTR, _I64, _PTR, _PTR, _I64, _PTR, _PTR, _I64, _INT, _PTR], _INT),
+    "gemm_i8_strided_batched": ([_I64, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _PTR, _I64, _I64, _PTR, _I64, _PTR,
+                                 _I64, _I64, _I64, _INT, _INT, ctypes.c_float, _PTR], _INT),
+    "gemm_i8_grouped": ([_I64, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _PTR, _I64, _I64, _PTR, _I64, _PTR, _I64,
+                         _I64, _PTR, _I64, _INT, _INT, ctypes.c_float, _PTR], _INT),
+    "tsm_gemm_i8_kernel_name": ([_I64, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64, _I64, _PTR,
+                                 _INT], ctypes.c_char_p),
+    "moe_sort": ([_I64, _I64, _PTR, _I64, _INT, _I64, _I64, _PTR, _PTR, _PTR, _I64, _PTR], _INT),
+    "moe_sort_workspace_bytes": ([_I64, _I64, _I64], _I64),
+    "moe_dispatch": ([_I64, _I64, _I64, _PTR, _I64, _INT, _PTR, _PTR, _I64, _PTR, _I64, _PTR, _PTR], _INT),
+    "moe_combine": ([_I64, _I64, _I64, _PTR, _I64, _I64, _INT, _PTR, _PTR, _PTR, _I64, _PTR], _INT),
+    "moe_combine_backward": ([_I64, _I64, _I64, _PTR, _I64, _PTR, _I64, _I64, _INT, _PTR, _PTR, _PTR, _I64, _PTR,
+                              _PTR], _INT),
 }
 
 
@@ -230,3 +251,69 @@ def rowsum(R, C, X, row_stride, col_stride, xdtype, out, stream=None):
 def tsm_rowsum_kernel_name(R, C, X, row_stride, col_stride, xdtype, out):
     r = load().tsm_rowsum_kernel_name(R, C, _ptr(X), row_stride, col_stride, xdtype, _ptr(out))
     return r.decode() if r else None
+
+
+def quantize_i8(R, C, X, ldx, strideX, xdtype, Q, ldq, strideQ, scale, stride_scale, rows, groups, stream=None):
+    lib = load()
+    return _check(lib, lib.quantize_i8(R, C, _ptr(X), ldx, strideX, xdtype, _ptr(Q), ldq, strideQ, _ptr(scale),
+                                       stride_scale, _ptr(rows), groups, _stream(stream)))
+
+
+def gemm_i8(M, N, K, A, lda, scale_a, B, ldb, scale_b, C, ldc, out_dtype, stream=None):
+    lib = load()
+    return _check(lib, lib.gemm_i8(M, N, K, _ptr(A), lda, _ptr(scale_a), _ptr(B), ldb, _ptr(scale_b), _ptr(C), ldc,
+                                   out_dtype, _stream(stream)))
+
+
+def gemm_i8_strided_batched(M, N, K, A, lda, strideA, scale_a, stride_sa, B, ldb, strideB, scale_b, stride_sb, C, ldc,
+                            strideC, batch, out_dtype, activation, slope, stream=None):
+    lib = load()
+    return _check(lib, lib.gemm_i8_strided_batched(M, N, K, _ptr(A), lda, strideA, _ptr(scale_a), stride_sa, _ptr(B),
+                                                   ldb, strideB, _ptr(scale_b), stride_sb, _ptr(C), ldc, strideC,
+                                                   batch, out_dtype, activation, slope, _stream(stream)))
+
+
+def gemm_i8_grouped(M, N, K, A, lda, strideA, scale_a, stride_sa, B, ldb, strideB, scale_b, stride_sb, C, ldc,
+                    strideC, rows, groups, out_dtype, activation, slope, stream=None):
+    lib = load()
+    return _check(lib, lib.gemm_i8_grouped(M, N, K, _ptr(A), lda, strideA, _ptr(scale_a), stride_sa, _ptr(B), ldb,
+                                           strideB, _ptr(scale_b), stride_sb, _ptr(C), ldc, strideC, _ptr(rows),
+                                           groups, out_dtype, activation, slope, _stream(stream)))
+
+
+def tsm_gemm_i8_kernel_name(M, N, K, A, lda, strideA, B, ldb, strideB, C, ldc, strideC, batch, rows, out_dtype):
+    r = load().tsm_gemm_i8_kernel_name(M, N, K, _ptr(A), lda, strideA, _ptr(B), ldb, strideB, _ptr(C), ldc, strideC,
+                                       batch, _ptr(rows), out_dtype)
+    return r.decode() if r else None
+
+
+def moe_sort(tokens, topk, ids, ld_ids, idtype, experts, capacity, positions, counts, workspace, workspace_bytes,
+             stream=None):
+    lib = load()
+    return _check(lib, lib.moe_sort(tokens, topk, _ptr(ids), ld_ids, idtype, experts, capacity, _ptr(positions),
+                                    _ptr(counts), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_sort_workspace_bytes(tokens, topk, experts):
+    return int(load().moe_sort_workspace_bytes(tokens, topk, experts))
+
+
+def moe_dispatch(tokens, topk, hidden, X, ldx, dtype, scale, positions, slots, slabs, ld_slabs, slab_scale,
+                 stream=None):
+    lib = load()
+    return _check(lib, lib.moe_dispatch(tokens, topk, hidden, _ptr(X), ldx, dtype, _ptr(scale), _ptr(positions), slots,
+                                        _ptr(slabs), ld_slabs, _ptr(slab_scale), _stream(stream)))
+
+
+def moe_combine(tokens, topk, hidden, slabs, ld_slabs, slots, dtype, positions, weights, Y, ldy, stream=None):
+    lib = load()
+    return _check(lib, lib.moe_combine(tokens, topk, hidden, _ptr(slabs), ld_slabs, slots, dtype, _ptr(positions),
+                                       _ptr(weights), _ptr(Y), ldy, _stream(stream)))
+
+
+def moe_combine_backward(tokens, topk, hidden, dY, lddy, slabs, ld_slabs, slots, dtype, positions, weights, dslabs,
+                         ld_dslabs, dweights, stream=None):
+    lib = load()
+    return _check(lib, lib.moe_combine_backward(tokens, topk, hidden, _ptr(dY), lddy, _ptr(slabs), ld_slabs, slots,
+                                                dtype, _ptr(positions), _ptr(weights), _ptr(dslabs), ld_dslabs,
+                                                _ptr(dweights), _stream(stream)))

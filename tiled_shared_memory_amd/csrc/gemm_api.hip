@@ -5,7 +5,6 @@
 // nothing.  Offsets and extents are computed in 64 bits with explicit overflow
 // checks (Intel XPU Triton README, "Avoid int32 Overflow": a stride product that
 // wraps silently addresses the wrong memory).
-#include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
@@ -16,37 +15,11 @@
 #include <string>
 
 #include "gemm_internal.hpp"
+#include "host_checks.hpp"
 #include "tsm_gemm.h"
 
 namespace tsm {
 namespace {
-
-thread_local char g_detail[256];
-
-int fail(int code, const char *fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_detail, sizeof g_detail, fmt, ap);
-  va_end(ap);
-  return code;
-}
-
-bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
-bool add_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_add_overflow(a, b, out); }
-
-// Number of elements spanned by `batch` matrices of rows x cols with leading
-// dimension ld and batch stride s: (batch-1)*s + (rows-1)*ld + cols.
-bool extent(int64_t batch, int64_t s, int64_t rows, int64_t ld, int64_t cols, int64_t *out) {
-  int64_t a, b, c;
-  if (!mul_ok(batch - 1, s, &a) || !mul_ok(rows - 1, ld, &b)) return false;
-  if (!add_ok(a, b, &c) || !add_ok(c, cols, out)) return false;
-  return true;
-}
-
-bool ranges_overlap(const void *p, int64_t pbytes, const void *q, int64_t qbytes) {
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  return a < b + (uintptr_t)qbytes && b < a + (uintptr_t)pbytes;
-}
 
 enum class Kernel {
   None, Masked8, MaskedU, Small8, SmallU, Tile32, Tile16, Tile16NN, TileW, TileWNN, Tile16TN, Tile16TT, TileWTT, Skinny,

@@ -1,0 +1,374 @@
+// Expert routing for gfx950: tokens sorted by expert, rows into the experts'
+// slabs and back, with weights, and the gradients.
+//
+// The slabs are what gemm_grouped multiplies: expert e owns rows
+// e * capacity .. of one matrix.  Entry (t, j) is choice j of token t.
+//
+//   sort      pos[t][j] = e * capacity + r,  e = ids[t][j],  r = the number of
+//             entries before (t, j), in token order, with the same expert;
+//             -1 when e names no expert or r >= capacity
+//   dispatch  slab[pos[t][j]] = X[t]
+//   combine   Y[t] = sum_j w[t][j] slab[pos[t][j]]
+//   backward  dslab[pos[t][j]] = w[t][j] dY[t];  dw[t][j] = <dY[t], slab[pos[t][j]]>
+#include "elems.hpp"
+#include "moe_internal.hpp"
+
+namespace tsm {
+namespace {
+
+// ---- sort ------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+
+// Expert of flat entry i, or -1 when it names none.
+template <bool ID64>
+__device__ __forceinline__ int expert_of(const SortArgs &a, int64_t i) {
+  const int64_t at = a.ld == a.topk ? i : i / a.topk * a.ld + i % a.topk;
+  if constexpr (ID64) {
+    const int64_t e = ((const int64_t *)a.ids)[at];
+    return e >= 0 && e < a.experts ? (int)e : -1;
+  } else {
+    const int32_t e = ((const int32_t *)a.ids)[at];
+    return e >= 0 && e < a.experts ? e : -1;
+  }
+}
+
+// Entries per expert of each tile, into hist[block][expert].  Integer sums: the
+// order of the atomics does not matter.
+template <bool ID64>
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
+  extern __shared__ int32_t sh[];
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) sh[e] = 0;
+  __syncthreads();
+  const int64_t n = a.tokens * a.topk, i0 = (int64_t)blockIdx.x * SortInfo::kTile;
+  for (int64_t i = i0 + threadIdx.x; i < i0 + SortInfo::kTile && i < n; i += kSortThreads) {
+    const int e = expert_of<ID64>(a, i);
+    if (e >= 0) atomicAdd(&sh[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) a.hist[(int64_t)blockIdx.x * a.experts + e] = sh[e];
+}
+
+// Positions of one tile's entries.  Each wave owns a run of consecutive
+// entries; LDS holds, per wave and expert, first the wave's count, then the
+// next rank it gives out.
+template <bool ID64>
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
+  extern __shared__ int32_t sh[];  // [waves][experts], then [experts]: entries before this tile
+  volatile int32_t *next = sh;
+  int32_t *before = sh + kSortWaves * a.experts;
+  const int E = a.experts, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < (kSortWaves + 1) * E; i += kSortThreads) sh[i] = 0;
+  __syncthreads();
+  const int64_t n = a.tokens * a.topk;
+  const int64_t tile = a.hist ? SortInfo::kTile : SortInfo::kOneBlock;
+  const int64_t i0 = (int64_t)blockIdx.x * tile;
+  const int64_t left = n - i0 < tile ? n - i0 : tile;
+  const int steps = (int)((left + kSortThreads - 1) / kSortThreads);  // 64 entries per wave and step
+  const int64_t w0 = i0 + (int64_t)wave * steps * 64;
+  for (int s = 0; s < steps; ++s) {
+    const int64_t i = w0 + s * 64 + lane;
+    const int e = i < n && i < i0 + tile ? expert_of<ID64>(a, i) : -1;
+    if (e >= 0) atomicAdd(&sh[wave * E + e], 1);
+  }
+  if (a.hist) {
+    // entries of the tiles before: thread tid adds up expert tid % E over every (1024 / E)-th tile
+    const int per = kSortThreads / E, g = threadIdx.x / E, e = threadIdx.x % E;
+    if (g < per) {
+      int32_t sum = 0;
+#pragma unroll 8
+      for (int b = g; b < (int)blockIdx.x; b += per) sum += a.hist[(int64_t)b * E + e];
+      if (sum) atomicAdd(&before[e], sum);
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kSortThreads) {
+    int32_t at = before[e];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int32_t c = sh[w * E + e];
+      sh[w * E + e] = at;
+      at += c;
+    }
+    if (blockIdx.x == gridDim.x - 1) a.counts[e] = at;
+  }
+  __syncthreads();
+  const int bits = 32 - __clz(E);  // enough for 0 .. experts
+  for (int s = 0; s < steps; ++s) {
+    const int64_t i = w0 + s * 64 + lane;
+    const bool in = i < n && i < i0 + tile;
+    const int e = in ? expert_of<ID64>(a, i) : -1;
+    // lanes with the same expert as this one
+    const uint32_t key = e < 0 ? (uint32_t)E : (uint32_t)e;
+    uint64_t same = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t m = __ballot((key >> b) & 1);
+      same &= (key >> b) & 1 ? m : ~m;
+    }
+    const int mine = __popcll(same & ((1ull << lane) - 1)), all = __popcll(same);
+    int32_t base = 0;
+    if (e >= 0) base = next[wave * E + e];
+    // every lane has read before the last of each expert writes (LDS
+    // operations of a wave complete in order)
+    if (e >= 0 && mine == all - 1) next[wave * E + e] = base + all;
+    if (in) {
+      const int64_t r = (int64_t)base + mine;
+      a.positions[i] = e >= 0 && r < a.capacity ? (int32_t)(e * a.capacity + r) : -1;
+    }
+  }
+}
+
+// ---- rows --------------------------------------------------------------------
+constexpr int kThreads = 256;
+
+// Slab row of entry i, or -1.  Rows past the slabs count as none, so no position can write outside them.
+__device__ __forceinline__ int64_t slot_of(const MoveArgs &a, int64_t i) {
+  const int32_t p = a.positions[i];
+  return p >= 0 && p < a.slots ? p : -1;
+}
+
+// Thread tid's place: token t and its first chunk, TPR threads to a row, U chunks to a thread TPR apart.
+template <int TPR, int U>
+__device__ __forceinline__ void place(const MoveArgs &a, int64_t &t, int64_t &c) {
+  const uint32_t g = blockIdx.x / (uint32_t)a.segs, seg = blockIdx.x - g * (uint32_t)a.segs;
+  t = a.t0 + (int64_t)g * (kThreads / TPR) + threadIdx.x / TPR;
+  c = (int64_t)seg * (TPR * U) + threadIdx.x % TPR;
+}
+
+template <int FMT, int TPR, int U>
+__global__ __launch_bounds__(kThreads) void dispatch_kernel(MoveArgs a) {
+  constexpr int ES = fmt_bytes(FMT), N = 16 / ES;
+  int64_t t, c0;
+  place<TPR, U>(a, t, c0);
+  if (t >= a.tokens) return;
+  const char *x = (const char *)a.X + t * a.ldx * ES;
+  const int64_t chunks = (a.hidden + N - 1) / N, whole = a.hidden / N;
+  Raw16 v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (c0 + u * TPR < whole) v[u] = *(const Raw16 *)(x + (c0 + u * TPR) * 16);
+  for (int j = 0; j < a.topk; ++j) {
+    const int64_t s = slot_of(a, t * a.topk + j);
+    if (s < 0) continue;
+    char *y = (char *)a.Y + s * a.ldy * ES;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + u * TPR;
+      if (c < whole)
+        *(Raw16 *)(y + c * 16) = v[u];
+      else if (c < chunks)
+        for (int64_t i = whole * N; i < a.hidden; ++i) put_bits<FMT>(y, i, elem_bits<FMT>(x, i));
+    }
+    if (a.scale && c0 == 0) a.slab_scale[s] = a.scale[t];
+  }
+}
+
+template <int FMT, int TPR, int U>
+__global__ __launch_bounds__(kThreads) void combine_kernel(MoveArgs a) {
+  constexpr int ES = fmt_bytes(FMT), N = 16 / ES;
+  int64_t t, c0;
+  place<TPR, U>(a, t, c0);
+  if (t >= a.tokens) return;
+  const int64_t chunks = (a.hidden + N - 1) / N, whole = a.hidden / N;
+  char *y = (char *)a.Y + t * a.ldy * ES;
+  float acc[U][N] = {};
+  for (int j = 0; j < a.topk; ++j) {
+    const int64_t s = slot_of(a, t * a.topk + j);
+    if (s < 0) continue;
+    const float w = a.weights ? a.weights[t * a.topk + j] : 1.f;
+    const char *x = (const char *)a.X + s * a.ldx * ES;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = c0 + u * TPR;
+      if (c < whole) {
+        Vec<FMT> v;
+        v.unpack(*(const Raw16 *)(x + c * 16));
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[u][i] = fmaf(w, v.v[i], acc[u][i]);
+      } else if (c < chunks) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (whole * N + i < a.hidden) acc[u][i] = fmaf(w, elem_f32<FMT>(elem_bits<FMT>(x, whole * N + i)), acc[u][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t c = c0 + u * TPR;
+    Vec<FMT> v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v.v[i] = acc[u][i];
+    if (c < whole) {
+      *(Raw16 *)(y + c * 16) = v.pack();
+    } else if (c < chunks) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (whole * N + i < a.hidden) put_bits<FMT>(y, whole * N + i, f32_elem<FMT>(v.v[i]));
+    }
+  }
+}
+
+// One workgroup (TPR = 256) or wave (TPR = 64) per token; JB choices at a time, so dY is read ceil(topk / JB)
+// times (from cache after the first).
+template <int FMT, int TPR, int JB>
+__global__ __launch_bounds__(kThreads) void combine_backward_kernel(MoveArgs a) {
+  constexpr int ES = fmt_bytes(FMT), N = 16 / ES;
+  __shared__ float part[kThreads / 64][JB];
+  const int lane = threadIdx.x % TPR;
+  const int64_t t = a.t0 + (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+  if (t >= a.tokens) return;  // whole waves; with TPR = 256 no workgroup lies past the tokens
+  const int64_t chunks = (a.hidden + N - 1) / N, whole = a.hidden / N;
+  const char *dy = (const char *)a.X + t * a.ldx * ES;
+  for (int j0 = 0; j0 < a.topk; j0 += JB) {
+    int64_t slot[JB];
+    float w[JB], dot[JB];
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+      const bool in = j0 + j < a.topk;
+      slot[j] = in ? slot_of(a, t * a.topk + j0 + j) : -1;
+      w[j] = in && a.weights ? a.weights[t * a.topk + j0 + j] : 1.f;
+      dot[j] = 0.f;
+    }
+    for (int64_t c = lane; c < chunks; c += TPR) {
+      if (c < whole) {
+        Vec<FMT> g;
+        g.unpack(*(const Raw16 *)(dy + c * 16));
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+          if (slot[j] < 0) continue;
+          Vec<FMT> v, d;
+          v.unpack(*(const Raw16 *)((const char *)a.S + slot[j] * a.lds * ES + c * 16));
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            dot[j] = fmaf(g.v[i], v.v[i], dot[j]);
+            d.v[i] = w[j] * g.v[i];
+          }
+          *(Raw16 *)((char *)a.Y + slot[j] * a.ldy * ES + c * 16) = d.pack();
+        }
+      } else {
+        for (int64_t i = whole * N; i < a.hidden; ++i) {
+          const float g = elem_f32<FMT>(elem_bits<FMT>(dy, i));
+#pragma unroll
+          for (int j = 0; j < JB; ++j) {
+            if (slot[j] < 0) continue;
+            dot[j] = fmaf(g, elem_f32<FMT>(elem_bits<FMT>((const char *)a.S + slot[j] * a.lds * ES, i)), dot[j]);
+            put_bits<FMT>((char *)a.Y + slot[j] * a.ldy * ES, i, f32_elem<FMT>(w[j] * g));
+          }
+        }
+      }
+    }
+    if (!a.dweights) continue;
+#pragma unroll
+    for (int j = 0; j < JB; ++j) dot[j] = wave_add(dot[j]);
+    if constexpr (TPR > 64) {
+      __syncthreads();  // the previous choices' sums are read
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) part[threadIdx.x >> 6][j] = dot[j];
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < JB; ++j) dot[j] = (part[0][j] + part[1][j]) + (part[2][j] + part[3][j]);
+    }
+    if (lane == 0)
+#pragma unroll
+      for (int j = 0; j < JB; ++j)
+        if (j0 + j < a.topk) a.dweights[t * a.topk + j0 + j] = dot[j];
+  }
+}
+
+// Tokens in launches whose work-items stay below 2^32.
+template <class F>
+hipError_t over_tokens(const MoveArgs &a, int rows_per_block, F &&launch) {
+  const int64_t most = (0xffffffffLL / kThreads / a.segs) * rows_per_block;
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += most) {
+    MoveArgs b = a;
+    b.t0 = t0;
+    const int64_t n = a.tokens - t0 < most ? a.tokens - t0 : most;
+    launch(b, (unsigned)((n + rows_per_block - 1) / rows_per_block * a.segs));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+constexpr int kU = 2;  // chunks per thread
+
+template <int FMT, int TPR>
+hipError_t rows_t(MoveArgs a, bool combine, hipStream_t stream) {
+  const int64_t chunks = (a.hidden * fmt_bytes(FMT) + 15) / 16;
+  a.segs = (int32_t)((chunks + TPR * kU - 1) / (TPR * kU));
+  return over_tokens(a, kThreads / TPR, [&](const MoveArgs &b, unsigned grid) {
+    if constexpr (FMT != FMT_I8) {
+      if (combine) {
+        hipLaunchKernelGGL((combine_kernel<FMT, TPR, kU>), dim3(grid), dim3(kThreads), 0, stream, b);
+        return;
+      }
+    }
+    hipLaunchKernelGGL((dispatch_kernel<FMT, TPR, kU>), dim3(grid), dim3(kThreads), 0, stream, b);
+  });
+}
+
+template <int FMT>
+hipError_t rows_fmt(const MoveArgs &a, bool combine, hipStream_t stream) {
+  const int64_t chunks = (a.hidden * fmt_bytes(FMT) + 15) / 16;
+  if (chunks <= 8 * kU) return rows_t<FMT, 8>(a, combine, stream);
+  if (chunks <= 64 * kU) return rows_t<FMT, 64>(a, combine, stream);
+  return rows_t<FMT, 256>(a, combine, stream);
+}
+
+hipError_t rows_any(const MoveArgs &a, bool combine, hipStream_t stream) {
+  switch (a.fmt) {
+    case FMT_F32:
+      return rows_fmt<FMT_F32>(a, combine, stream);
+    case FMT_F16:
+      return rows_fmt<FMT_F16>(a, combine, stream);
+    case FMT_BF16:
+      return rows_fmt<FMT_BF16>(a, combine, stream);
+    default:
+      return rows_fmt<FMT_I8>(a, false, stream);
+  }
+}
+
+template <int FMT>
+hipError_t backward_fmt(MoveArgs a, hipStream_t stream) {
+  constexpr int JB = 4;
+  a.segs = 1;
+  return over_tokens(a, 1, [&](const MoveArgs &b, unsigned grid) {
+    hipLaunchKernelGGL((combine_backward_kernel<FMT, 256, JB>), dim3(grid), dim3(kThreads), 0, stream, b);
+  });
+}
+
+}  // namespace
+
+hipError_t launch_sort(const SortArgs &a, hipStream_t stream) {
+  const int64_t blocks = sort_blocks(a.tokens * a.topk);
+  const size_t lds = (size_t)(kSortWaves + 1) * a.experts * 4;
+  if (blocks > 1) {
+    if (a.id64)
+      hipLaunchKernelGGL(sort_count_kernel<true>, dim3((unsigned)blocks), dim3(kSortThreads), (size_t)a.experts * 4, stream, a);
+    else
+      hipLaunchKernelGGL(sort_count_kernel<false>, dim3((unsigned)blocks), dim3(kSortThreads), (size_t)a.experts * 4, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.id64)
+    hipLaunchKernelGGL(sort_place_kernel<true>, dim3((unsigned)blocks), dim3(kSortThreads), lds, stream, a);
+  else
+    hipLaunchKernelGGL(sort_place_kernel<false>, dim3((unsigned)blocks), dim3(kSortThreads), lds, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_dispatch(const MoveArgs &a, hipStream_t stream) { return rows_any(a, false, stream); }
+hipError_t launch_combine(const MoveArgs &a, hipStream_t stream) { return rows_any(a, true, stream); }
+
+hipError_t launch_combine_backward(const MoveArgs &a, hipStream_t stream) {
+  switch (a.fmt) {
+    case FMT_F32:
+      return backward_fmt<FMT_F32>(a, stream);
+    case FMT_F16:
+      return backward_fmt<FMT_F16>(a, stream);
+    default:
+      return backward_fmt<FMT_BF16>(a, stream);
+  }
+}
+
+}  // namespace tsm
