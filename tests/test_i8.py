@@ -93,6 +93,35 @@ def test_product(shape, out):
     assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,pad", [(256, 256, 128 * n, 0) for n in range(1, 15)]
+                         + [(1, 8, 256, 0), (257, 264, 384, 16), (700, 520, 128, 32), (255, 1032, 1664, 0)])
+def test_large_tiles(monkeypatch, M, N, K, pad, out):
+    """The 256 x 256 kernel, forced: every count of slabs in and after its loop, ragged M and N, padded rows, an
+    activation, a batch, and grouped counts."""
+    import torch
+
+    monkeypatch.setenv("TSM_GEMM_KERNEL", "i8_tile_256x256x128")
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    a, b = padded(M, K, K + pad, g), padded(N, K, K + pad, g)
+    sa, sb = scales(M, g), scales(N, g) / K ** 0.5
+    buf = torch.full((M + 1, N + 8), 77.0, dtype=dtypes()[out], device="cuda")
+    say(f"[gpu] i8 large tiles {M}x{N}x{K} {out}")
+    tsm.matmul_i8(a, sa, b.t(), sb, out=buf[:M, :N], activation="leaky_relu", slope=0.5)
+    check(buf[:M, :N], reference(a, sa, b, sb, "leaky_relu", 0.5), out, 4)
+    assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
+    rows = torch.tensor([M, 0, M // 2, M + 5, 1], dtype=torch.int32, device="cuda")
+    a3 = torch.randint(-128, 128, (5, M, K), generator=g, device="cuda", dtype=torch.int8)
+    b3 = torch.randint(-128, 128, (5, N, K), generator=g, device="cuda", dtype=torch.int8)
+    s3, t3 = scales((5, M), g), scales((5, N), g) / K ** 0.5
+    plain = tsm.matmul_i8(a3, s3, b3.transpose(1, 2), t3, out_dtype=dtypes()[out])
+    c = torch.full((5, M, N), 55.0, dtype=dtypes()[out], device="cuda")
+    tsm.matmul_i8(a3, s3, b3.transpose(1, 2), t3, rows=rows, out=c)
+    for z, m in enumerate([M, 0, M // 2, M, 1]):
+        check(plain[z], reference(a3[z], s3[z], b3[z], t3[z]), out)
+        assert torch.equal(c[z, :m], plain[z, :m]) and (c[z, m:] == 55.0).all()
+
+
 @pytest.mark.parametrize("shape", [(1, 512, 512), (16, 300, 1000), (300, 200, 100), (2304, 2304, 512)])
 @pytest.mark.parametrize("act", ["relu", "leaky_relu"])
 def test_activation(shape, act):

@@ -45,6 +45,16 @@ def test_gemm_i8_empty(kw):
     assert gemm(**kw) == 0
 
 
+@pytest.mark.parametrize("name,kw,status", [("i8_nothing", {}, 1), ("i8_tile_256x256x128", dict(K=127), 2),
+                                            ("i8_tile_256x256x128", dict(N=124), 2),
+                                            ("i8_tile_256x256x128", dict(A=A0 + 8), 2),
+                                            ("i8_tile_256x256x128", dict(lda=136), 2),
+                                            ("i8_tile_256x256x128", dict(dt=2, ldc=132), 2)])
+def test_forced_variants_that_cannot_run_are_refused(monkeypatch, name, kw, status):
+    monkeypatch.setenv("TSM_GEMM_KERNEL", name)
+    refused(gemm, kw, status, name)
+
+
 def test_gemm_i8_grouped_needs_counts():
     for rows, needle in ((0, "rows is NULL"), (P0 + 2, "rows not 4-byte")):
         with pytest.raises(tsm.TsmError) as ei:

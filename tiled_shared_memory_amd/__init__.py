@@ -9,14 +9,16 @@ HIP kernels.
 
 from __future__ import annotations
 
-from ._lib import (TSM_ACT_LEAKY_RELU, TSM_ACT_NONE, TSM_ACT_RELU, TSM_BF16, TSM_BF16_BF16, TSM_BF16_F16,  # noqa: F401
-                   TSM_BF16_F32, TSM_COL, TSM_ERROR_INVALID_VALUE, TSM_ERROR_LAUNCH, TSM_ERROR_NOT_SUPPORTED, TSM_F16,
-                   TSM_F16_BF16, TSM_F16_F16, TSM_F16_F32, TSM_F32, TSM_I8, TSM_I32, TSM_I64, TSM_ROW, TSM_ROWSUM_BF16,
-                   TSM_ROWSUM_F16, TSM_ROWSUM_F32, TSM_SUCCESS, TsmError, gemm, gemm_ex, gemm_grouped, gemm_i8,
-                   gemm_i8_grouped, gemm_i8_strided_batched, gemm_noalloc_scratch_bytes, gemm_strided_batched,
-                   gemm_strided_batched_act, gemm_strided_batched_ex, gemm_strided_batched_noalloc,
-                   gemm_strided_batched_ws, gemm_workspace_bytes, load, moe_combine, moe_combine_backward,
-                   moe_dispatch, moe_sort, moe_sort_workspace_bytes, quantize_i8, rowsum,
+import functools
+
+from ._lib import (TSM_ACT_LEAKY_RELU, TSM_ACT_NONE, TSM_ACT_RELU, TSM_BF16, TSM_BF16_BF16,  # noqa: F401
+                   TSM_BF16_F16, TSM_BF16_F32, TSM_COL, TSM_ERROR_INVALID_VALUE, TSM_ERROR_LAUNCH,
+                   TSM_ERROR_NOT_SUPPORTED, TSM_F16, TSM_F16_BF16, TSM_F16_F16, TSM_F16_F32, TSM_F32, TSM_I8, TSM_I32,
+                   TSM_I64, TSM_ROW, TSM_ROWSUM_BF16, TSM_ROWSUM_F16, TSM_ROWSUM_F32, TSM_SUCCESS, TsmError,
+                   current_device, gemm, gemm_ex, gemm_grouped, gemm_i8, gemm_i8_grouped, gemm_i8_strided_batched,
+                   gemm_noalloc_scratch_bytes, gemm_strided_batched, gemm_strided_batched_act, gemm_strided_batched_ex,
+                   gemm_strided_batched_noalloc, gemm_strided_batched_ws, gemm_workspace_bytes, load, moe_combine,
+                   moe_combine_backward, moe_dispatch, moe_sort, moe_sort_workspace_bytes, quantize_i8, rowsum,
                    tsm_gemm_grouped_kernel_name, tsm_gemm_i8_kernel_name, tsm_gemm_kernel_name,
                    tsm_gemm_ws_kernel_name, tsm_last_error_detail, tsm_rowsum_kernel_name, tsm_status_string)
 
@@ -133,7 +135,7 @@ def _wants(what, t, formats, shape=None):
     f = _format(t)
     if f not in formats:
         _bad(f"{what} has dtype {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         _bad(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} wanted")
     return f
 
@@ -152,23 +154,41 @@ def _packed(what, t):
         _bad(f"{what} must be contiguous")
 
 
-def _launch(stream, fn, first, *others):
-    """fn(stream handle) on the GPU that every tensor is on, on its current stream unless one is given."""
+def _new(like, shape, dtype, fill=None):
+    """A tensor of a dtype (torch's, or its name) on the GPU of ``like``."""
     import torch
 
-    dev = first.device
+    dtype = getattr(torch, dtype) if isinstance(dtype, str) else dtype
+    return (torch.empty if fill is None else torch.zeros)(shape, dtype=dtype, device=like.device)
+
+
+def _one_gpu(first, *others):
+    """Every tensor is on the GPU of the first."""
+    d = first.get_device()
     for t in others:
-        if t is not None and t.device != dev:
-            _bad(f"tensors on {dev} and {t.device}")
-    if dev.index == torch.cuda.current_device():
-        return fn(stream)
-    with torch.cuda.device(dev):
-        return fn(stream)
+        if t is not None and t.get_device() != d:
+            _bad(f"tensors on {first.device} and {t.device}")
+
+
+def _on_its_gpu(fn):
+    """Run fn with the GPU of its first tensor current: its launches, allocations and default stream are that GPU's."""
+
+    @functools.wraps(fn)
+    def run(first, *args, **kwargs):
+        if not first.is_cuda or first.get_device() == current_device():
+            return fn(first, *args, **kwargs)
+        import torch
+
+        with torch.cuda.device(first.device):
+            return fn(first, *args, **kwargs)
+
+    return run
 
 
 _FLOATS = (TSM_F32, TSM_F16, TSM_BF16)
 
 
+@_on_its_gpu
 def quantize(x, *, rows=None, out=None, scale=None, stream=None):
     """(codes, scales) of the rows of ``x`` (..., R, C) in float32, float16 or bfloat16: int8 codes with
     ``x ~ codes * scales[..., None]``, the scales float32 of shape (..., R).
@@ -176,15 +196,13 @@ def quantize(x, *, rows=None, out=None, scale=None, stream=None):
     2-D or 3-D.  With ``rows`` (int32, one count per matrix of a 3-D ``x``, on the GPU) only the first rows of each
     are read and written.
     """
-    import torch
-
     if x.dim() not in (2, 3):
         _bad("x must be 2-D or 3-D")
     f = _wants("x", x, _FLOATS)
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        out = _new(x, x.shape, "int8")
     if scale is None:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        scale = _new(x, x.shape[:-1], "float32")
     _wants("out", out, (TSM_I8,), x.shape)
     _wants("scale", scale, (TSM_F32,), x.shape[:-1])
     G = x.shape[0] if x.dim() == 3 else 1
@@ -195,11 +213,12 @@ def quantize(x, *, rows=None, out=None, scale=None, stream=None):
         _bad("scale: rows must be contiguous")
     ldx, ldq = _rows_ld("x", x), _rows_ld("out", out)
     sx, sq, ss = (x.stride(0), out.stride(0), scale.stride(0)) if x.dim() == 3 else (0, 0, 0)
-    _launch(stream, lambda s: quantize_i8(x.shape[-2], x.shape[-1], x, ldx, sx, f, out, ldq, sq, scale, ss, rows, G, s),
-            x, out, scale, rows)
+    _one_gpu(x, out, scale, rows)
+    quantize_i8(x.shape[-2], x.shape[-1], x, ldx, sx, f, out, ldq, sq, scale, ss, rows, G, stream)
     return out, scale
 
 
+@_on_its_gpu
 def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, activation=None, slope=0.01, stream=None):
     """C = act(scale_a[..., None] * scale_b * (A.B)) for int8 CUDA tensors ``a`` (..., M, K) and ``b`` (..., K, N).
 
@@ -208,8 +227,6 @@ def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, ac
     dim of size 1 broadcasts); with ``rows`` (int32 counts on the GPU, one per problem) the grouped product over a
     mixture of experts' slabs.  The result is float32 (default), float16 or bfloat16; ``activation`` as for ``matmul``.
     """
-    import torch
-
     if a.dim() not in (2, 3) or b.dim() not in (2, 3):
         _bad("a and b must be 2-D or 3-D")
     _wants("a", a, (TSM_I8,))
@@ -225,7 +242,7 @@ def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, ac
     batch = ba if bb == 1 else bb
     shape = (batch, M, N) if batched else (M, N)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or torch.float32, device=a.device)
+        out = _new(a, shape, out_dtype or "float32")
     elif out_dtype is not None and out.dtype != out_dtype:
         _bad(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
     f = _wants("out", out, _FLOATS, shape)
@@ -249,26 +266,25 @@ def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, ac
     sc = out.stride(0) if batched else 0
     act = _ACTIVATIONS[activation]
     if rows is None:
-        _launch(stream, lambda s: gemm_i8_strided_batched(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb,
-                                                          out, ldc, sc, batch, f, act, slope, s),
-                a, b, out, scale_a, scale_b)
+        _one_gpu(a, b, out, scale_a, scale_b)
+        gemm_i8_strided_batched(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb, out, ldc, sc, batch, f,
+                                act, slope, stream)
     else:
         _wants("rows", rows, (TSM_I32,), (batch,))
         _packed("rows", rows)
-        _launch(stream, lambda s: gemm_i8_grouped(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb, out, ldc,
-                                                  sc, rows, batch, f, act, slope, s),
-                a, b, out, scale_a, scale_b, rows)
+        _one_gpu(a, b, out, scale_a, scale_b, rows)
+        gemm_i8_grouped(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb, out, ldc, sc, rows, batch, f,
+                        act, slope, stream)
     return out
 
 
 def sort_workspace_for(ids, experts):
     """A CUDA tensor for ``sort_tokens(..., workspace=...)``, or None when the sizes need none."""
-    import torch
-
     n = moe_sort_workspace_bytes(ids.shape[0], ids.shape[1], experts)
-    return torch.empty(n, dtype=torch.uint8, device=ids.device) if n else None
+    return _new(ids, (n,), "uint8") if n else None
 
 
+@_on_its_gpu
 def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspace=None, stream=None):
     """(positions, counts) of the experts' ids (tokens, topk), int32 or int64: the row of each choice in the slabs
     (experts * capacity rows, expert e's from e * capacity), in token order, -1 for an id outside [0, experts) or past
@@ -276,15 +292,13 @@ def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspac
 
     A workspace (see ``sort_workspace_for``) is allocated when the sizes need one and none is given.
     """
-    import torch
-
     if ids.dim() != 2:
         _bad("ids must be 2-D")
     f = _wants("ids", ids, (TSM_I32, TSM_I64))
     if positions is None:
-        positions = torch.empty(ids.shape, dtype=torch.int32, device=ids.device)
+        positions = _new(ids, ids.shape, "int32")
     if counts is None:
-        counts = torch.empty((experts,), dtype=torch.int32, device=ids.device)
+        counts = _new(ids, (experts,), "int32")
     _wants("positions", positions, (TSM_I32,), ids.shape)
     _wants("counts", counts, (TSM_I32,), (experts,))
     _packed("positions", positions)
@@ -296,9 +310,9 @@ def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspac
             _bad("workspace is not on a GPU")
         _packed("workspace", workspace)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _launch(stream, lambda s: moe_sort(ids.shape[0], ids.shape[1], ids, _rows_ld("ids", ids), f, experts, capacity,
-                                       positions, counts, workspace, nbytes, s),
-            ids, positions, counts, workspace)
+    _one_gpu(ids, positions, counts, workspace)
+    moe_sort(ids.shape[0], ids.shape[1], ids, _rows_ld("ids", ids), f, experts, capacity, positions, counts,
+             workspace, nbytes, stream)
     return positions, counts
 
 
@@ -312,6 +326,7 @@ def _slab_args(what, slabs, positions, tokens, hidden):
     _packed("positions", positions)
 
 
+@_on_its_gpu
 def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale=None, stream=None):
     """Token rows ``x`` (tokens, hidden) at their ``positions`` (tokens, topk) in the slabs (slots, hidden), float32,
     float16, bfloat16 or int8.
@@ -319,15 +334,13 @@ def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale
     ``out`` keeps its other rows; without it the slabs are allocated with ``slots`` rows (the others unset).  With
     ``scale`` (float32, one per token) also the slab rows' scales: returns (slabs, scales).
     """
-    import torch
-
     if x.dim() != 2:
         _bad("x must be 2-D")
     f = _wants("x", x, _FLOATS + (TSM_I8,))
     if out is None:
         if slots is None:
             _bad("slots or out is needed")
-        out = torch.empty((slots, x.shape[1]), dtype=x.dtype, device=x.device)
+        out = _new(x, (slots, x.shape[1]), x.dtype)
     elif slots is not None and out.shape[0] != slots:
         _bad(f"out has {out.shape[0]} rows, slots is {slots}")
     _slab_args("out", out, positions, x.shape[0], x.shape[1])
@@ -336,34 +349,33 @@ def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale
         _wants("scale", scale, (TSM_F32,), (x.shape[0],))
         _packed("scale", scale)
         if out_scale is None:
-            out_scale = torch.empty((out.shape[0],), dtype=torch.float32, device=x.device)
+            out_scale = _new(x, (out.shape[0],), "float32")
         _wants("out_scale", out_scale, (TSM_F32,), (out.shape[0],))
         _packed("out_scale", out_scale)
     elif out_scale is not None:
         _bad("out_scale without scale")
-    _launch(stream, lambda s: moe_dispatch(x.shape[0], positions.shape[1], x.shape[1], x, _rows_ld("x", x), f, scale,
-                                           positions, out.shape[0], out, _rows_ld("out", out), out_scale, s),
-            x, out, positions, scale, out_scale)
+    _one_gpu(x, out, positions, scale, out_scale)
+    moe_dispatch(x.shape[0], positions.shape[1], x.shape[1], x, _rows_ld("x", x), f, scale, positions,
+                 out.shape[0], out, _rows_ld("out", out), out_scale, stream)
     return out if scale is None else (out, out_scale)
 
 
+@_on_its_gpu
 def combine_tokens(slabs, positions, weights=None, *, out=None, stream=None):
     """Y[t] = sum_j weights[t, j] * slabs[positions[t, j]] over the choices with a position, float32 sums in the order
     of j; ``weights`` float32 (tokens, topk), None for ones.  Y has the slabs' dtype (float32, float16 or bfloat16)."""
-    import torch
-
     _slab_args("slabs", slabs, positions, None, None)
     f = _wants("slabs", slabs, _FLOATS)
     tokens, hidden = positions.shape[0], slabs.shape[1]
     if out is None:
-        out = torch.empty((tokens, hidden), dtype=slabs.dtype, device=slabs.device)
+        out = _new(slabs, (tokens, hidden), slabs.dtype)
     _wants("out", out, (f,), (tokens, hidden))
     if weights is not None:
         _wants("weights", weights, (TSM_F32,), positions.shape)
         _packed("weights", weights)
-    _launch(stream, lambda s: moe_combine(tokens, positions.shape[1], hidden, slabs, _rows_ld("slabs", slabs),
-                                          slabs.shape[0], f, positions, weights, out, _rows_ld("out", out), s),
-            slabs, out, positions, weights)
+    _one_gpu(slabs, out, positions, weights)
+    moe_combine(tokens, positions.shape[1], hidden, slabs, _rows_ld("slabs", slabs), slabs.shape[0], f,
+                positions, weights, out, _rows_ld("out", out), stream)
     return out
 
 
@@ -372,29 +384,28 @@ def dispatch_tokens_backward(dslabs, positions, *, out=None, stream=None):
     return combine_tokens(dslabs, positions, None, out=out, stream=stream)
 
 
+@_on_its_gpu
 def combine_tokens_backward(dy, slabs, positions, weights=None, *, out=None, dweights=None, stream=None):
     """(dslabs, dweights) of ``combine_tokens`` from ``dy`` (tokens, hidden): dslabs[positions[t, j]] =
     weights[t, j] * dy[t] (``out``; its other rows are kept, or zeros where it is allocated here) and
     dweights[t, j] = <dy[t], slabs[positions[t, j]]> (float32, 0 without a position)."""
-    import torch
-
     if dy.dim() != 2:
         _bad("dy must be 2-D")
     f = _wants("dy", dy, _FLOATS)
     _slab_args("slabs", slabs, positions, dy.shape[0], dy.shape[1])
     _wants("slabs", slabs, (f,))
     if out is None:
-        out = torch.zeros(slabs.shape, dtype=slabs.dtype, device=slabs.device)
+        out = _new(slabs, slabs.shape, slabs.dtype, 0)
     _wants("out", out, (f,), slabs.shape)
     if dweights is None:
-        dweights = torch.empty(positions.shape, dtype=torch.float32, device=dy.device)
+        dweights = _new(dy, positions.shape, "float32")
     _wants("dweights", dweights, (TSM_F32,), positions.shape)
     _packed("dweights", dweights)
     if weights is not None:
         _wants("weights", weights, (TSM_F32,), positions.shape)
         _packed("weights", weights)
-    _launch(stream, lambda s: moe_combine_backward(dy.shape[0], positions.shape[1], dy.shape[1], dy,
-                                                   _rows_ld("dy", dy), slabs, _rows_ld("slabs", slabs), slabs.shape[0],
-                                                   f, positions, weights, out, _rows_ld("out", out), dweights, s),
-            dy, slabs, out, positions, weights, dweights)
+    _one_gpu(dy, slabs, out, positions, weights, dweights)
+    moe_combine_backward(dy.shape[0], positions.shape[1], dy.shape[1], dy, _rows_ld("dy", dy), slabs,
+                         _rows_ld("slabs", slabs), slabs.shape[0], f, positions, weights, out, _rows_ld("out", out),
+                         dweights, stream)
     return out, dweights

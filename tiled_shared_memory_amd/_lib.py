@@ -134,11 +134,35 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _stream(stream):
-    if stream is None:
+_LOOKUPS = None  # torch's (current device index, current stream handle of a device)
+
+
+def _lookups():
+    global _LOOKUPS
+    if _LOOKUPS is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        torch.cuda.current_stream()  # initialises the device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _LOOKUPS = (torch.cuda.current_device, raw or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+    return _LOOKUPS
+
+
+def current_device():
+    """Index of torch's current GPU."""
+    return _lookups()[0]()
+
+
+def _current_stream():
+    """Handle of the current stream of the current GPU: torch's own lookup, without the Stream object that
+    ``torch.cuda.current_stream()`` builds around it (2.6 us, as much as a launch)."""
+    device, stream = _lookups()
+    return stream(device())
+
+
+def _stream(stream):
+    if stream is None:
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -7,28 +7,14 @@
 // with one load at any byte address; rows past M or N read the last row (their
 // products are never stored); the codes past K are shifted out of the last
 // vector (make_tail), so they are zeros in both operands.
-#include "elems.hpp"
-#include "gemm_internal.hpp"
-#include "i8_internal.hpp"
-#include "mfma.hpp"
+#include "i8_common.hpp"
 
 namespace tsm {
 namespace {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
-}
-
 constexpr int kThreads = 256;
 constexpr int BK = 128;           // codes per slab
 constexpr int PITCH = BK + 16;    // LDS row pitch: 16 rows of one fragment read fall on distinct banks
-
-__device__ __forceinline__ u32x4 load16(const int8_t *p) {
-  const Raw16 r = *(const Raw16 *)p;
-  return u32x4{r.d[0], r.d[1], r.d[2], r.d[3]};
-}
 
 // Codes k .. k+15 of a row of K, zeros past K; nothing outside the row is read.
 __device__ __forceinline__ u32x4 load_tail(const int8_t *row, int64_t k, int64_t K) {
@@ -56,42 +42,17 @@ __device__ __forceinline__ u32x4 load_tail(const int8_t *row, int64_t k, int64_t
   return v;
 }
 
-// Four results of one row of C, columns n .. n+3.
-template <int FMT>
-__device__ __forceinline__ void store_i8(const I8Args &p, const Epilogue &ep, char *row, int64_t n, float sa,
-                                         const float (&sb)[4], i32x4 acc) {
-  float v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = ep.apply((float)acc[i] * sa * sb[i]);
-  if (p.vec_store && n + 4 <= p.N) {
-    if constexpr (FMT == FMT_F32) {
-      *reinterpret_cast<f32x4 *>(row + n * 4) = f32x4{v[0], v[1], v[2], v[3]};
-    } else {
-      *reinterpret_cast<u32x2 *>(row + n * 2) = u32x2{f32_elem<FMT>(v[0]) | (f32_elem<FMT>(v[1]) << 16),
-                                                      f32_elem<FMT>(v[2]) | (f32_elem<FMT>(v[3]) << 16)};
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < p.N) put_bits<FMT>(row, n + i, f32_elem<FMT>(v[i]));
-  }
-}
-
 template <int T, int FMT>
 __global__ __launch_bounds__(kThreads) void gemm_i8_block_kernel(I8Args p) {
   constexpr int W = T / 2, NB = W / 16;       // wave tile, 16 x 16 blocks per dimension
   constexpr int V = T * (BK / 16) / kThreads;  // vectors per thread and operand
   __shared__ __attribute__((aligned(16))) char sA[2][T * PITCH], sB[2][T * PITCH];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-  const int T2 = p.tiles_m * p.tiles_n;
-  int pid = xcd_remap(blockIdx.x, gridDim.x);
-  const int64_t z = p.z0 + pid / T2;
-  pid %= T2;
   int tm, tn;
-  tile_order(pid, p.tiles_m, p.tiles_n, 8, tm, tn);
+  int64_t z;
+  if (!i8_tile_of<T>(p, 8, z, tm, tn)) return;  // uniform
   const int64_t m0 = (int64_t)tm * T, n0 = (int64_t)tn * T;
   const int64_t M = i8_rows(p, z);
-  if (m0 >= M) return;  // uniform
 
   const int row0 = tid >> 3, kc = (tid & 7) * 16;  // 8 vectors per row, 32 rows per pass
   const int8_t *ap[V], *bp[V];
@@ -161,12 +122,7 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_block_kernel(I8Args p) {
   const float *sa = p.sa ? p.sa + z * p.stride_sa : nullptr, *sb = p.sb ? p.sb + z * p.stride_sb : nullptr;
   float cb[NB][4];
 #pragma unroll
-  for (int j = 0; j < NB; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t n = n0 + wn * W + j * 16 + 4 * (lane >> 4) + i;
-      cb[j][i] = sb && n < p.N ? sb[n] : 1.f;
-    }
+  for (int j = 0; j < NB; ++j) channel_scales(p, sb, n0 + wn * W + j * 16 + 4 * (lane >> 4), cb[j]);
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
     const int64_t m = m0 + wm * W + i * 16 + (lane & 15);
@@ -181,32 +137,15 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_block_kernel(I8Args p) {
   }
 }
 
-// One 1-D grid over the tiles of as many problems as keep its work-items below 2^32 (the host checks that one does).
-template <class F>
-hipError_t over_tiles(I8Args a, int tile_m, int tile_n, F &&launch) {
-  a.tiles_m = (int32_t)((a.M + tile_m - 1) / tile_m);
-  a.tiles_n = (int32_t)((a.N + tile_n - 1) / tile_n);
-  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-  const int64_t most = 0xffffffffLL / kThreads / tiles;
-  for (int64_t z0 = 0; z0 < a.batch; z0 += most) {
-    const int64_t nz = a.batch - z0 < most ? a.batch - z0 : most;
-    a.z0 = z0;
-    launch(a, (unsigned)(tiles * nz));
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
-}
-
 template <int T>
 hipError_t block_t(const I8Args &p, hipStream_t stream) {
-  return over_tiles(p, T, T, [&](const I8Args &a, unsigned grid) {
+  return over_tiles(p, T, T, kThreads, [&](const I8Args &a, dim3 grid) {
     if (a.fmt == FMT_F32)
-      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_F32>), dim3(grid), dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_F32>), grid, dim3(kThreads), 0, stream, a);
     else if (a.fmt == FMT_F16)
-      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_F16>), dim3(grid), dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_F16>), grid, dim3(kThreads), 0, stream, a);
     else
-      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_BF16>), dim3(grid), dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_BF16>), grid, dim3(kThreads), 0, stream, a);
   });
 }
 

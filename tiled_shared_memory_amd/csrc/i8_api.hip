@@ -1,6 +1,9 @@
 // Host side of the int8 entry points (include/tsm_gemm.h): argument checks,
 // kernel selection and launch on the caller's stream.  As in gemm_api.hip,
 // every check runs before any HIP call.
+#include <stdlib.h>
+#include <string.h>
+
 #include "elems.hpp"
 #include "gemm_internal.hpp"
 #include "host_checks.hpp"
@@ -10,7 +13,7 @@
 namespace tsm {
 namespace {
 
-enum class I8Kernel { None, Block128, Block64 };
+enum class I8Kernel { None, Block128, Block64, Tile };
 
 const char *i8_name(I8Kernel k) {
   switch (k) {
@@ -18,6 +21,8 @@ const char *i8_name(I8Kernel k) {
       return "i8_block_128x128x128";
     case I8Kernel::Block64:
       return "i8_block_64x64x128";
+    case I8Kernel::Tile:
+      return "i8_tile_256x256x128";
     default:
       return nullptr;
   }
@@ -110,6 +115,20 @@ int i8_plan(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64
   *kernel = tiles128 * batch < 512 ? I8Kernel::Block64 : I8Kernel::Block128;
   if ((*kernel == I8Kernel::Block64 ? tiles64 : tiles128) * 256 > 0xffffffffLL)
     return fail(TSM_ERROR_NOT_SUPPORTED, "tile grid too large");
+  const int64_t tiles256 = ((M + 255) / 256) * ((N + 255) / 256) * batch;
+  if (tiles256 >= 72 && i8_tile_supports(*p)) *kernel = I8Kernel::Tile;
+  // TSM_GEMM_KERNEL=<name> forces a variant (tests and tuning); names of other
+  // families are left alone, a variant that cannot run the problem is an error.
+  const char *force = getenv("TSM_GEMM_KERNEL");
+  if (force && strncmp(force, "i8_", 3) == 0) {
+    I8Kernel want = I8Kernel::None;
+    for (I8Kernel k : {I8Kernel::Block128, I8Kernel::Block64, I8Kernel::Tile})
+      if (strcmp(force, i8_name(k)) == 0) want = k;
+    if (want == I8Kernel::None) return fail(TSM_ERROR_INVALID_VALUE, "TSM_GEMM_KERNEL=%s names no kernel", force);
+    if (want == I8Kernel::Tile && !i8_tile_supports(*p))
+      return fail(TSM_ERROR_NOT_SUPPORTED, "TSM_GEMM_KERNEL=%s cannot run this problem", force);
+    *kernel = want;
+  }
   return TSM_SUCCESS;
 }
 
@@ -124,6 +143,9 @@ int i8_run(const I8Args &p, I8Kernel k, void *stream) {
       break;
     case I8Kernel::Block64:
       e = launch_i8_block(p, 64, s);
+      break;
+    case I8Kernel::Tile:
+      e = launch_i8_tile(p, s);
       break;
   }
   if (e != hipSuccess) return fail(TSM_ERROR_LAUNCH, "launch failed: %s", hipGetErrorString(e));

@@ -1,0 +1,106 @@
+// Pieces shared by the int8 product kernels.
+#pragma once
+
+#include "elems.hpp"
+#include "gemm_internal.hpp"
+#include "i8_internal.hpp"
+#include "mfma.hpp"
+
+namespace tsm {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// v_mfma_i32_16x16x64_i8: D(16x16) += A(16x64) * B(64x16), 16 codes per lane and
+// operand: row (column) lane % 16, k = 16 * (lane / 16) + 0..15 in both, so any
+// order of k that both operands share gives the same sum.  D as for the
+// 16x16x32 forms (mfma.hpp).
+__device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ u32x4 load16(const int8_t *p) {
+  const Raw16 r = *(const Raw16 *)p;
+  return u32x4{r.d[0], r.d[1], r.d[2], r.d[3]};
+}
+
+// Four results of one row of C, columns n .. n+3 (n < N): each sum to float32
+// once, times the token's scale, times the channel's, then the activation and
+// the output's rounding.
+template <int FMT>
+__device__ __forceinline__ void store_i8(const I8Args &p, const Epilogue &ep, char *row, int64_t n, float sa,
+                                         const float (&sb)[4], i32x4 acc) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = ep.apply((float)acc[i] * sa * sb[i]);
+  if (p.vec_store && n + 4 <= p.N) {
+    if constexpr (FMT == FMT_F32) {
+      *reinterpret_cast<f32x4 *>(row + n * 4) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+      *reinterpret_cast<u32x2 *>(row + n * 2) = u32x2{f32_elem<FMT>(v[0]) | (f32_elem<FMT>(v[1]) << 16),
+                                                      f32_elem<FMT>(v[2]) | (f32_elem<FMT>(v[3]) << 16)};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < p.N) put_bits<FMT>(row, n + i, f32_elem<FMT>(v[i]));
+  }
+}
+
+// Scales of channels n .. n+3 (ones past N or without scales).
+__device__ __forceinline__ void channel_scales(const I8Args &p, const float *sb, int64_t n, float (&c)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = sb && n + i < p.N ? sb[n + i] : 1.f;
+}
+
+// Where a workgroup of a flat grid works: problem z, tile (tm, tn) in the
+// grouped tile order, the grid regrouped per XCD.  Grouped calls of up to
+// kCompactGroups experts number only the tiles that hold rows, so the real work
+// spreads evenly over the XCDs; false: nothing to do.
+constexpr int kCompactGroups = 256;
+
+template <int BM>
+__device__ __forceinline__ bool i8_tile_of(const I8Args &p, int group_m, int64_t &z, int &tm, int &tn) {
+  if (p.compact) {
+    const int G = p.compact;
+    int V = 0;
+    for (int g = 0; g < G; ++g) V += (int)((i8_rows(p, g) + BM - 1) / BM);
+    V *= p.tiles_n;
+    if ((int)blockIdx.x >= V) return false;
+    int pid = xcd_remap(blockIdx.x, V);
+    int g = 0;
+    for (; g < G - 1; ++g) {
+      const int t = (int)((i8_rows(p, g) + BM - 1) / BM) * p.tiles_n;
+      if (pid < t) break;
+      pid -= t;
+    }
+    tile_order(pid, (int)((i8_rows(p, g) + BM - 1) / BM), p.tiles_n, group_m, tm, tn);
+    z = g;
+    return true;
+  }
+  const int T = p.tiles_m * p.tiles_n;
+  const int pid = xcd_remap(blockIdx.x, gridDim.x);
+  z = p.z0 + pid / T;
+  tile_order(pid % T, p.tiles_m, p.tiles_n, group_m, tm, tn);
+  return (int64_t)tm * BM < i8_rows(p, z);
+}
+
+// One 1-D grid of workgroups of `threads` over the tiles of as many problems as
+// keep its work-items below 2^32 (the host checks that one problem does).
+template <class F>
+hipError_t over_tiles(I8Args a, int tile_m, int tile_n, int threads, F &&launch) {
+  a.tiles_m = (int32_t)((a.M + tile_m - 1) / tile_m);
+  a.tiles_n = (int32_t)((a.N + tile_n - 1) / tile_n);
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  const int64_t most = 0xffffffffLL / threads / tiles;
+  a.compact = a.rows && a.batch <= kCompactGroups && a.batch <= most ? (int32_t)a.batch : 0;
+  for (int64_t z0 = 0; z0 < a.batch; z0 += most) {
+    const int64_t nz = a.batch - z0 < most ? a.batch - z0 : most;
+    a.z0 = z0;
+    launch(a, dim3((unsigned)(tiles * nz)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace tsm

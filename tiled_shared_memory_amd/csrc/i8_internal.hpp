@@ -22,7 +22,8 @@ struct I8Args {
   int32_t vec_store;    // C's rows take stores of 4 elements
   // set by the launch
   int32_t tiles_m, tiles_n;
-  int64_t z0;  // first problem of this launch
+  int64_t z0;       // first problem of this launch
+  int32_t compact;  // grouped: number of groups, tiles numbered over the valid ones only
 };
 
 // Rows of problem z (a grouped call's count, clamped to [0, M]).
@@ -35,6 +36,9 @@ __device__ __forceinline__ int64_t i8_rows(const I8Args &p, int64_t z) {
 // |sum| <= K * 128 * 128 stays below 2^31
 constexpr int64_t kI8MaxK = 131071;
 
+// 256 x 256 tiles: see i8_tile_supports for what they need.
+bool i8_tile_supports(const I8Args &p);
+hipError_t launch_i8_tile(const I8Args &p, hipStream_t stream);
 hipError_t launch_i8_block(const I8Args &p, int tile, hipStream_t stream);
 
 struct QuantArgs {
