@@ -122,6 +122,35 @@ def test_large_tiles(monkeypatch, M, N, K, pad, out):
         assert torch.equal(c[z, :m], plain[z, :m]) and (c[z, m:] == 55.0).all()
 
 
+@pytest.mark.parametrize("kernel", ["i8_skinny", "i8_stream"])
+@pytest.mark.parametrize("M", [1, 3, 4, 5, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("N,K", [(40, 16), (16, 256), (4200, 272), (20000, 1040), (100, 5120), (8208, 4112)])
+def test_few_rows(monkeypatch, kernel, M, N, K):
+    """The streaming and the register kernel on the same problems: K inside one step, in several, and past the ring;
+    more columns than one round of workgroups holds; padded rows; a grouped call."""
+    import torch
+
+    monkeypatch.setenv("TSM_GEMM_KERNEL", kernel)
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    a, b = padded(M, K, K + 16, g), padded(N, K, K + 48, g)
+    sa, sb = scales(M, g), scales(N, g) / K ** 0.5
+    say(f"[gpu] {kernel} {M}x{N}x{K}")
+    buf = torch.full((M + 1, N + 3), 77.0, dtype=torch.bfloat16, device="cuda")
+    tsm.matmul_i8(a, sa, b.t(), sb, out=buf[:M, :N], activation="relu")
+    check(buf[:M, :N], reference(a, sa, b, sb, "relu"), "bf16")
+    assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
+    if N > 5000:
+        return
+    rows = torch.tensor([0, M, 1, M // 2, -1, M + 1], dtype=torch.int32, device="cuda")
+    a3 = torch.randint(-128, 128, (6, M, K), generator=g, device="cuda", dtype=torch.int8)
+    b3 = torch.randint(-128, 128, (6, N, K), generator=g, device="cuda", dtype=torch.int8)
+    c = torch.full((6, M, N), 55.0, device="cuda")
+    tsm.matmul_i8(a3, None, b3.transpose(1, 2), None, rows=rows, out=c)
+    for z, m in enumerate([0, M, 1, M // 2, 0, M]):
+        check(c[z, :m], reference(a3[z, :m], None, b3[z], None), "f32")
+        assert (c[z, m:] == 55.0).all()
+
+
 @pytest.mark.parametrize("shape", [(1, 512, 512), (16, 300, 1000), (300, 200, 100), (2304, 2304, 512)])
 @pytest.mark.parametrize("act", ["relu", "leaky_relu"])
 def test_activation(shape, act):

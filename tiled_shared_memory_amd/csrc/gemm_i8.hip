@@ -16,32 +16,6 @@ constexpr int kThreads = 256;
 constexpr int BK = 128;           // codes per slab
 constexpr int PITCH = BK + 16;    // LDS row pitch: 16 rows of one fragment read fall on distinct banks
 
-// Codes k .. k+15 of a row of K, zeros past K; nothing outside the row is read.
-__device__ __forceinline__ u32x4 load_tail(const int8_t *row, int64_t k, int64_t K) {
-  if (k + 16 <= K) return load16(row + k);
-  u32x4 v = {};
-  if (k >= K) return v;
-  if (K >= 16) {
-    // the row's last 16 codes, those before k shifted out
-    const Raw16 r = *(const Raw16 *)(row + K - 16);
-    const int drop = (int)(16 - (K - k));  // 1..15
-    const uint64_t lo = (uint64_t)r.d[0] | ((uint64_t)r.d[1] << 32), hi = (uint64_t)r.d[2] | ((uint64_t)r.d[3] << 32);
-    uint64_t a, b;
-    if (drop >= 8) {
-      a = hi >> (8 * (drop - 8));
-      b = 0;
-    } else {
-      a = (lo >> (8 * drop)) | (hi << (64 - 8 * drop));
-      b = hi >> (8 * drop);
-    }
-    return u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
-  }
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (k + i < K) v[i >> 2] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i & 3));
-  return v;
-}
-
 template <int T, int FMT>
 __global__ __launch_bounds__(kThreads) void gemm_i8_block_kernel(I8Args p) {
   constexpr int W = T / 2, NB = W / 16;       // wave tile, 16 x 16 blocks per dimension

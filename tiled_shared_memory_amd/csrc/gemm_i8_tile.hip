@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
   int tm, tn;
   int64_t z;
   // groups of 4 tile rows from 32 up, else 8 (as the 16-bit kernel)
-  if (!i8_tile_of<BM>(p, p.tiles_m >= 32 && !p.compact ? 4 : 8, z, tm, tn)) return;  // uniform
+  if (!i8_tile_of<BM>(p, p.tiles_m >= 32 && !p.rows ? 4 : 8, z, tm, tn)) return;  // uniform
   Ctx c;
   c.lane = threadIdx.x & 63;
   c.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

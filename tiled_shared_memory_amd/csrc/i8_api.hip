@@ -13,7 +13,7 @@
 namespace tsm {
 namespace {
 
-enum class I8Kernel { None, Block128, Block64, Tile };
+enum class I8Kernel { None, Block128, Block64, Tile, Stream, Skinny };
 
 const char *i8_name(I8Kernel k) {
   switch (k) {
@@ -23,6 +23,10 @@ const char *i8_name(I8Kernel k) {
       return "i8_block_64x64x128";
     case I8Kernel::Tile:
       return "i8_tile_256x256x128";
+    case I8Kernel::Stream:
+      return "i8_stream";
+    case I8Kernel::Skinny:
+      return "i8_skinny";
     default:
       return nullptr;
   }
@@ -117,15 +121,18 @@ int i8_plan(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64
     return fail(TSM_ERROR_NOT_SUPPORTED, "tile grid too large");
   const int64_t tiles256 = ((M + 255) / 256) * ((N + 255) / 256) * batch;
   if (tiles256 >= 72 && i8_tile_supports(*p)) *kernel = I8Kernel::Tile;
+  const I8Skinny sk = i8_skinny_plan(*p);
+  if (sk.rows) *kernel = sk.stream ? I8Kernel::Stream : I8Kernel::Skinny;
   // TSM_GEMM_KERNEL=<name> forces a variant (tests and tuning); names of other
   // families are left alone, a variant that cannot run the problem is an error.
   const char *force = getenv("TSM_GEMM_KERNEL");
   if (force && strncmp(force, "i8_", 3) == 0) {
     I8Kernel want = I8Kernel::None;
-    for (I8Kernel k : {I8Kernel::Block128, I8Kernel::Block64, I8Kernel::Tile})
+    for (I8Kernel k : {I8Kernel::Block128, I8Kernel::Block64, I8Kernel::Tile, I8Kernel::Stream, I8Kernel::Skinny})
       if (strcmp(force, i8_name(k)) == 0) want = k;
     if (want == I8Kernel::None) return fail(TSM_ERROR_INVALID_VALUE, "TSM_GEMM_KERNEL=%s names no kernel", force);
-    if (want == I8Kernel::Tile && !i8_tile_supports(*p))
+    if ((want == I8Kernel::Tile && !i8_tile_supports(*p)) || (want == I8Kernel::Stream && !(sk.rows && sk.can_stream)) ||
+        (want == I8Kernel::Skinny && !sk.rows))
       return fail(TSM_ERROR_NOT_SUPPORTED, "TSM_GEMM_KERNEL=%s cannot run this problem", force);
     *kernel = want;
   }
@@ -147,6 +154,13 @@ int i8_run(const I8Args &p, I8Kernel k, void *stream) {
     case I8Kernel::Tile:
       e = launch_i8_tile(p, s);
       break;
+    case I8Kernel::Stream:
+    case I8Kernel::Skinny: {
+      I8Skinny sk = i8_skinny_plan(p);
+      sk.stream = k == I8Kernel::Stream;
+      e = launch_i8_skinny(p, sk, s);
+      break;
+    }
   }
   if (e != hipSuccess) return fail(TSM_ERROR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
   return TSM_SUCCESS;

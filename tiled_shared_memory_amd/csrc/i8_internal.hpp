@@ -23,7 +23,7 @@ struct I8Args {
   // set by the launch
   int32_t tiles_m, tiles_n;
   int64_t z0;       // first problem of this launch
-  int32_t compact;  // grouped: number of groups, tiles numbered over the valid ones only
+  int32_t nz;       // problems of this launch
 };
 
 // Rows of problem z (a grouped call's count, clamped to [0, M]).
@@ -39,6 +39,14 @@ constexpr int64_t kI8MaxK = 131071;
 // 256 x 256 tiles: see i8_tile_supports for what they need.
 bool i8_tile_supports(const I8Args &p);
 hipError_t launch_i8_tile(const I8Args &p, hipStream_t stream);
+// Few rows (up to 64): `rows` of them (0: not for this problem) by 16 nb columns per workgroup of `waves` waves.
+struct I8Skinny {
+  int rows = 0, nb = 0, waves = 0;
+  bool can_stream = false;  // the operands allow the streaming kernel
+  bool stream = false;      // and the rule takes it
+};
+I8Skinny i8_skinny_plan(const I8Args &p);
+hipError_t launch_i8_skinny(const I8Args &p, const I8Skinny &s, hipStream_t stream);
 hipError_t launch_i8_block(const I8Args &p, int tile, hipStream_t stream);
 
 struct QuantArgs {
