@@ -1,12 +1,21 @@
 // Rows to int8 codes with one float32 scale each, for gemm_i8:
 //   m = max_c |X[r][c]|,  scale[r] = m / 127,  Q[r][c] = nearest(127 X[r][c] / m), ties to even.
 //
-// The codes are those of the exact quotient 127 x / m, not of a rounded one:
-// t = x * (127 / m) is off by at most 127 * 2^-23 < 2^-16, so where t is
-// further than that from a half its nearest whole number is the right one;
-// nearer, the sign of 254 |x| - (2n + 1) m decides, whose two products are
-// exact in float64 (24 + 8 bits).  (x = m / 2 is a true tie, 63.5, and common
-// in bf16.)
+// The codes are those of the exact quotient t = 127 x / m.  With inv = 127 / m
+// rounded once, x * inv is off by at most t * 2^-24 < 2^-17, so its nearest whole
+// number is the right one unless it lies that close to a half:
+//  * 16-bit x: t - (n + 1/2) is (254 x - (2n + 1) m) / (2 m).  With x = X 2^a and
+//    m = M 2^b, a <= b, X and M whole and below 2^11, that is 0 or at least
+//    2^(a-b) / (2 M), i.e. t / (254 X) > t * 2^-19: within t * 2^-21 of a half it
+//    is a tie and takes the even neighbour (x = m / 2 is 63.5, common in bf16);
+//  * float32 x: the quotient in float64, whose rounding (t * 2^-53) is too small
+//    to turn the nearest non-tie (t * 2^-32 away, X below 2^24) into one.
+// fma(x, inv, 1.5 * 2^23) rounds to a whole number in one step, its low byte is
+// the code, and fma(x, inv, -that) the distance: three operations per element
+// and half a maximum; the rare cases run under a branch per 8 elements.
+//
+// The row stays in registers, so it is read once: bound by memory (16384 rows of
+// 4096 bf16: see the time at quantize_fmt).
 #include "elems.hpp"
 #include "i8_internal.hpp"
 
@@ -15,35 +24,65 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr uint32_t kInf = 0x7f800000u;
-constexpr float kTiny = 0x1p-100f;  // rows below this are scaled by 2^100 first: 127 / m stays finite
+constexpr float kTiny = 0x1p-100f;     // below, 127 / m could overflow: every element takes the exact path
+constexpr float kMagic = 12582912.f;    // 1.5 * 2^23: added, the sum's low bits are the rounded whole number
+constexpr float kNearHalf = 0.5f - 0x1p-13f;
 
 struct RowScale {
-  float m, up, inv;
-  bool ok;  // false: every code is 0 (the row is all zeros, or holds a NaN or an infinity)
+  float m, inv;
+  bool ok, tiny;  // ok: neither all zeros nor a NaN or an infinity, whose rows get codes of 0
 };
 
 // From the largest magnitude's bits (a NaN's are above infinity's, so either shows).
 __device__ __forceinline__ RowScale row_scale(uint32_t top, float *scale) {
   RowScale s;
   s.m = __builtin_bit_cast(float, top);
-  s.up = s.m < kTiny ? 0x1p100f : 1.f;
   s.ok = top != 0 && top < kInf;
-  s.inv = s.ok ? 127.f / (s.m * s.up) : 0.f;
+  s.tiny = s.m < kTiny;
+  s.inv = s.ok && !s.tiny ? 127.f / s.m : 0.f;
   *scale = top < kInf ? s.m / 127.f : __builtin_nanf("");
   return s;
 }
 
-__device__ __forceinline__ int code_of(float x, const RowScale &s) {
-  const float t = x * s.up * s.inv;
-  float q = rintf(t);
-  const float a = fabsf(t);
-  const float n = floorf(a);
-  if (fabsf(a - n - 0.5f) < 0x1p-14f && s.ok) {
-    const double d = 254.0 * fabs((double)x) - (2.0 * n + 1.0) * (double)s.m;
-    const bool upper = d > 0 || (d == 0 && ((int)n & 1));
-    q = copysignf(upper ? n + 1.f : n, x);
+__device__ __forceinline__ uint32_t exact_code(float x, float m) {
+  return (uint32_t)(int)rint(127.0 * (double)x / (double)m);
+}
+
+// Codes of N elements (N a multiple of 4), four to a dword.
+template <int FMT, int N>
+__device__ __forceinline__ void codes_of(const float (&x)[N], const RowScale &s, uint32_t (&out)[N / 4]) {
+  uint32_t q[N];
+  float far = 0.f;
+  if (s.ok && !s.tiny) {  // the same for the whole row
+    float e[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float r = fmaf(x[i], s.inv, kMagic);
+      q[i] = __builtin_bit_cast(uint32_t, r);
+      e[i] = fmaf(x[i], s.inv, kMagic - r);
+      far = fmaxf(far, fabsf(e[i]));
+    }
+    if (far > kNearHalf) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (fabsf(e[i]) <= kNearHalf) continue;
+        if constexpr (FMT == FMT_F32)
+          q[i] = exact_code(x[i], s.m);
+        else if ((q[i] & 1) && fabsf(e[i]) >= 0.5f - fabsf(x[i] * s.inv) * 0x1p-21f)
+          q[i] += e[i] > 0.f ? 1 : -1;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = s.ok ? exact_code(x[i], s.m) : 0;
   }
-  return s.ok ? (int)q : 0;
+#pragma unroll
+  for (int h = 0; h < N / 4; ++h) {
+    // the low bytes of four
+    const uint32_t lo = __builtin_amdgcn_perm(q[4 * h + 1], q[4 * h], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(q[4 * h + 3], q[4 * h + 2], 0x04000c0cu);
+    out[h] = lo | hi;
+  }
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
@@ -66,8 +105,6 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *part) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t mag(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
-
 // This thread's row: group z, row r; false when it lies past the group's rows.
 template <int TPR>
 __device__ __forceinline__ bool row_at(const QuantArgs &a, int64_t &z, int64_t &r) {
@@ -82,22 +119,48 @@ __device__ __forceinline__ bool row_at(const QuantArgs &a, int64_t &z, int64_t &
   return !a.rows || r < a.rows[z];
 }
 
-// Elements per chunk: 8 (16-bit rows: 16 bytes; float32: two vectors), codes 8 bytes.
+// A chunk is 8 elements (16 bytes, or two vectors of float32), kept as loaded; its codes are 8 bytes.
 template <int FMT>
 struct Chunk {
-  float v[8];
+  static constexpr int V = FMT == FMT_F32 ? 2 : 1;
+  Raw16 raw[V];
   __device__ __forceinline__ void load(const char *x, int64_t c) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) raw[i] = *(const Raw16 *)(x + (c * V + i) * 16);
+  }
+  // the first n elements at x, zeros behind them
+  __device__ __forceinline__ void load_part(const char *x, int64_t c, int n) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = i < n ? elem_bits<FMT>(x, c * 8 + i) : 0u;
+#pragma unroll
+    for (int i = 0; i < 4 * V; ++i)
+      raw[i / 4].d[i % 4] = FMT == FMT_F32 ? w[i] : w[(2 * i) % 8] | (w[(2 * i + 1) % 8] << 16);
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      Vec<FMT> u;
+      u.unpack(raw[i]);
+#pragma unroll
+      for (int j = 0; j < Vec<FMT>::N; ++j) v[i * Vec<FMT>::N + j] = u.v[j];
+    }
+  }
+  // bits of the largest magnitude as float32 (magnitudes of every format order like their bits)
+  __device__ __forceinline__ uint32_t top() const {
     if constexpr (FMT == FMT_F32) {
-      Vec<FMT> lo, hi;
-      lo.unpack(*(const Raw16 *)(x + c * 32));
-      hi.unpack(*(const Raw16 *)(x + c * 32 + 16));
+      uint32_t t = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = lo.v[i], v[4 + i] = hi.v[i];
+      for (int i = 0; i < 8; ++i) t = max(t, raw[i / 4].d[i % 4] & 0x7fffffffu);
+      return t;
     } else {
-      Vec<FMT> w;
-      w.unpack(*(const Raw16 *)(x + c * 16));
+      uint32_t lo = 0, hi = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = w.v[i];
+      for (int i = 0; i < 4; ++i) {
+        lo = max(lo, raw[0].d[i] & 0x7fffu);
+        hi = max(hi, raw[0].d[i] & 0x7fff0000u);
+      }
+      return __builtin_bit_cast(uint32_t, elem_f32<FMT>(max(lo, hi >> 16)));
     }
   }
 };
@@ -122,18 +185,11 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantArgs a) {
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const int c = lane + u * TPR;
-    if (c < whole) {
-      ch[u].load(x, c);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        ch[u].v[i] = c == whole && i < rest ? elem_f32<FMT>(elem_bits<FMT>(x, (int64_t)c * 8 + i)) : 0.f;
-    }
+    if (c < whole) ch[u].load(x, c);
+    else ch[u].load_part(x, c, c == whole ? rest : 0);
   }
 #pragma unroll
-  for (int u = 0; u < VPT; ++u)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, mag(ch[u].v[i]));
+  for (int u = 0; u < VPT; ++u) top = max(top, ch[u].top());
   top = row_max<TPR>(top, part);
   float sc;
   const RowScale s = row_scale(top, &sc);
@@ -141,18 +197,13 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantArgs a) {
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     const int c = lane + u * TPR;
-    if (c > whole || (c == whole && !rest)) continue;
+    float v[8];
+    ch[u].values(v);
     Raw8 o;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t d = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d |= ((uint32_t)code_of(ch[u].v[4 * h + i], s) & 0xffu) << (8 * i);
-      o.d[h] = d;
-    }
+    codes_of<FMT, 8>(v, s, o.d);
     if (c < whole) {
       *(Raw8 *)(q + (int64_t)c * 8) = o;
-    } else {
+    } else if (c == whole) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < rest) q[(int64_t)c * 8 + i] = (char)(o.d[i >> 2] >> (8 * (i & 3)));
@@ -170,52 +221,59 @@ __global__ __launch_bounds__(kThreads) void quantize_long_kernel(QuantArgs a) {
   const char *x = (const char *)a.X + (z * a.strideX + r * a.ldx) * ES;
   char *q = (char *)a.Q + z * a.strideQ + r * a.ldq;
   const int64_t whole = a.C / 8;
+  const int rest = (int)(a.C % 8);
   uint32_t top = 0;
+  Chunk<FMT> ch;
   for (int64_t c = threadIdx.x; c < whole; c += kThreads) {
-    Chunk<FMT> ch;
     ch.load(x, c);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, mag(ch.v[i]));
+    top = max(top, ch.top());
   }
-  const int64_t tail = whole * 8 + threadIdx.x;
-  const float xt = tail < a.C ? elem_f32<FMT>(elem_bits<FMT>(x, tail)) : 0.f;
-  top = row_max<kThreads>(max(top, mag(xt)), part);
+  if (threadIdx.x == 0) {
+    ch.load_part(x, whole, rest);
+    top = max(top, ch.top());
+  }
+  top = row_max<kThreads>(top, part);
   float sc;
   const RowScale s = row_scale(top, &sc);
   if (threadIdx.x == 0) a.scale[z * a.strideS + r] = sc;
+  float v[8];
+  Raw8 o;
   for (int64_t c = threadIdx.x; c < whole; c += kThreads) {
-    Chunk<FMT> ch;
     ch.load(x, c);
-    Raw8 o;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t d = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d |= ((uint32_t)code_of(ch.v[4 * h + i], s) & 0xffu) << (8 * i);
-      o.d[h] = d;
-    }
+    ch.values(v);
+    codes_of<FMT, 8>(v, s, o.d);
     *(Raw8 *)(q + c * 8) = o;
   }
-  if (tail < a.C) q[tail] = (char)code_of(xt, s);
+  if (threadIdx.x == 0) {
+    ch.load_part(x, whole, rest);
+    ch.values(v);
+    codes_of<FMT, 8>(v, s, o.d);
+    for (int i = 0; i < rest; ++i) q[whole * 8 + i] = (char)(o.d[i >> 2] >> (8 * (i & 3)));
+  }
 }
 
 template <int FMT>
 hipError_t quantize_fmt(const QuantArgs &base, hipStream_t stream) {
   const int64_t chunks = (base.C + 7) / 8;
-  const int tpr = chunks <= 64 ? 64 : 256;
-  const int64_t rows = base.R * base.groups, per = kThreads / tpr;
+  const int64_t rows = base.R * base.groups;
+  // a wave per row while its share of the row fits the registers and the rows fill the chip (no barrier); else a
+  // workgroup per row
+  const bool wave = chunks <= 64 || (chunks <= 512 && rows >= 2048);
+  const int64_t per = wave ? 4 : 1;
   const int64_t most = 0xffffffffLL / kThreads * per;  // rows per launch: work-items stay below 2^32
   for (int64_t r0 = 0; r0 < rows; r0 += most) {
     QuantArgs a = base;
     a.r0 = r0;
     const int64_t n = rows - r0 < most ? rows - r0 : most;
     const dim3 grid((unsigned)((n + per - 1) / per)), block(kThreads);
-    if (tpr == 64)
+    if (wave && chunks <= 64)
       hipLaunchKernelGGL((quantize_kernel<FMT, 64, 1>), grid, block, 0, stream, a);
+    else if (wave && chunks <= 256)
+      hipLaunchKernelGGL((quantize_kernel<FMT, 64, 4>), grid, block, 0, stream, a);
+    else if (wave)
+      hipLaunchKernelGGL((quantize_kernel<FMT, 64, 8>), grid, block, 0, stream, a);
     else if (chunks <= 256)
       hipLaunchKernelGGL((quantize_kernel<FMT, 256, 1>), grid, block, 0, stream, a);
-    else if (chunks <= 512)
-      hipLaunchKernelGGL((quantize_kernel<FMT, 256, 2>), grid, block, 0, stream, a);
     else if (chunks <= 1024)
       hipLaunchKernelGGL((quantize_kernel<FMT, 256, 4>), grid, block, 0, stream, a);
     else if (chunks <= 2048)
