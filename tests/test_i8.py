@@ -122,6 +122,43 @@ def test_large_tiles(monkeypatch, M, N, K, pad, out):
         assert torch.equal(c[z, :m], plain[z, :m]) and (c[z, m:] == 55.0).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(4352, 4096, 128), (4100, 4360, 256), (2200, 2304, 384)])
+def test_tiles_past_whole_rounds(M, N, K):
+    """A few 256-tiles more than one per CU (272, 306), or fewer than a round: the two launches together write every
+    element once, plain and with a batch."""
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a, b = padded(M, K, K, g), padded(N, K, K, g)
+    sa, sb = scales(M, g), scales(N, g) / K ** 0.5
+    buf = torch.full((M + 1, N + 8), 77.0, dtype=torch.float16, device="cuda")
+    say(f"[gpu] i8 tiles past whole rounds {M}x{N}x{K}")
+    assert tsm.tsm_gemm_i8_kernel_name(M, N, K, a, K, 0, b, K, 0, buf, N + 8, 0, 1, None, 1) == "i8_tile_256x256x128"
+    tsm.matmul_i8(a, sa, b.t(), sb, out=buf[:M, :N])
+    check(buf[:M, :N], reference(a, sa, b, sb), "f16")
+    assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
+
+
+@pytest.mark.parametrize("rows", [[2048] * 4 + [100] * 2, [600, 0, 300, 1, 0, 0], [0] * 6, [2048, 2048, 2048, 2048, 257, 513],
+                                  [2048] * 6])
+def test_grouped_rounds(rows):
+    """6 groups of up to 2048 rows, 2048 columns: 48 to 384 tiles of which the device leaves some to the second launch."""
+    import torch
+
+    M, N, K = 2048, 2048, 128
+    g = torch.Generator(device="cuda").manual_seed(sum(rows))
+    a = torch.randint(-128, 128, (6, M, K), generator=g, device="cuda", dtype=torch.int8)
+    b = torch.randint(-128, 128, (6, N, K), generator=g, device="cuda", dtype=torch.int8)
+    sa, sb = scales((6, M), g), scales((6, N), g)
+    c = torch.full((6, M, N), 55.0, dtype=torch.bfloat16, device="cuda")
+    r = torch.tensor(rows, dtype=torch.int32, device="cuda")
+    say(f"[gpu] i8 grouped rounds {rows}")
+    tsm.matmul_i8(a, sa, b.transpose(1, 2), sb, rows=r, out=c)
+    for z, m in enumerate(rows):
+        check(c[z, :m], reference(a[z, :m], sa[z, :m], b[z], sb[z]), "bf16")
+        assert (c[z, m:] == 55.0).all()
+
+
 @pytest.mark.parametrize("kernel", ["i8_skinny", "i8_stream"])
 @pytest.mark.parametrize("M", [1, 3, 4, 5, 16, 17, 32, 33, 64])
 @pytest.mark.parametrize("N,K", [(40, 16), (16, 256), (4200, 272), (20000, 1040), (100, 5120), (8208, 4112)])

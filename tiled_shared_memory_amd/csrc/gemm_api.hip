@@ -283,6 +283,8 @@ int plan_one(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, int la
   return TSM_SUCCESS;
 }
 
+}  // namespace
+
 // CUs of the current device (looked up once per device).
 int device_cus() {
   static std::atomic<int> cache[64];
@@ -294,6 +296,8 @@ int device_cus() {
   cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
+
+namespace {
 
 bool is_tile256(Kernel k) {
   return k == Kernel::TileST || k == Kernel::Tile16NN || k == Kernel::Tile16TN || k == Kernel::Tile16TT;

@@ -113,7 +113,7 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_skinny_kernel(I8Args p) {
     for (int j = 0; j < NB; ++j) part[wave][i * NB + j][lane] = acc[i][j];
   __syncthreads();
   const Epilogue ep{p.act, p.slope, false};
-  const float *sa = p.sa ? p.sa + z * p.stride_sa : nullptr, *sb = p.sb ? p.sb + z * p.stride_sb : nullptr;
+  const float *sa = p.sa ? p.sa + z * p.stride_sa : nullptr;
   for (int q = threadIdx.x; q < MB * NB * 64; q += W * 64) {
     const int blk = q >> 6, l = q & 63;
     const int64_t m = m0 + 16 * (blk / NB) + (l & 15), n = n0 + 16 * (blk % NB) + 4 * (l >> 4);
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_skinny_kernel(I8Args p) {
 #pragma unroll
     for (int w = 1; w < W; ++w) sum += part[w][blk][l];
     float cb[4];
-    channel_scales(p, sb, n, cb);
+    channel_scales(p, z, n, cb);
     store_i8<FMT>(p, ep, (char *)p.C + (z * p.strideC + m * p.ldc) * fmt_bytes(FMT), n, sa ? sa[m] : 1.f, cb, sum);
   }
 }
@@ -293,7 +293,7 @@ __device__ __forceinline__ void stream(const I8Args &p) {
     const I8Args e = *(const I8Args *)ka;
     const Place o = stream_tile<AR, NB>(e, t, first, lane);
     const Epilogue ep{e.act, e.slope, false};
-    const float *sa = e.sa ? e.sa + o.z * e.stride_sa : nullptr, *sb = e.sb ? e.sb + o.z * e.stride_sb : nullptr;
+    const float *sa = e.sa ? e.sa + o.z * e.stride_sa : nullptr;
     const char *const last = S == 2 ? s1 : s2;
     for (int k = threadIdx.x; k < MB * NB * 64; k += W * 64) {
       const int blk = k >> 6, l = k & 63;
@@ -303,7 +303,7 @@ __device__ __forceinline__ void stream(const I8Args &p) {
 #pragma unroll
       for (int w = 0; w < W; ++w) sum += *reinterpret_cast<const i32x4 *>(last + w * BYTES + k * 16);
       float cb[4];
-      channel_scales(e, sb, n, cb);
+      channel_scales(e, o.z, n, cb);
       store_i8<FMT>(e, ep, (char *)e.C + (o.z * e.strideC + m * e.ldc) * fmt_bytes(FMT), n, sa ? sa[m] : 1.f, cb, sum);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -107,8 +107,7 @@ template <int FMT>
 __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
   int tm, tn;
   int64_t z;
-  // groups of 4 tile rows from 32 up, else 8 (as the 16-bit kernel)
-  if (!i8_tile_of<BM>(p, p.tiles_m >= 32 && !p.rows ? 4 : 8, z, tm, tn)) return;  // uniform
+  if (!i8_tile_of<BM, true>(p, i8_tile_group(p), z, tm, tn)) return;  // uniform
   Ctx c;
   c.lane = threadIdx.x & 63;
   c.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -164,14 +163,15 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
   // ---- epilogue: acc.v[i][j] holds C[16 i + lane % 16][16 j + 4 (lane / 16) + 0..3] of the quadrant
   const Epilogue ep{p.act, p.slope, false};
   const int t = lane & 15, g = lane >> 4;
-  const float *sa = p.sa ? p.sa + z * p.stride_sa + m0 : nullptr;
-  const float *sb = p.sb ? p.sb + z * p.stride_sb + n0 : nullptr;
   float ca[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = wm * 128 + 16 * i + t;
-    ca[i] = sa && r < vr ? sa[r] : 1.f;
+    ca[i] = p.sa ? p.sa[z * p.stride_sa + m0 + (r < vr ? r : vr - 1)] : 1.f;
   }
+  float cb[8][4];
+#pragma unroll
+  for (int j2 = 0; j2 < 8; ++j2) channel_scales(p, z, n0 + wn * 128 + 16 * j2 + 4 * g, cb[j2]);
   constexpr int ES = fmt_bytes(FMT);
   const int64_t ldc = p.ldc;
   const __amdgpu_buffer_rsrc_t rc = make_rsrc((char *)p.C + (z * p.strideC + m0 * ldc + n0) * ES,
@@ -182,15 +182,11 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
     char *const q = c.wave == 0 ? s_a0 : c.wave == 1 ? s_a1 : c.wave == 2 ? s_b0 : s_b1;
 #pragma unroll
     for (int j2 = 0; j2 < 8; ++j2) {
-      float cb[4];
-      const int col = wn * 128 + 16 * j2 + 4 * g;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) cb[e] = sb && col < vc ? sb[col + e] : 1.f;  // N is a multiple of 8
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = ep.apply((float)acc.v[i][j2][e] * ca[i] * cb[e]);
+        for (int e = 0; e < 4; ++e) v[e] = ep.apply((float)acc.v[i][j2][e] * ca[i] * cb[j2][e]);
         *reinterpret_cast<u32x2 *>(q + (16 * i + t) * 256 + ((32 * j2 + 8 * g) ^ (16 * t))) =
             u32x2{f32_elem<FMT>(v[0]) | (f32_elem<FMT>(v[1]) << 16), f32_elem<FMT>(v[2]) | (f32_elem<FMT>(v[3]) << 16)};
       }
@@ -206,16 +202,13 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
   } else {
 #pragma unroll
     for (int j2 = 0; j2 < 8; ++j2) {
-      float cb[4];
       const int col = wn * 128 + 16 * j2 + 4 * g;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) cb[e] = sb && col < vc ? sb[col + e] : 1.f;
       const uint32_t off = col < vc ? (uint32_t)(((wm * 128 + t) * ldc + col) * 4) : kOutside;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         f32x4 v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = ep.apply((float)acc.v[i][j2][e] * ca[i] * cb[e]);
+        for (int e = 0; e < 4; ++e) v[e] = ep.apply((float)acc.v[i][j2][e] * ca[i] * cb[j2][e]);
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rc, off + (uint32_t)(16 * i * ldc * 4), 0, 0);
       }
     }
@@ -234,14 +227,26 @@ bool i8_tile_supports(const I8Args &p) {
   return 256 * p.ldc * es < (int64_t)1 << 31;  // 32-bit store offsets
 }
 
-hipError_t launch_i8_tile(const I8Args &p, hipStream_t stream) {
-  return over_tiles(p, BM, BN, 256, [&](const I8Args &a, dim3 grid) {
-    if (a.fmt == FMT_F32)
-      hipLaunchKernelGGL((gemm_i8_tile_kernel<FMT_F32>), grid, dim3(256), 0, stream, a);
-    else if (a.fmt == FMT_F16)
-      hipLaunchKernelGGL((gemm_i8_tile_kernel<FMT_F16>), grid, dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((gemm_i8_tile_kernel<FMT_BF16>), grid, dim3(256), 0, stream, a);
+hipError_t launch_i8_tile(const I8Args &p, bool whole_only, hipStream_t stream) {
+  I8Args q = p;
+  q.cus = whole_only ? device_cus() : 0;
+  return over_tiles(q, BM, BN, 256, [&](const I8Args &a, dim3 grid) {
+    // without counts the host knows the tiles of whole rounds
+    const int64_t whole = a.rows ? (int64_t)grid.x : whole_rounds(grid.x, a.cus);
+    if (whole) {
+      const dim3 g((unsigned)whole);
+      if (a.fmt == FMT_F32)
+        hipLaunchKernelGGL((gemm_i8_tile_kernel<FMT_F32>), g, dim3(256), 0, stream, a);
+      else if (a.fmt == FMT_F16)
+        hipLaunchKernelGGL((gemm_i8_tile_kernel<FMT_F16>), g, dim3(256), 0, stream, a);
+      else
+        hipLaunchKernelGGL((gemm_i8_tile_kernel<FMT_BF16>), g, dim3(256), 0, stream, a);
+      if (hipPeekAtLastError() != hipSuccess) return;
+    }
+    if (whole_only && (a.rows || whole < (int64_t)grid.x)) {
+      const hipError_t e = launch_i8_rest(a, stream);
+      (void)e;  // the launch's error is the last one
+    }
   });
 }
 

@@ -7,7 +7,7 @@
 #include "elems.hpp"
 #include "gemm_internal.hpp"
 #include "host_checks.hpp"
-#include "i8_internal.hpp"
+#include "i8_common.hpp"
 #include "tsm_gemm.h"
 
 namespace tsm {
@@ -35,9 +35,10 @@ const char *i8_name(I8Kernel k) {
 int i8_plan(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64_t strideA, const float *scale_a,
             int64_t stride_sa, const int8_t *B, int64_t ldb, int64_t strideB, const float *scale_b, int64_t stride_sb,
             void *C, int64_t ldc, int64_t strideC, int64_t batch, const int32_t *rows, bool grouped, int out_dtype,
-            int act, float slope, I8Args *p, I8Kernel *kernel) {
+            int act, float slope, I8Args *p, I8Kernel *kernel, bool *forced) {
   g_detail[0] = '\0';
   *kernel = I8Kernel::None;
+  *forced = false;
   if (out_dtype != TSM_F32 && out_dtype != TSM_F16 && out_dtype != TSM_BF16)
     return fail(TSM_ERROR_INVALID_VALUE, "unknown out_dtype %d", out_dtype);
   if (act != TSM_ACT_NONE && act != TSM_ACT_RELU && act != TSM_ACT_LEAKY_RELU)
@@ -115,12 +116,16 @@ int i8_plan(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64
   p->slope = act == TSM_ACT_LEAKY_RELU ? slope : 0.f;
   p->vec_store = (uintptr_t)C % (uintptr_t)(4 * es) == 0 && ldc % 4 == 0 && strideC % 4 == 0;
 
+  // 64-tiles up to 128 of 128 x 128 (512 x 4096 x 4096, 128 tiles: 24.6 us
+  // against 26.3; 640 x 4096 x 2048, 160: 19.0 against 15.5), 256-tiles from 72
+  // (2304 x 2304 x 1024, 81: 19.4 against 21.1; 2048 x 2048 x 2048, 64: 27.7
+  // against 17.3), the streaming kernels up to 64 rows.
   const int64_t tiles128 = ((M + 127) / 128) * ((N + 127) / 128), tiles64 = ((M + 63) / 64) * ((N + 63) / 64);
-  *kernel = tiles128 * batch < 512 ? I8Kernel::Block64 : I8Kernel::Block128;
-  if ((*kernel == I8Kernel::Block64 ? tiles64 : tiles128) * 256 > 0xffffffffLL)
+  *kernel = tiles128 * batch <= 128 ? I8Kernel::Block64 : I8Kernel::Block128;
+  if ((*kernel == I8Kernel::Block64 ? tiles64 : tiles128) * 512 > 0xffffffffLL)
     return fail(TSM_ERROR_NOT_SUPPORTED, "tile grid too large");
   const int64_t tiles256 = ((M + 255) / 256) * ((N + 255) / 256) * batch;
-  if (tiles256 >= 72 && i8_tile_supports(*p)) *kernel = I8Kernel::Tile;
+  if (tiles256 >= kFewTiles && i8_tile_supports(*p)) *kernel = I8Kernel::Tile;
   const I8Skinny sk = i8_skinny_plan(*p);
   if (sk.rows) *kernel = sk.stream ? I8Kernel::Stream : I8Kernel::Skinny;
   // TSM_GEMM_KERNEL=<name> forces a variant (tests and tuning); names of other
@@ -135,11 +140,12 @@ int i8_plan(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64
         (want == I8Kernel::Skinny && !sk.rows))
       return fail(TSM_ERROR_NOT_SUPPORTED, "TSM_GEMM_KERNEL=%s cannot run this problem", force);
     *kernel = want;
+    *forced = true;
   }
   return TSM_SUCCESS;
 }
 
-int i8_run(const I8Args &p, I8Kernel k, void *stream) {
+int i8_run(const I8Args &p, I8Kernel k, bool forced, void *stream) {
   const hipStream_t s = (hipStream_t)stream;
   hipError_t e = hipSuccess;
   switch (k) {
@@ -152,7 +158,7 @@ int i8_run(const I8Args &p, I8Kernel k, void *stream) {
       e = launch_i8_block(p, 64, s);
       break;
     case I8Kernel::Tile:
-      e = launch_i8_tile(p, s);
+      e = launch_i8_tile(p, !forced, s);
       break;
     case I8Kernel::Stream:
     case I8Kernel::Skinny: {
@@ -177,9 +183,10 @@ int gemm_i8_strided_batched(int64_t M, int64_t N, int64_t K, const int8_t *A, in
                             int64_t batch, int out_dtype, int activation, float slope, void *stream) {
   tsm::I8Args p;
   tsm::I8Kernel k;
+  bool forced;
   const int st = tsm::i8_plan(M, N, K, A, lda, strideA, scale_a, stride_sa, B, ldb, strideB, scale_b, stride_sb, C, ldc,
-                              strideC, batch, nullptr, false, out_dtype, activation, slope, &p, &k);
-  return st == TSM_SUCCESS ? tsm::i8_run(p, k, stream) : st;
+                              strideC, batch, nullptr, false, out_dtype, activation, slope, &p, &k, &forced);
+  return st == TSM_SUCCESS ? tsm::i8_run(p, k, forced, stream) : st;
 }
 
 int gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *scale_a, const int8_t *B,
@@ -194,9 +201,10 @@ int gemm_i8_grouped(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t ld
                     const int32_t *rows, int64_t groups, int out_dtype, int activation, float slope, void *stream) {
   tsm::I8Args p;
   tsm::I8Kernel k;
+  bool forced;
   const int st = tsm::i8_plan(M, N, K, A, lda, strideA, scale_a, stride_sa, B, ldb, strideB, scale_b, stride_sb, C, ldc,
-                              strideC, groups, rows, true, out_dtype, activation, slope, &p, &k);
-  return st == TSM_SUCCESS ? tsm::i8_run(p, k, stream) : st;
+                              strideC, groups, rows, true, out_dtype, activation, slope, &p, &k, &forced);
+  return st == TSM_SUCCESS ? tsm::i8_run(p, k, forced, stream) : st;
 }
 
 const char *tsm_gemm_i8_kernel_name(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64_t strideA,
@@ -204,8 +212,9 @@ const char *tsm_gemm_i8_kernel_name(int64_t M, int64_t N, int64_t K, const int8_
                                     int64_t strideC, int64_t batch, const int32_t *rows, int out_dtype) {
   tsm::I8Args p;
   tsm::I8Kernel k;
+  bool forced;
   if (tsm::i8_plan(M, N, K, A, lda, strideA, nullptr, 0, B, ldb, strideB, nullptr, 0, C, ldc, strideC, batch, rows,
-                   rows != nullptr, out_dtype, TSM_ACT_NONE, 0.f, &p, &k) != TSM_SUCCESS)
+                   rows != nullptr, out_dtype, TSM_ACT_NONE, 0.f, &p, &k, &forced) != TSM_SUCCESS)
     return nullptr;
   return tsm::i8_name(k);
 }

@@ -23,26 +23,28 @@ __device__ __forceinline__ u32x4 load16(const int8_t *p) {
   return u32x4{r.d[0], r.d[1], r.d[2], r.d[3]};
 }
 
+// 16 codes without their first `drop`, zeros behind the others (drop <= 0: as they are).
+__device__ __forceinline__ u32x4 drop_front(u32x4 v, int drop) {
+  if (drop <= 0) return v;
+  if (drop >= 16) return u32x4{};
+  const uint64_t lo = (uint64_t)v[0] | ((uint64_t)v[1] << 32), hi = (uint64_t)v[2] | ((uint64_t)v[3] << 32);
+  uint64_t a, b;
+  if (drop >= 8) {
+    a = hi >> (8 * (drop - 8));
+    b = 0;
+  } else {
+    a = (lo >> (8 * drop)) | (hi << (64 - 8 * drop));
+    b = hi >> (8 * drop);
+  }
+  return u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+}
+
 // Codes k .. k+15 of a row of K, zeros past K; nothing outside the row is read.
 __device__ __forceinline__ u32x4 load_tail(const int8_t *row, int64_t k, int64_t K) {
   if (k + 16 <= K) return load16(row + k);
   u32x4 v = {};
   if (k >= K) return v;
-  if (K >= 16) {
-    // the row's last 16 codes, those before k shifted out
-    const Raw16 r = *(const Raw16 *)(row + K - 16);
-    const int drop = (int)(16 - (K - k));  // 1..15
-    const uint64_t lo = (uint64_t)r.d[0] | ((uint64_t)r.d[1] << 32), hi = (uint64_t)r.d[2] | ((uint64_t)r.d[3] << 32);
-    uint64_t a, b;
-    if (drop >= 8) {
-      a = hi >> (8 * (drop - 8));
-      b = 0;
-    } else {
-      a = (lo >> (8 * drop)) | (hi << (64 - 8 * drop));
-      b = hi >> (8 * drop);
-    }
-    return u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
-  }
+  if (K >= 16) return drop_front(load16(row + K - 16), (int)(16 - (K - k)));
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     if (k + i < K) v[i >> 2] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i & 3));
@@ -72,10 +74,16 @@ __device__ __forceinline__ void store_i8(const I8Args &p, const Epilogue &ep, ch
   }
 }
 
-// Scales of channels n .. n+3 (ones past N or without scales).
-__device__ __forceinline__ void channel_scales(const I8Args &p, const float *sb, int64_t n, float (&c)[4]) {
+// Scales of channels n .. n+3 of problem z (past N the last one's, for results that are not stored).
+__device__ __forceinline__ void channel_scales(const I8Args &p, int64_t z, int64_t n, float (&c)[4]) {
+  if (!p.sb) {  // uniform
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = sb && n + i < p.N ? sb[n + i] : 1.f;
+    for (int i = 0; i < 4; ++i) c[i] = 1.f;
+    return;
+  }
+  const float *sb = p.sb + z * p.stride_sb;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = sb[n + i < p.N ? n + i : p.N - 1];
 }
 
 // ---- grouped calls: which group a tile belongs to, by the counts in device memory ----
@@ -125,23 +133,48 @@ __device__ __forceinline__ void find_group(const I8Args &p, int lane, int &t, in
 // Where a workgroup of a flat grid works: problem z, tile (tm, tn) in the
 // grouped tile order, the grid regrouped per XCD.  Grouped calls number only
 // the tiles that hold rows, so the real work spreads evenly over the XCDs;
-// false: nothing to do.
+// false: nothing to do.  WHOLE: only the tiles of whole_rounds.
+// Fewer than this many 256-tiles left over from whole rounds of the CUs run as
+// 128-tiles in a second launch: a round takes as long for one tile as for all
+// (2304 x 2304 x 1024, 81 tiles: 19.4 us against 21.1 in 128-tiles; 2048 x 2048 x
+// 2048, 64 tiles: 27.7 against 17.3).
+// (cus = 0: every tile stays.)
+constexpr int kFewTiles = 72;
+__host__ __device__ inline int64_t whole_rounds(int64_t tiles, int64_t cus) {
+  if (!cus) return tiles;
+  const int64_t left = tiles % cus;
+  return left < kFewTiles ? tiles - left : tiles;
+}
+
+// Tile rows per group of the 256-tiles' order: 4 from 32 tile rows up, else 8 (as the 16-bit kernel).
+__device__ __forceinline__ int i8_tile_group(const I8Args &p) { return p.tiles_m >= 32 && !p.rows ? 4 : 8; }
+
+// Tile pid of problem-after-problem order, BM rows of a problem's rows each.
 template <int BM>
-__device__ __forceinline__ bool i8_tile_of(const I8Args &p, int group_m, int64_t &z, int &tm, int &tn) {
+__device__ __forceinline__ void i8_tile_at(const I8Args &p, int pid, int group_m, int64_t &z, int &tm, int &tn) {
+  int tiles = p.tiles_m;
   if (p.rows) {
-    const int lane = threadIdx.x & 63;
-    const int V = all_group_tiles<BM>(p, lane) * p.tiles_n;
-    if ((int)blockIdx.x >= V) return false;
-    int pid = xcd_remap(blockIdx.x, V), g, tiles;
-    find_group<BM>(p, lane, pid, g, tiles);
-    tile_order(pid, tiles, p.tiles_n, group_m, tm, tn);
+    int g;
+    find_group<BM>(p, threadIdx.x & 63, pid, g, tiles);
     z = p.z0 + g;
-    return true;
+  } else {
+    const int T = p.tiles_m * p.tiles_n;
+    z = p.z0 + pid / T;
+    pid %= T;
   }
-  const int T = p.tiles_m * p.tiles_n;
-  const int pid = xcd_remap(blockIdx.x, gridDim.x);
-  z = p.z0 + pid / T;
-  tile_order(pid % T, p.tiles_m, p.tiles_n, group_m, tm, tn);
+  tile_order(pid, tiles, p.tiles_n, group_m, tm, tn);
+}
+template <int BM>
+__device__ __forceinline__ int i8_tiles(const I8Args &p) {
+  return (p.rows ? all_group_tiles<BM>(p, threadIdx.x & 63) : p.tiles_m * p.nz) * p.tiles_n;
+}
+
+template <int BM, bool WHOLE = false>
+__device__ __forceinline__ bool i8_tile_of(const I8Args &p, int group_m, int64_t &z, int &tm, int &tn) {
+  int V = i8_tiles<BM>(p);
+  if (WHOLE) V = (int)whole_rounds(V, p.cus);
+  if ((int)blockIdx.x >= V) return false;
+  i8_tile_at<BM>(p, xcd_remap(blockIdx.x, V), group_m, z, tm, tn);
   return true;
 }
 

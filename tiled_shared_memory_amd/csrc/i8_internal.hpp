@@ -24,6 +24,7 @@ struct I8Args {
   int32_t tiles_m, tiles_n;
   int64_t z0;       // first problem of this launch
   int32_t nz;       // problems of this launch
+  int32_t cus;      // 256 x 256 tiles: CUs, one tile each per round (0: no second launch)
 };
 
 // Rows of problem z (a grouped call's count, clamped to [0, M]).
@@ -38,7 +39,10 @@ constexpr int64_t kI8MaxK = 131071;
 
 // 256 x 256 tiles: see i8_tile_supports for what they need.
 bool i8_tile_supports(const I8Args &p);
-hipError_t launch_i8_tile(const I8Args &p, hipStream_t stream);
+// whole_only: tiles left over from whole rounds of the CUs go to launch_i8_rest.
+hipError_t launch_i8_tile(const I8Args &p, bool whole_only, hipStream_t stream);
+// The 256 x 256 tiles that whole_rounds leaves of a launch (tiles_m, tiles_n, z0 and nz set), as 128 x 128 ones.
+hipError_t launch_i8_rest(const I8Args &a, hipStream_t stream);
 // Few rows (up to 64): `rows` of them (0: not for this problem) by 16 nb columns per workgroup of `waves` waves.
 struct I8Skinny {
   int rows = 0, nb = 0, waves = 0;
