@@ -391,7 +391,7 @@ const char *tsm_gemm_i8_kernel_name(int64_t M, int64_t N, int64_t K, const int8_
  * the grouped products clamp to their M).
  *   ids        : DEVICE expert ids, idtype TSM_I32 or TSM_I64, ld_ids >= topk.
  *   experts    : at most 512.  experts * capacity and tokens * topk below 2^31.
- *   workspace  : DEVICE memory of moe_sort_workspace_bytes(...) bytes, 4-byte
+ *   workspace  : DEVICE memory of moe_sort_workspace_bytes(...) bytes, 16-byte
  *                aligned, its contents irrelevant before and after (NULL where
  *                that is 0).  Calls in flight at once must not share one.
  * The result is the same on every call.  tokens = 0 or topk = 0 writes counts of 0.

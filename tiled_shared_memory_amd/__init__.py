@@ -9,8 +9,6 @@ HIP kernels.
 
 from __future__ import annotations
 
-import functools
-
 from ._lib import (TSM_ACT_LEAKY_RELU, TSM_ACT_NONE, TSM_ACT_RELU, TSM_BF16, TSM_BF16_BF16,  # noqa: F401
                    TSM_BF16_F16, TSM_BF16_F32, TSM_COL, TSM_ERROR_INVALID_VALUE, TSM_ERROR_LAUNCH,
                    TSM_ERROR_NOT_SUPPORTED, TSM_F16, TSM_F16_BF16, TSM_F16_F16, TSM_F16_F32, TSM_F32, TSM_I8, TSM_I32,
@@ -162,33 +160,35 @@ def _new(like, shape, dtype, fill=None):
     return (torch.empty if fill is None else torch.zeros)(shape, dtype=dtype, device=like.device)
 
 
-def _one_gpu(first, *others):
-    """Every tensor is on the GPU of the first."""
+class _Here:
+    """The guard of a call whose tensors are on the current GPU: none."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _gpu_of(first, *others):
+    """Check that every tensor is on the GPU of the first; a guard that makes it the current one for the launch."""
     d = first.get_device()
     for t in others:
         if t is not None and t.get_device() != d:
             _bad(f"tensors on {first.device} and {t.device}")
+    if d == current_device():
+        return _HERE
+    import torch
 
-
-def _on_its_gpu(fn):
-    """Run fn with the GPU of its first tensor current: its launches, allocations and default stream are that GPU's."""
-
-    @functools.wraps(fn)
-    def run(first, *args, **kwargs):
-        if not first.is_cuda or first.get_device() == current_device():
-            return fn(first, *args, **kwargs)
-        import torch
-
-        with torch.cuda.device(first.device):
-            return fn(first, *args, **kwargs)
-
-    return run
+    return torch.cuda.device(d)
 
 
 _FLOATS = (TSM_F32, TSM_F16, TSM_BF16)
 
 
-@_on_its_gpu
 def quantize(x, *, rows=None, out=None, scale=None, stream=None):
     """(codes, scales) of the rows of ``x`` (..., R, C) in float32, float16 or bfloat16: int8 codes with
     ``x ~ codes * scales[..., None]``, the scales float32 of shape (..., R).
@@ -213,12 +213,11 @@ def quantize(x, *, rows=None, out=None, scale=None, stream=None):
         _bad("scale: rows must be contiguous")
     ldx, ldq = _rows_ld("x", x), _rows_ld("out", out)
     sx, sq, ss = (x.stride(0), out.stride(0), scale.stride(0)) if x.dim() == 3 else (0, 0, 0)
-    _one_gpu(x, out, scale, rows)
-    quantize_i8(x.shape[-2], x.shape[-1], x, ldx, sx, f, out, ldq, sq, scale, ss, rows, G, stream)
+    with _gpu_of(x, out, scale, rows):
+        quantize_i8(x.shape[-2], x.shape[-1], x, ldx, sx, f, out, ldq, sq, scale, ss, rows, G, stream)
     return out, scale
 
 
-@_on_its_gpu
 def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, activation=None, slope=0.01, stream=None):
     """C = act(scale_a[..., None] * scale_b * (A.B)) for int8 CUDA tensors ``a`` (..., M, K) and ``b`` (..., K, N).
 
@@ -266,15 +265,15 @@ def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, ac
     sc = out.stride(0) if batched else 0
     act = _ACTIVATIONS[activation]
     if rows is None:
-        _one_gpu(a, b, out, scale_a, scale_b)
-        gemm_i8_strided_batched(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb, out, ldc, sc, batch, f,
-                                act, slope, stream)
+        with _gpu_of(a, b, out, scale_a, scale_b):
+            gemm_i8_strided_batched(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb, out, ldc, sc, batch, f,
+                                    act, slope, stream)
     else:
         _wants("rows", rows, (TSM_I32,), (batch,))
         _packed("rows", rows)
-        _one_gpu(a, b, out, scale_a, scale_b, rows)
-        gemm_i8_grouped(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb, out, ldc, sc, rows, batch, f,
-                        act, slope, stream)
+        with _gpu_of(a, b, out, scale_a, scale_b, rows):
+            gemm_i8_grouped(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb, out, ldc, sc, rows, batch, f,
+                            act, slope, stream)
     return out
 
 
@@ -284,7 +283,6 @@ def sort_workspace_for(ids, experts):
     return _new(ids, (n,), "uint8") if n else None
 
 
-@_on_its_gpu
 def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspace=None, stream=None):
     """(positions, counts) of the experts' ids (tokens, topk), int32 or int64: the row of each choice in the slabs
     (experts * capacity rows, expert e's from e * capacity), in token order, -1 for an id outside [0, experts) or past
@@ -310,9 +308,9 @@ def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspac
             _bad("workspace is not on a GPU")
         _packed("workspace", workspace)
     nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _one_gpu(ids, positions, counts, workspace)
-    moe_sort(ids.shape[0], ids.shape[1], ids, _rows_ld("ids", ids), f, experts, capacity, positions, counts,
-             workspace, nbytes, stream)
+    with _gpu_of(ids, positions, counts, workspace):
+        moe_sort(ids.shape[0], ids.shape[1], ids, _rows_ld("ids", ids), f, experts, capacity, positions, counts,
+                 workspace, nbytes, stream)
     return positions, counts
 
 
@@ -326,7 +324,6 @@ def _slab_args(what, slabs, positions, tokens, hidden):
     _packed("positions", positions)
 
 
-@_on_its_gpu
 def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale=None, stream=None):
     """Token rows ``x`` (tokens, hidden) at their ``positions`` (tokens, topk) in the slabs (slots, hidden), float32,
     float16, bfloat16 or int8.
@@ -354,13 +351,12 @@ def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale
         _packed("out_scale", out_scale)
     elif out_scale is not None:
         _bad("out_scale without scale")
-    _one_gpu(x, out, positions, scale, out_scale)
-    moe_dispatch(x.shape[0], positions.shape[1], x.shape[1], x, _rows_ld("x", x), f, scale, positions,
-                 out.shape[0], out, _rows_ld("out", out), out_scale, stream)
+    with _gpu_of(x, out, positions, scale, out_scale):
+        moe_dispatch(x.shape[0], positions.shape[1], x.shape[1], x, _rows_ld("x", x), f, scale, positions,
+                     out.shape[0], out, _rows_ld("out", out), out_scale, stream)
     return out if scale is None else (out, out_scale)
 
 
-@_on_its_gpu
 def combine_tokens(slabs, positions, weights=None, *, out=None, stream=None):
     """Y[t] = sum_j weights[t, j] * slabs[positions[t, j]] over the choices with a position, float32 sums in the order
     of j; ``weights`` float32 (tokens, topk), None for ones.  Y has the slabs' dtype (float32, float16 or bfloat16)."""
@@ -373,9 +369,9 @@ def combine_tokens(slabs, positions, weights=None, *, out=None, stream=None):
     if weights is not None:
         _wants("weights", weights, (TSM_F32,), positions.shape)
         _packed("weights", weights)
-    _one_gpu(slabs, out, positions, weights)
-    moe_combine(tokens, positions.shape[1], hidden, slabs, _rows_ld("slabs", slabs), slabs.shape[0], f,
-                positions, weights, out, _rows_ld("out", out), stream)
+    with _gpu_of(slabs, out, positions, weights):
+        moe_combine(tokens, positions.shape[1], hidden, slabs, _rows_ld("slabs", slabs), slabs.shape[0], f,
+                    positions, weights, out, _rows_ld("out", out), stream)
     return out
 
 
@@ -384,7 +380,6 @@ def dispatch_tokens_backward(dslabs, positions, *, out=None, stream=None):
     return combine_tokens(dslabs, positions, None, out=out, stream=stream)
 
 
-@_on_its_gpu
 def combine_tokens_backward(dy, slabs, positions, weights=None, *, out=None, dweights=None, stream=None):
     """(dslabs, dweights) of ``combine_tokens`` from ``dy`` (tokens, hidden): dslabs[positions[t, j]] =
     weights[t, j] * dy[t] (``out``; its other rows are kept, or zeros where it is allocated here) and
@@ -404,8 +399,8 @@ def combine_tokens_backward(dy, slabs, positions, weights=None, *, out=None, dwe
     if weights is not None:
         _wants("weights", weights, (TSM_F32,), positions.shape)
         _packed("weights", weights)
-    _one_gpu(dy, slabs, out, positions, weights, dweights)
-    moe_combine_backward(dy.shape[0], positions.shape[1], dy.shape[1], dy, _rows_ld("dy", dy), slabs,
-                         _rows_ld("slabs", slabs), slabs.shape[0], f, positions, weights, out, _rows_ld("out", out),
-                         dweights, stream)
+    with _gpu_of(dy, slabs, out, positions, weights, dweights):
+        moe_combine_backward(dy.shape[0], positions.shape[1], dy.shape[1], dy, _rows_ld("dy", dy), slabs,
+                             _rows_ld("slabs", slabs), slabs.shape[0], f, positions, weights, out, _rows_ld("out", out),
+                             dweights, stream)
     return out, dweights

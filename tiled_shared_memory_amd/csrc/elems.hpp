@@ -19,6 +19,30 @@ struct __attribute__((packed, aligned(1))) Raw16 {
 };
 static_assert(sizeof(Raw16) == 16, "");
 
+// The same past the caches (read or written once).
+__device__ __forceinline__ Raw16 load_once(const char *p) {
+  typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(1)));
+  const vec v = __builtin_nontemporal_load((const vec *)p);
+  return Raw16{{v[0], v[1], v[2], v[3]}};
+}
+__device__ __forceinline__ void store_once(char *p, const Raw16 &r) {
+  typedef uint32_t vec __attribute__((ext_vector_type(4), aligned(1)));
+  __builtin_nontemporal_store(vec{r.d[0], r.d[1], r.d[2], r.d[3]}, (vec *)p);
+}
+
+template <bool ONCE>
+__device__ __forceinline__ Raw16 load_vec(const char *p) {
+  if constexpr (ONCE) return load_once(p);
+  return *(const Raw16 *)p;
+}
+template <bool ONCE>
+__device__ __forceinline__ void store_vec(char *p, const Raw16 &r) {
+  if constexpr (ONCE)
+    store_once(p, r);
+  else
+    *(Raw16 *)p = r;
+}
+
 template <int FMT>
 __device__ __forceinline__ float elem_f32(uint32_t bits) {
   if constexpr (FMT == FMT_F32) return __builtin_bit_cast(float, bits);

@@ -33,7 +33,7 @@ __device__ __forceinline__ int expert_of(const SortArgs &a, int64_t i) {
   }
 }
 
-// Entries per expert of each tile, into hist[block][expert].  Integer sums: the
+// Entries per expert of each tile, into hist[tile][expert] (rows of a multiple of 4 experts).  Integer sums: the
 // order of the atomics does not matter.
 template <bool ID64>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
     if (e >= 0) atomicAdd(&sh[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) a.hist[(int64_t)blockIdx.x * a.experts + e] = sh[e];
+  for (int e = threadIdx.x; e < a.experts; e += kSortThreads) a.hist[(int64_t)blockIdx.x * sort_pitch(a.experts) + e] = sh[e];
 }
 
 // Positions of one tile's entries.  Each wave owns a run of consecutive
@@ -66,37 +66,59 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   const int64_t left = n - i0 < tile ? n - i0 : tile;
   const int steps = (int)((left + kSortThreads - 1) / kSortThreads);  // 64 entries per wave and step
   const int64_t w0 = i0 + (int64_t)wave * steps * 64;
-  for (int s = 0; s < steps; ++s) {
+  constexpr int S = (int)(SortInfo::kOneBlock / kSortThreads);
+  int own[S];  // this lane's experts
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
     const int64_t i = w0 + s * 64 + lane;
-    const int e = i < n && i < i0 + tile ? expert_of<ID64>(a, i) : -1;
-    if (e >= 0) atomicAdd(&sh[wave * E + e], 1);
+    own[s] = s < steps && i < n && i < i0 + tile ? expert_of<ID64>(a, i) : -1;
   }
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (own[s] >= 0) atomicAdd(&sh[wave * E + own[s]], 1);
   if (a.hist) {
-    // entries of the tiles before: thread tid adds up expert tid % E over every (1024 / E)-th tile
-    const int per = kSortThreads / E, g = threadIdx.x / E, e = threadIdx.x % E;
+    // entries of the tiles before: a thread adds up 4 experts over every (1024 / (E / 4))-th tile, eight loads at a time
+    // (past the tiles before this one its last again, not counted; a loop of single loads waits for each)
+    const int E4 = (int)sort_pitch(E) / 4, per = kSortThreads / E4, g = threadIdx.x / E4, e4 = threadIdx.x % E4;
     if (g < per) {
-      int32_t sum = 0;
-#pragma unroll 8
-      for (int b = g; b < (int)blockIdx.x; b += per) sum += a.hist[(int64_t)b * E + e];
-      if (sum) atomicAdd(&before[e], sum);
+      const int4 *col = (const int4 *)a.hist + e4;
+      const int mine = (int)blockIdx.x;
+      int4 sum{0, 0, 0, 0};
+      constexpr int U = 8;
+      for (int b0 = g; b0 < mine; b0 += U * per) {
+        int4 h[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) h[u] = col[(int64_t)min(b0 + u * per, mine - 1) * E4];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (b0 + u * per < mine) sum.x += h[u].x, sum.y += h[u].y, sum.z += h[u].z, sum.w += h[u].w;
+      }
+      const int32_t s4[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * e4 + i < E && s4[i]) atomicAdd(&before[4 * e4 + i], s4[i]);
     }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kSortThreads) {
-    int32_t at = before[e];
+    int32_t at = before[e], c[kSortWaves];
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) c[w] = sh[w * E + e];
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const int32_t c = sh[w * E + e];
       sh[w * E + e] = at;
-      at += c;
+      at += c[w];
     }
     if (blockIdx.x == gridDim.x - 1) a.counts[e] = at;
   }
   __syncthreads();
   const int bits = 32 - __clz(E);  // enough for 0 .. experts
-  for (int s = 0; s < steps; ++s) {
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    if (s >= steps) break;  // uniform
     const int64_t i = w0 + s * 64 + lane;
     const bool in = i < n && i < i0 + tile;
-    const int e = in ? expert_of<ID64>(a, i) : -1;
+    const int e = own[s];
     // lanes with the same expert as this one
     const uint32_t key = e < 0 ? (uint32_t)E : (uint32_t)e;
     uint64_t same = ~0ull;
@@ -145,7 +167,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(MoveArgs a) {
   Raw16 v[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (c0 + u * TPR < whole) v[u] = *(const Raw16 *)(x + (c0 + u * TPR) * 16);
+    if (c0 + u * TPR < whole) v[u] = load_once(x + (c0 + u * TPR) * 16);
   for (int j = 0; j < a.topk; ++j) {
     const int64_t s = slot_of(a, t * a.topk + j);
     if (s < 0) continue;
@@ -154,7 +176,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(MoveArgs a) {
     for (int u = 0; u < U; ++u) {
       const int64_t c = c0 + u * TPR;
       if (c < whole)
-        *(Raw16 *)(y + c * 16) = v[u];
+        store_once(y + c * 16, v[u]);
       else if (c < chunks)
         for (int64_t i = whole * N; i < a.hidden; ++i) put_bits<FMT>(y, i, elem_bits<FMT>(x, i));
     }
@@ -162,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(MoveArgs a) {
   }
 }
 
-template <int FMT, int TPR, int U>
+template <int FMT, int TPR, int U, bool ONCE>
 __global__ __launch_bounds__(kThreads) void combine_kernel(MoveArgs a) {
   constexpr int ES = fmt_bytes(FMT), N = 16 / ES;
   int64_t t, c0;
@@ -181,7 +203,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(MoveArgs a) {
       const int64_t c = c0 + u * TPR;
       if (c < whole) {
         Vec<FMT> v;
-        v.unpack(*(const Raw16 *)(x + c * 16));
+        v.unpack(load_vec<ONCE>(x + c * 16));
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[u][i] = fmaf(w, v.v[i], acc[u][i]);
       } else if (c < chunks) {
@@ -198,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(MoveArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v.v[i] = acc[u][i];
     if (c < whole) {
-      *(Raw16 *)(y + c * 16) = v.pack();
+      store_vec<ONCE>(y + c * 16, v.pack());
     } else if (c < chunks) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -209,7 +231,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(MoveArgs a) {
 
 // One workgroup (TPR = 256) or wave (TPR = 64) per token; JB choices at a time, so dY is read ceil(topk / JB)
 // times (from cache after the first).
-template <int FMT, int TPR, int JB>
+template <int FMT, int TPR, int JB, bool ONCE>
 __global__ __launch_bounds__(kThreads) void combine_backward_kernel(MoveArgs a) {
   constexpr int ES = fmt_bytes(FMT), N = 16 / ES;
   __shared__ float part[kThreads / 64][JB];
@@ -236,13 +258,13 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(MoveArgs a) 
         for (int j = 0; j < JB; ++j) {
           if (slot[j] < 0) continue;
           Vec<FMT> v, d;
-          v.unpack(*(const Raw16 *)((const char *)a.S + slot[j] * a.lds * ES + c * 16));
+          v.unpack(load_vec<ONCE>((const char *)a.S + slot[j] * a.lds * ES + c * 16));
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             dot[j] = fmaf(g.v[i], v.v[i], dot[j]);
             d.v[i] = w[j] * g.v[i];
           }
-          *(Raw16 *)((char *)a.Y + slot[j] * a.ldy * ES + c * 16) = d.pack();
+          store_vec<ONCE>((char *)a.Y + slot[j] * a.ldy * ES + c * 16, d.pack());
         }
       } else {
         for (int64_t i = whole * N; i < a.hidden; ++i) {
@@ -292,6 +314,15 @@ hipError_t over_tokens(const MoveArgs &a, int rows_per_block, F &&launch) {
 
 constexpr int kU = 2;  // chunks per thread
 
+// Slab rows of more bytes than the caches keep from their producer are read and
+// written non-temporally: 8192 x 2 rows of 4096 bf16 (134 MB) combine 35.3 us
+// against 40.3, gradients 59.6 against 68.1; 16384 x 2 rows of 512 (34 MB) 12.7
+// against 10.4.
+template <int FMT>
+bool past_caches(const MoveArgs &a) {
+  return (double)a.tokens * a.topk * a.hidden * fmt_bytes(FMT) > 64e6;
+}
+
 template <int FMT, int TPR>
 hipError_t rows_t(MoveArgs a, bool combine, hipStream_t stream) {
   const int64_t chunks = (a.hidden * fmt_bytes(FMT) + 15) / 16;
@@ -299,7 +330,10 @@ hipError_t rows_t(MoveArgs a, bool combine, hipStream_t stream) {
   return over_tokens(a, kThreads / TPR, [&](const MoveArgs &b, unsigned grid) {
     if constexpr (FMT != FMT_I8) {
       if (combine) {
-        hipLaunchKernelGGL((combine_kernel<FMT, TPR, kU>), dim3(grid), dim3(kThreads), 0, stream, b);
+        if (past_caches<FMT>(b))
+          hipLaunchKernelGGL((combine_kernel<FMT, TPR, kU, true>), dim3(grid), dim3(kThreads), 0, stream, b);
+        else
+          hipLaunchKernelGGL((combine_kernel<FMT, TPR, kU, false>), dim3(grid), dim3(kThreads), 0, stream, b);
         return;
       }
     }
@@ -328,13 +362,24 @@ hipError_t rows_any(const MoveArgs &a, bool combine, hipStream_t stream) {
   }
 }
 
-template <int FMT>
-hipError_t backward_fmt(MoveArgs a, hipStream_t stream) {
+template <int FMT, int TPR>
+hipError_t backward_t(MoveArgs a, hipStream_t stream) {
   constexpr int JB = 4;
   a.segs = 1;
-  return over_tokens(a, 1, [&](const MoveArgs &b, unsigned grid) {
-    hipLaunchKernelGGL((combine_backward_kernel<FMT, 256, JB>), dim3(grid), dim3(kThreads), 0, stream, b);
+  return over_tokens(a, kThreads / TPR, [&](const MoveArgs &b, unsigned grid) {
+    if (past_caches<FMT>(b))
+      hipLaunchKernelGGL((combine_backward_kernel<FMT, TPR, JB, true>), dim3(grid), dim3(kThreads), 0, stream, b);
+    else
+      hipLaunchKernelGGL((combine_backward_kernel<FMT, TPR, JB, false>), dim3(grid), dim3(kThreads), 0, stream, b);
   });
+}
+
+template <int FMT>
+hipError_t backward_fmt(const MoveArgs &a, hipStream_t stream) {
+  const int64_t chunks = (a.hidden * fmt_bytes(FMT) + 15) / 16;
+  // a wave per token for short rows (16384 x 2 rows of 64 chunks: 18.4 us against 48.0 on a workgroup each), a
+  // workgroup for long ones (8192 x 2 rows of 512 chunks: 59.5 us against 82.4 on a wave)
+  return chunks <= 128 ? backward_t<FMT, 64>(a, stream) : backward_t<FMT, 256>(a, stream);
 }
 
 }  // namespace

@@ -75,7 +75,7 @@ int64_t moe_sort_workspace_bytes(int64_t tokens, int64_t topk, int64_t experts) 
       experts > tsm::SortInfo::kMaxExperts)
     return 0;
   const int64_t blocks = tsm::sort_blocks(n);
-  return blocks > 1 ? blocks * experts * 4 : 0;
+  return blocks > 1 ? blocks * tsm::sort_pitch(experts) * 4 : 0;
 }
 
 int moe_sort(int64_t tokens, int64_t topk, const void *ids, int64_t ld_ids, int idtype, int64_t experts,
@@ -105,7 +105,8 @@ int moe_sort(int64_t tokens, int64_t topk, const void *ids, int64_t ld_ids, int 
   }
   const int64_t need = moe_sort_workspace_bytes(tokens, topk, experts);
   if (need) {
-    if ((st = array_check("workspace", workspace)) != TSM_SUCCESS) return st;
+    if (!workspace) return fail(TSM_ERROR_INVALID_VALUE, "workspace is NULL");
+    if ((uintptr_t)workspace & 15) return fail(TSM_ERROR_INVALID_VALUE, "workspace not 16-byte aligned");
     if (workspace_bytes < need)
       return fail(TSM_ERROR_INVALID_VALUE, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,
                   (long long)need);

@@ -14,7 +14,7 @@ struct SortArgs {
   bool id64;
   int32_t *positions;  // [tokens][topk]
   int32_t *counts;     // [experts]
-  int32_t *hist;       // [blocks][experts] (null: one block)
+  int32_t *hist;       // [blocks][sort_pitch(experts)], 16-byte aligned (null: one block)
 };
 struct SortInfo {
   static constexpr int kMaxExperts = 512;
@@ -22,6 +22,7 @@ struct SortInfo {
   static constexpr int64_t kTile = 4096;      // entries per workgroup otherwise
 };
 inline int64_t sort_blocks(int64_t n) { return n <= SortInfo::kOneBlock ? 1 : (n + SortInfo::kTile - 1) / SortInfo::kTile; }
+__host__ __device__ inline int64_t sort_pitch(int64_t experts) { return (experts + 3) / 4 * 4; }
 hipError_t launch_sort(const SortArgs &a, hipStream_t stream);
 
 // Rows between a token-major matrix and the experts' slabs.
