@@ -418,8 +418,8 @@ int moe_dispatch(int64_t tokens, int64_t topk, int64_t hidden, const void *X, in
 
 /*
  * moe_combine -- Y[t] := sum_j weights[t*topk + j] * slabs[positions[t*topk + j]],
- * over the entries with a position (no others are read, so a NaN weight or
- * stale slab row of one without a position does not matter); float32 sums in
+ * over the entries with a position (no others count: a NaN weight of one without
+ * a position or a stale slab row does not matter); float32 sums in
  * the order of j, rounded once.  weights NULL means ones.  A token without any
  * gets zeros.  dtype (slabs and Y): TSM_F32, TSM_F16 or TSM_BF16.
  */

@@ -264,6 +264,20 @@ def test_positions_outside_the_slabs_are_ignored():
     assert (dw[2] == 0).all() and dw[0, 1] == 0 and dw[1, 0] == 0
 
 
+def test_without_slab_rows():
+    import torch
+
+    say("[gpu] no slab rows")
+    pos = torch.tensor([[0, 3], [1, -1]], dtype=torch.int32, device="cuda")
+    empty = torch.empty((0, 40), device="cuda")
+    assert (tsm.combine_tokens(empty, pos, torch.ones((2, 2), device="cuda")) == 0).all()
+    ds, dw = tsm.combine_tokens_backward(torch.ones((2, 40), device="cuda"), empty, pos)
+    assert ds.shape == (0, 40) and (dw == 0).all()
+    assert tsm.dispatch_tokens(torch.ones((2, 40), device="cuda"), pos, slots=0).shape == (0, 40)
+    none = torch.empty((3, 0), dtype=torch.int32, device="cuda")
+    assert (tsm.combine_tokens(torch.ones((4, 40), device="cuda"), none) == 0).all()
+
+
 def layer(x, ids, w, up, down, E, cap):
     """A 16-bit expert layer: sort, dispatch, two grouped products, combine."""
     import torch

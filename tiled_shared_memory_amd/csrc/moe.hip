@@ -142,10 +142,21 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
 // ---- rows --------------------------------------------------------------------
 constexpr int kThreads = 256;
 
-// Slab row of entry i, or -1.  Rows past the slabs count as none, so no position can write outside them.
-__device__ __forceinline__ int64_t slot_of(const MoveArgs &a, int64_t i) {
-  const int32_t p = a.positions[i];
-  return p >= 0 && p < a.slots ? p : -1;
+// Slab rows of choices j0 .. j0 + J - 1 of a token, their positions requested together (one after the other they
+// would cost a memory latency each).  -1: none, past topk, or outside the slabs, so no position can reach outside them.
+constexpr int kAhead = 4;
+template <int J>
+__device__ __forceinline__ void slots_of(const MoveArgs &a, int64_t t, int j0, int64_t (&slot)[J]) {
+  int32_t p[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) p[j] = a.positions[t * a.topk + min(j0 + j, a.topk - 1)];
+#pragma unroll
+  for (int j = 0; j < J; ++j) slot[j] = j0 + j < a.topk && p[j] >= 0 && p[j] < a.slots ? p[j] : -1;
+}
+template <int J>
+__device__ __forceinline__ void weights_of(const MoveArgs &a, int64_t t, int j0, float (&w)[J]) {
+#pragma unroll
+  for (int j = 0; j < J; ++j) w[j] = a.weights ? a.weights[t * a.topk + min(j0 + j, a.topk - 1)] : 1.f;
 }
 
 // Thread tid's place: token t and its first chunk, TPR threads to a row, U chunks to a thread TPR apart.
@@ -168,23 +179,29 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(MoveArgs a) {
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (c0 + u * TPR < whole) v[u] = load_once(x + (c0 + u * TPR) * 16);
-  for (int j = 0; j < a.topk; ++j) {
-    const int64_t s = slot_of(a, t * a.topk + j);
-    if (s < 0) continue;
-    char *y = (char *)a.Y + s * a.ldy * ES;
+  for (int j0 = 0; j0 < a.topk; j0 += kAhead) {
+    int64_t slot[kAhead];
+    slots_of(a, t, j0, slot);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = c0 + u * TPR;
-      if (c < whole)
-        store_once(y + c * 16, v[u]);
-      else if (c < chunks)
-        for (int64_t i = whole * N; i < a.hidden; ++i) put_bits<FMT>(y, i, elem_bits<FMT>(x, i));
+    for (int j = 0; j < kAhead; ++j) {
+      if (slot[j] < 0) continue;
+      char *y = (char *)a.Y + slot[j] * a.ldy * ES;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t c = c0 + u * TPR;
+        if (c < whole)
+          store_once(y + c * 16, v[u]);
+        else if (c < chunks)
+          for (int64_t i = whole * N; i < a.hidden; ++i) put_bits<FMT>(y, i, elem_bits<FMT>(x, i));
+      }
+      if (a.scale && c0 == 0) a.slab_scale[slot[j]] = a.scale[t];
     }
-    if (a.scale && c0 == 0) a.slab_scale[s] = a.scale[t];
   }
 }
 
-template <int FMT, int TPR, int U, bool ONCE>
+// J choices at a time: their rows are requested together, choices without one reading row 0 (the host launches no
+// choices when there are no slabs), whose values are not used.
+template <int FMT, int TPR, int U, bool ONCE, int J>
 __global__ __launch_bounds__(kThreads) void combine_kernel(MoveArgs a) {
   constexpr int ES = fmt_bytes(FMT), N = 16 / ES;
   int64_t t, c0;
@@ -193,23 +210,36 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(MoveArgs a) {
   const int64_t chunks = (a.hidden + N - 1) / N, whole = a.hidden / N;
   char *y = (char *)a.Y + t * a.ldy * ES;
   float acc[U][N] = {};
-  for (int j = 0; j < a.topk; ++j) {
-    const int64_t s = slot_of(a, t * a.topk + j);
-    if (s < 0) continue;
-    const float w = a.weights ? a.weights[t * a.topk + j] : 1.f;
-    const char *x = (const char *)a.X + s * a.ldx * ES;
+  for (int j0 = 0; j0 < a.topk; j0 += J) {
+    int64_t slot[J];
+    float w[J];
+    slots_of(a, t, j0, slot);
+    weights_of(a, t, j0, w);
+    Raw16 r[U][J];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (c0 + u * TPR < whole)
+          r[u][j] = load_vec<ONCE>((const char *)a.X + (slot[j] < 0 ? 0 : slot[j]) * a.ldx * ES + (c0 + u * TPR) * 16);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t c = c0 + u * TPR;
-      if (c < whole) {
-        Vec<FMT> v;
-        v.unpack(load_vec<ONCE>(x + c * 16));
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[u][i] = fmaf(w, v.v[i], acc[u][i]);
-      } else if (c < chunks) {
+      for (int j = 0; j < J; ++j) {
+        if (slot[j] < 0) continue;
+        if (c < whole) {
+          Vec<FMT> v;
+          v.unpack(r[u][j]);
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (whole * N + i < a.hidden) acc[u][i] = fmaf(w, elem_f32<FMT>(elem_bits<FMT>(x, whole * N + i)), acc[u][i]);
+          for (int i = 0; i < N; ++i) acc[u][i] = fmaf(w[j], v.v[i], acc[u][i]);
+        } else if (c < chunks) {
+          const char *x = (const char *)a.X + slot[j] * a.ldx * ES;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (whole * N + i < a.hidden)
+              acc[u][i] = fmaf(w[j], elem_f32<FMT>(elem_bits<FMT>(x, whole * N + i)), acc[u][i]);
+        }
       }
     }
   }
@@ -243,22 +273,23 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(MoveArgs a) 
   for (int j0 = 0; j0 < a.topk; j0 += JB) {
     int64_t slot[JB];
     float w[JB], dot[JB];
+    slots_of(a, t, j0, slot);
+    weights_of(a, t, j0, w);
 #pragma unroll
-    for (int j = 0; j < JB; ++j) {
-      const bool in = j0 + j < a.topk;
-      slot[j] = in ? slot_of(a, t * a.topk + j0 + j) : -1;
-      w[j] = in && a.weights ? a.weights[t * a.topk + j0 + j] : 1.f;
-      dot[j] = 0.f;
-    }
+    for (int j = 0; j < JB; ++j) dot[j] = 0.f;
     for (int64_t c = lane; c < chunks; c += TPR) {
       if (c < whole) {
         Vec<FMT> g;
         g.unpack(*(const Raw16 *)(dy + c * 16));
+        Raw16 r[JB];  // (row 0 for a choice without one, not used: hidden is 0 when there are no slabs)
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+          r[j] = load_vec<ONCE>((const char *)a.S + (slot[j] < 0 ? 0 : slot[j]) * a.lds * ES + c * 16);
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
           if (slot[j] < 0) continue;
           Vec<FMT> v, d;
-          v.unpack(load_vec<ONCE>((const char *)a.S + slot[j] * a.lds * ES + c * 16));
+          v.unpack(r[j]);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             dot[j] = fmaf(g.v[i], v.v[i], dot[j]);
@@ -330,10 +361,15 @@ hipError_t rows_t(MoveArgs a, bool combine, hipStream_t stream) {
   return over_tokens(a, kThreads / TPR, [&](const MoveArgs &b, unsigned grid) {
     if constexpr (FMT != FMT_I8) {
       if (combine) {
-        if (past_caches<FMT>(b))
-          hipLaunchKernelGGL((combine_kernel<FMT, TPR, kU, true>), dim3(grid), dim3(kThreads), 0, stream, b);
+        const bool once = past_caches<FMT>(b);
+        if (b.topk <= 2 && once)
+          hipLaunchKernelGGL((combine_kernel<FMT, TPR, kU, true, 2>), dim3(grid), dim3(kThreads), 0, stream, b);
+        else if (b.topk <= 2)
+          hipLaunchKernelGGL((combine_kernel<FMT, TPR, kU, false, 2>), dim3(grid), dim3(kThreads), 0, stream, b);
+        else if (once)
+          hipLaunchKernelGGL((combine_kernel<FMT, TPR, kU, true, 4>), dim3(grid), dim3(kThreads), 0, stream, b);
         else
-          hipLaunchKernelGGL((combine_kernel<FMT, TPR, kU, false>), dim3(grid), dim3(kThreads), 0, stream, b);
+          hipLaunchKernelGGL((combine_kernel<FMT, TPR, kU, false, 4>), dim3(grid), dim3(kThreads), 0, stream, b);
         return;
       }
     }
@@ -362,9 +398,8 @@ hipError_t rows_any(const MoveArgs &a, bool combine, hipStream_t stream) {
   }
 }
 
-template <int FMT, int TPR>
-hipError_t backward_t(MoveArgs a, hipStream_t stream) {
-  constexpr int JB = 4;
+template <int FMT, int TPR, int JB>
+hipError_t backward_j(MoveArgs a, hipStream_t stream) {
   a.segs = 1;
   return over_tokens(a, kThreads / TPR, [&](const MoveArgs &b, unsigned grid) {
     if (past_caches<FMT>(b))
@@ -372,6 +407,11 @@ hipError_t backward_t(MoveArgs a, hipStream_t stream) {
     else
       hipLaunchKernelGGL((combine_backward_kernel<FMT, TPR, JB, false>), dim3(grid), dim3(kThreads), 0, stream, b);
   });
+}
+
+template <int FMT, int TPR>
+hipError_t backward_t(const MoveArgs &a, hipStream_t stream) {
+  return a.topk <= 2 ? backward_j<FMT, TPR, 2>(a, stream) : backward_j<FMT, TPR, 4>(a, stream);
 }
 
 template <int FMT>

@@ -186,7 +186,7 @@ int moe_combine(int64_t tokens, int64_t topk, int64_t hidden, const void *slabs,
   a.tokens = tokens;
   a.hidden = hidden;
   a.slots = slots;
-  a.topk = (int32_t)topk;
+  a.topk = slots ? (int32_t)topk : 0;  // no slabs: zeros
   a.fmt = dtype;
   a.positions = positions;
   a.weights = weights;
