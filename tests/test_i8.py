@@ -216,6 +216,22 @@ def test_extreme_codes_are_exact(shape):
     assert (c == float(np.float32(K * 16384))).all()
 
 
+@pytest.mark.parametrize("M", [3, 20, 70, 2600])
+def test_weights_past_4_gib(M):
+    """A weight of 4.9e9 bytes: its last columns."""
+    import torch
+
+    N, K = (37600, 131056) if M < 100 else (37632, 130944)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    b = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    a = torch.randint(-128, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    sa, sb = scales(M, g), scales(N, g)
+    say(f"[gpu] i8 weights past 4 GiB, {M} rows")
+    c = tsm.matmul_i8(a, sa, b.t(), sb)
+    for lo in (0, N - 100):
+        check(c[:, lo:lo + 100], reference(a, sa, b[lo:lo + 100], sb[lo:lo + 100]), "f32")
+
+
 def test_zero_k_and_scales_of_nan():
     import torch
 

@@ -124,7 +124,7 @@ def dispatch(**kw):
     (dict(pos=P0 + 2), 1, "positions not"), (dict(scale=S0), 1, "come together"), (dict(ss=S0), 1, "come together"),
     (dict(scale=S0 + 1, ss=W0), 1, "scale not"), (dict(slabs=A0 + 64), 1, "slabs overlaps X"),
     (dict(slabs=P0), 1, "slabs overlaps positions"), (dict(scale=S0, ss=B0 + 4), 1, "slab_scale overlaps slabs"),
-    (dict(T=(1 << 31) - 1, ldx=1 << 40), 2, "overflows")])
+    (dict(T=(1 << 31) - 1, k=1, ldx=1 << 40), 2, "overflows"), (dict(T=1 << 30), 2, "2^31")])
 def test_dispatch_refusals(kw, status, needle):
     refused(dispatch, kw, status, needle)
 

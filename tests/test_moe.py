@@ -29,6 +29,13 @@ def plain_sort(ids, experts, capacity):
     T, k = ids.shape
     pos = np.full((T, k), -1, np.int32)
     counts = np.zeros(experts, np.int32)
+    if T * k > 100000:  # the same, expert by expert
+        flat, out = ids.reshape(-1), pos.reshape(-1)
+        for e in range(experts):
+            at = np.flatnonzero(flat == e)
+            counts[e] = at.size
+            out[at[:capacity]] = e * capacity + np.arange(min(at.size, capacity))
+        return pos, counts
     for t in range(T):
         for j in range(k):
             e = int(ids[t, j])
@@ -40,7 +47,8 @@ def plain_sort(ids, experts, capacity):
 
 
 SORTS = [(0, 3, 4, 5), (5, 0, 4, 5), (1, 1, 1, 1), (1, 8, 8, 1), (64, 8, 256, 64), (1000, 2, 8, 300), (1024, 8, 512, 40),
-         (1025, 8, 60, 150), (4096, 2, 3, 5000), (4097, 2, 500, 7), (20000, 3, 16, 4000), (9000, 1, 1, 9000)]
+         (1025, 8, 60, 150), (4096, 2, 3, 5000), (4097, 2, 500, 7), (20000, 3, 16, 4000), (9000, 1, 1, 9000),
+         (140000, 8, 37, 30000), (2100000, 2, 5, 900000)]
 
 
 @pytest.mark.parametrize("T,k,E,cap", SORTS)
@@ -262,6 +270,48 @@ def test_positions_outside_the_slabs_are_ignored():
     ds, dw = tsm.combine_tokens_backward(x, s, pos)
     assert [float(v) for v in ds[:, 0]] == [1.0, 0.0, 0.0, 2.0]
     assert (dw[2] == 0).all() and dw[0, 1] == 0 and dw[1, 0] == 0
+
+
+def test_scales_without_elements():
+    import torch
+
+    say("[gpu] dispatch of scales alone")
+    pos = torch.tensor([[2, 0], [-1, 1]], dtype=torch.int32, device="cuda")
+    s = torch.tensor([5.0, 7.0], device="cuda")
+    _, ss = tsm.dispatch_tokens(torch.empty((2, 0), device="cuda"), pos, slots=3, scale=s)
+    assert ss.tolist() == [5.0, 7.0, 5.0]
+
+
+def test_slabs_past_4_gib():
+    """Slab rows whose byte offsets pass 2^32."""
+    import torch
+
+    rows, H = 300000, 8192
+    say("[gpu] slabs past 4 GiB")
+    slabs = torch.zeros((rows, H), dtype=torch.bfloat16, device="cuda")
+    x = torch.randn((4, H), device="cuda").to(torch.bfloat16)
+    pos = torch.tensor([[rows - 1], [0], [262144], [262143]], dtype=torch.int32, device="cuda")
+    tsm.dispatch_tokens(x, pos, out=slabs)
+    assert torch.equal(slabs[pos[:, 0].long()], x) and int((slabs != 0).any(1).sum()) == 4
+    assert torch.equal(tsm.combine_tokens(slabs, pos), x)
+    ds, dw = tsm.combine_tokens_backward(x, slabs, pos, out=torch.zeros_like(slabs))
+    assert torch.equal(ds, slabs)
+    assert torch.allclose(dw[:, 0].double(), (x.double() ** 2).sum(1), rtol=(H + 8) * 2.0 ** -24, atol=0)
+
+
+def test_other_stream_needs_its_workspace():
+    import torch
+
+    ids = torch.zeros((5000, 2), dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    with pytest.raises(tsm.TsmError):
+        tsm.sort_tokens(ids, 4, 10000, stream=side)
+    say("[gpu] sort on a stream of its own")
+    ws = tsm.sort_workspace_for(ids, 4)
+    torch.cuda.synchronize()
+    pos, counts = tsm.sort_tokens(ids, 4, 10000, workspace=ws, stream=side)
+    side.synchronize()
+    assert counts.tolist() == [10000, 0, 0, 0] and torch.equal(pos.view(-1).cpu(), torch.arange(10000, dtype=torch.int32))
 
 
 def test_without_slab_rows():

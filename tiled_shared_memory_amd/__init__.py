@@ -288,7 +288,8 @@ def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspac
     (experts * capacity rows, expert e's from e * capacity), in token order, -1 for an id outside [0, experts) or past
     the capacity; and how many choices each expert got (int32, those past the capacity among them).
 
-    A workspace (see ``sort_workspace_for``) is allocated when the sizes need one and none is given.
+    A workspace (see ``sort_workspace_for``) is allocated when the sizes need one and none is given, for calls on the
+    current stream.
     """
     if ids.dim() != 2:
         _bad("ids must be 2-D")
@@ -303,6 +304,9 @@ def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspac
     _packed("counts", counts)
     if workspace is None:
         workspace = sort_workspace_for(ids, experts)
+        if workspace is not None and stream is not None:
+            # memory of the current stream, which would take it back before the other stream is done with it
+            _bad("a call on a stream of its own needs its workspace (see sort_workspace_for)")
     if workspace is not None:
         if not workspace.is_cuda:
             _bad("workspace is not on a GPU")

@@ -326,7 +326,8 @@ hipError_t stream_t(I8Args a, hipStream_t st) {
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   // what 256 CUs of 160 KiB hold at once; the rest of the tiles follow in the same workgroups
   const int64_t resident = 256 * (163840 / LDS);
-  const int64_t most = a.rows ? (kMaxGroups < 0x7fffffffLL / tiles ? kMaxGroups : 0x7fffffffLL / tiles) : 0x7fffffffLL / tiles;
+  int64_t most = 0x3fffffff / tiles;  // problems per launch: tile numbers stay far below 2^31
+  if (a.rows && most > kMaxGroups) most = kMaxGroups;
   for (int64_t z0 = 0; z0 < a.batch; z0 += most) {
     a.z0 = z0;
     a.nz = (int32_t)(a.batch - z0 < most ? a.batch - z0 : most);
@@ -361,7 +362,8 @@ hipError_t stream_t(I8Args a, hipStream_t st) {
 //    32 (256 groups of 1024 x 2048, 16 rows each of 64: 112 us against 137).
 I8Skinny i8_skinny_plan(const I8Args &p) {
   I8Skinny s;
-  if (p.M > 64 || p.K == 0) return s;
+  // (more columns than workgroups of 256 fit a launch go to the general kernel)
+  if (p.M > 64 || p.K == 0 || p.N > 0xffffffffLL / 256 * 16) return s;
   const bool aligned = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && p.K % 16 == 0 && p.lda % 16 == 0 &&
                        p.ldb % 16 == 0 && p.strideA % 16 == 0 && p.strideB % 16 == 0;
   // 32-bit offsets over a block's rows

@@ -49,6 +49,35 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
   for (int e = threadIdx.x; e < a.experts; e += kSortThreads) a.hist[(int64_t)blockIdx.x * sort_pitch(a.experts) + e] = sh[e];
 }
 
+// Many tiles: every tile's counts to the sums of the tiles before it, a workgroup per expert.
+__global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(int32_t *hist, int64_t pitch, int blocks) {
+  __shared__ int32_t wsum[kSortWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int32_t *col = hist + blockIdx.x;
+  int32_t before = 0;
+  for (int b0 = 0; b0 < blocks; b0 += kSortThreads) {
+    const int b = b0 + (int)threadIdx.x;
+    const int32_t v = b < blocks ? col[b * pitch] : 0;
+    int32_t s = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t o = __shfl_up(s, d, 64);
+      if (lane >= d) s += o;
+    }
+    if (lane == 63) wsum[wave] = s;
+    __syncthreads();
+    int32_t earlier = before, all = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      if (w < wave) earlier += wsum[w];
+      all += wsum[w];
+    }
+    if (b < blocks) col[b * pitch] = earlier + s - v;
+    before += all;
+    __syncthreads();  // the waves' sums are read
+  }
+}
+
 // Positions of one tile's entries.  Each wave owns a run of consecutive
 // entries; LDS holds, per wave and expert, first the wave's count, then the
 // next rank it gives out.
@@ -76,7 +105,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
 #pragma unroll
   for (int s = 0; s < S; ++s)
     if (own[s] >= 0) atomicAdd(&sh[wave * E + own[s]], 1);
-  if (a.hist) {
+  if (a.scanned) {
+    for (int e = threadIdx.x; e < E; e += kSortThreads) before[e] = a.hist[(int64_t)blockIdx.x * sort_pitch(E) + e];
+  } else if (a.hist) {
     // entries of the tiles before: a thread adds up 4 experts over every (1024 / (E / 4))-th tile, eight loads at a time
     // (past the tiles before this one its last again, not counted; a loop of single loads waits for each)
     const int E4 = (int)sort_pitch(E) / 4, per = kSortThreads / E4, g = threadIdx.x / E4, e4 = threadIdx.x % E4;
@@ -358,6 +389,7 @@ template <int FMT, int TPR>
 hipError_t rows_t(MoveArgs a, bool combine, hipStream_t stream) {
   const int64_t chunks = (a.hidden * fmt_bytes(FMT) + 15) / 16;
   a.segs = (int32_t)((chunks + TPR * kU - 1) / (TPR * kU));
+  if (a.segs < 1) a.segs = 1;  // (rows of no elements may still have scales)
   return over_tokens(a, kThreads / TPR, [&](const MoveArgs &b, unsigned grid) {
     if constexpr (FMT != FMT_I8) {
       if (combine) {
@@ -424,7 +456,8 @@ hipError_t backward_fmt(const MoveArgs &a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_sort(const SortArgs &a, hipStream_t stream) {
+hipError_t launch_sort(const SortArgs &args, hipStream_t stream) {
+  SortArgs a = args;
   const int64_t blocks = sort_blocks(a.tokens * a.topk);
   const size_t lds = (size_t)(kSortWaves + 1) * a.experts * 4;
   if (blocks > 1) {
@@ -432,8 +465,16 @@ hipError_t launch_sort(const SortArgs &a, hipStream_t stream) {
       hipLaunchKernelGGL(sort_count_kernel<true>, dim3((unsigned)blocks), dim3(kSortThreads), (size_t)a.experts * 4, stream, a);
     else
       hipLaunchKernelGGL(sort_count_kernel<false>, dim3((unsigned)blocks), dim3(kSortThreads), (size_t)a.experts * 4, stream, a);
-    const hipError_t e = hipGetLastError();
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    // every tile adding up all tiles before it reads their square: a launch of its own from kScanBlocks tiles
+    a.scanned = blocks > SortInfo::kScanBlocks;
+    if (a.scanned) {
+      hipLaunchKernelGGL(sort_scan_kernel, dim3((unsigned)a.experts), dim3(kSortThreads), 0, stream, a.hist,
+                         sort_pitch(a.experts), (int)blocks);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
   if (a.id64)
     hipLaunchKernelGGL(sort_place_kernel<true>, dim3((unsigned)blocks), dim3(kSortThreads), lds, stream, a);

@@ -56,6 +56,7 @@ int sizes_check(int64_t tokens, int64_t topk, int64_t hidden, int64_t slots, int
   if (tokens > 0x7fffffffLL || topk > 0x7fffffffLL || hidden > 0x7fffffffLL || slots > 0x7fffffffLL)
     return fail(TSM_ERROR_NOT_SUPPORTED, "a size exceeds 2^31-1");
   *entries = tokens * topk;  // below 2^62
+  if (*entries > 0x7fffffffLL) return fail(TSM_ERROR_NOT_SUPPORTED, "tokens * topk exceeds 2^31-1");
   return TSM_SUCCESS;
 }
 
@@ -118,7 +119,7 @@ int moe_sort(int64_t tokens, int64_t topk, const void *ids, int64_t ld_ids, int 
   if ((st = disjoint(out, in)) != TSM_SUCCESS) return st;
   if (n == 0 && experts == 0) return TSM_SUCCESS;
   const SortArgs a{ids,      tokens, topk ? ld_ids : 0, (int32_t)topk, (int32_t)experts, capacity, idtype == TSM_I64,
-                   positions, counts, need ? (int32_t *)workspace : nullptr};
+                   positions, counts, need ? (int32_t *)workspace : nullptr, false};
   return launched(launch_sort(a, (hipStream_t)stream));
 }
 

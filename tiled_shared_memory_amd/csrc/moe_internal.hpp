@@ -15,11 +15,13 @@ struct SortArgs {
   int32_t *positions;  // [tokens][topk]
   int32_t *counts;     // [experts]
   int32_t *hist;       // [blocks][sort_pitch(experts)], 16-byte aligned (null: one block)
+  bool scanned;        // hist holds sums of the blocks before (set by the launch)
 };
 struct SortInfo {
   static constexpr int kMaxExperts = 512;
   static constexpr int64_t kOneBlock = 8192;  // entries one workgroup sorts by itself
   static constexpr int64_t kTile = 4096;      // entries per workgroup otherwise
+  static constexpr int64_t kScanBlocks = 256; // workgroups from which their counts are summed in a launch of their own
 };
 inline int64_t sort_blocks(int64_t n) { return n <= SortInfo::kOneBlock ? 1 : (n + SortInfo::kTile - 1) / SortInfo::kTile; }
 __host__ __device__ inline int64_t sort_pitch(int64_t experts) { return (experts + 3) / 4 * 4; }
