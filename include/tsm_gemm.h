@@ -1,5 +1,6 @@
 /*
  * tsm_gemm.h -- C ABI of the MI355X (gfx950) blocked GEMM library.
+ * (The int8 products and the expert routing have a section of their own below.)
  *
  * The operation is the blocked matrix product C = A.B with 16-bit floating-point
  * operands (f16 or bf16), float32 accumulation and a float32 or f16 result.  It

@@ -7,7 +7,9 @@
 // (T/2 x T/2 each); a team multiplies one 64-deep half of every slab, and their
 // sums, which are exact, meet in LDS at the end.  Two waves per SIMD overlap one
 // team's LDS reads with the other's MFMAs where a grid of one workgroup per CU
-// would leave each SIMD a single wave (1024 x 4096 x 4096: 34.7 us with one team).
+// would leave each SIMD a single wave (1024 x 4096 x 4096: 29.1 us, 34.7 with one
+// team; 2048^3 17.3 us, 21.9).  Bound by the slabs' chain of LDS writes, barrier,
+// reads and MFMAs while a CU has one workgroup, by LDS bandwidth once it has two.
 //
 // Any sizes and any alignment: a thread's 16 codes come with one load at any
 // byte address; rows past M or N read the last row (their products are never

@@ -10,6 +10,13 @@
 //   dispatch  slab[pos[t][j]] = X[t]
 //   combine   Y[t] = sum_j w[t][j] slab[pos[t][j]]
 //   backward  dslab[pos[t][j]] = w[t][j] dY[t];  dw[t][j] = <dY[t], slab[pos[t][j]]>
+//
+// The row operators are bound by memory; a row moves as 16-byte vectors at any
+// alignment, a token's choices are requested together.  8192 tokens, 2 choices,
+// 4096 bf16: dispatch 33.9 us (5.9 TB/s), combine 32.6 us (6.2 TB/s), gradients
+// 52.2 us (6.4 TB/s); a large device copy reaches 5.0 TB/s.  Odd rows (4095
+// elements) cost a third more.  The sort is bound by latencies and launches: 64 x 8
+// entries 3.1 us in one workgroup, 65536 x 8 of 256 experts 3.3 + 9.4 us.
 #include "elems.hpp"
 #include "moe_internal.hpp"
 

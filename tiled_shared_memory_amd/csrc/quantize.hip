@@ -15,7 +15,8 @@
 // and half a maximum; the rare cases run under a branch per 8 elements.
 //
 // The row stays in registers, so it is read once: bound by memory (16384 rows of
-// 4096 bf16: see the time at quantize_fmt).
+// 4096 bf16 35 us = 5.7 TB/s, 8192 of 8192 32.5 us = 6.2 TB/s; with a division, a
+// rounding and a conversion per element and a workgroup per row 50 us).
 #include "elems.hpp"
 #include "i8_internal.hpp"
 
