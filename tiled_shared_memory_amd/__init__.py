@@ -13,7 +13,7 @@ from ._lib import (TSM_ACT_LEAKY_RELU, TSM_ACT_NONE, TSM_ACT_RELU, TSM_BF16, TSM
                    TSM_BF16_F16, TSM_BF16_F32, TSM_COL, TSM_ERROR_INVALID_VALUE, TSM_ERROR_LAUNCH,
                    TSM_ERROR_NOT_SUPPORTED, TSM_F16, TSM_F16_BF16, TSM_F16_F16, TSM_F16_F32, TSM_F32, TSM_I8, TSM_I32,
                    TSM_I64, TSM_ROW, TSM_ROWSUM_BF16, TSM_ROWSUM_F16, TSM_ROWSUM_F32, TSM_SUCCESS, TsmError,
-                   current_device, gemm, gemm_ex, gemm_grouped, gemm_i8, gemm_i8_grouped, gemm_i8_strided_batched,
+                   _check, _lookups, gemm, gemm_ex, gemm_grouped, gemm_i8, gemm_i8_grouped, gemm_i8_strided_batched,
                    gemm_noalloc_scratch_bytes, gemm_strided_batched, gemm_strided_batched_act, gemm_strided_batched_ex,
                    gemm_strided_batched_noalloc, gemm_strided_batched_ws, gemm_workspace_bytes, load, moe_combine,
                    moe_combine_backward, moe_dispatch, moe_sort, moe_sort_workspace_bytes, quantize_i8, rowsum,
@@ -112,25 +112,22 @@ def _bad(text):
     raise TsmError(TSM_ERROR_INVALID_VALUE, text)
 
 
-_FORMATS = None
+_FORMATS = {}
 
 
-def _format(t):
-    """The library's code of a tensor's dtype (TSM_F32 .. TSM_I64), or None."""
-    global _FORMATS
-    if _FORMATS is None:
+def _formats():
+    """The library's codes (TSM_F32 .. TSM_I64) by torch dtype."""
+    if not _FORMATS:
         import torch
 
-        _FORMATS = {torch.float32: TSM_F32, torch.float16: TSM_F16, torch.bfloat16: TSM_BF16, torch.int8: TSM_I8,
-                    torch.int32: TSM_I32, torch.int64: TSM_I64}
-    return _FORMATS.get(t.dtype)
+        _FORMATS.update({torch.float32: TSM_F32, torch.float16: TSM_F16, torch.bfloat16: TSM_BF16, torch.int8: TSM_I8,
+                         torch.int32: TSM_I32, torch.int64: TSM_I64})
+    return _FORMATS
 
 
 def _wants(what, t, formats, shape=None):
-    """Check a tensor argument: on a GPU, of one of the formats, of the shape.  Returns its format."""
-    if not t.is_cuda:
-        _bad(f"{what} is not on a GPU")
-    f = _format(t)
+    """Check a tensor argument: of one of the formats, of the shape.  Returns its format."""
+    f = (_FORMATS or _formats()).get(t.dtype)
     if f not in formats:
         _bad(f"{what} has dtype {t.dtype}")
     if shape is not None and t.shape != shape:
@@ -160,30 +157,35 @@ def _new(like, shape, dtype, fill=None):
     return (torch.empty if fill is None else torch.zeros)(shape, dtype=dtype, device=like.device)
 
 
-class _Here:
-    """The guard of a call whose tensors are on the current GPU: none."""
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
-_HERE = _Here()
-
-
-def _gpu_of(first, *others):
-    """Check that every tensor is on the GPU of the first; a guard that makes it the current one for the launch."""
-    d = first.get_device()
-    for t in others:
+def _launch(call, stream, tensors, args):
+    """call(*args, stream) through the C interface, the GPU of the tensors (None among them: not given) current: they
+    must all be on one.  Without a stream, its current one.  A small operator's time is this path (3.9 us are the
+    launch itself), so it goes to the library without the checks and conversions of the functions in _lib."""
+    d = tensors[0].get_device()
+    if d < 0:
+        _bad("tensors must be on a GPU (the first is not on a GPU)")
+    for t in tensors:
         if t is not None and t.get_device() != d:
-            _bad(f"tensors on {first.device} and {t.device}")
-    if d == current_device():
-        return _HERE
-    import torch
+            _bad(f"tensors on {tensors[0].device} and {t.device}")
+    lib = load()
+    device, current_stream = _lookups()
+    if stream is None:
+        stream = current_stream(d)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if d == device():
+        status = getattr(lib, call)(*args, stream)
+    else:
+        import torch
 
-    return torch.cuda.device(d)
+        with torch.cuda.device(d):
+            status = getattr(lib, call)(*args, stream)
+    if status:
+        _check(lib, status)
 
 
 _FLOATS = (TSM_F32, TSM_F16, TSM_BF16)
@@ -213,8 +215,9 @@ def quantize(x, *, rows=None, out=None, scale=None, stream=None):
         _bad("scale: rows must be contiguous")
     ldx, ldq = _rows_ld("x", x), _rows_ld("out", out)
     sx, sq, ss = (x.stride(0), out.stride(0), scale.stride(0)) if x.dim() == 3 else (0, 0, 0)
-    with _gpu_of(x, out, scale, rows):
-        quantize_i8(x.shape[-2], x.shape[-1], x, ldx, sx, f, out, ldq, sq, scale, ss, rows, G, stream)
+    _launch("quantize_i8", stream, (x, out, scale, rows),
+            (x.shape[-2], x.shape[-1], x.data_ptr(), ldx, sx, f, out.data_ptr(), ldq, sq, scale.data_ptr(), ss,
+             _at(rows), G))
     return out, scale
 
 
@@ -265,15 +268,15 @@ def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, ac
     sc = out.stride(0) if batched else 0
     act = _ACTIVATIONS[activation]
     if rows is None:
-        with _gpu_of(a, b, out, scale_a, scale_b):
-            gemm_i8_strided_batched(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb, out, ldc, sc, batch, f,
-                                    act, slope, stream)
+        _launch("gemm_i8_strided_batched", stream, (a, b, out, scale_a, scale_b),
+                (M, N, K, a.data_ptr(), lda, sa, _at(scale_a), ssa, b.data_ptr(), ldb, sb, _at(scale_b), ssb,
+                 out.data_ptr(), ldc, sc, batch, f, act, slope))
     else:
         _wants("rows", rows, (TSM_I32,), (batch,))
         _packed("rows", rows)
-        with _gpu_of(a, b, out, scale_a, scale_b, rows):
-            gemm_i8_grouped(M, N, K, a, lda, sa, scale_a, ssa, b, ldb, sb, scale_b, ssb, out, ldc, sc, rows, batch, f,
-                            act, slope, stream)
+        _launch("gemm_i8_grouped", stream, (a, b, out, scale_a, scale_b, rows),
+                (M, N, K, a.data_ptr(), lda, sa, _at(scale_a), ssa, b.data_ptr(), ldb, sb, _at(scale_b), ssb,
+                 out.data_ptr(), ldc, sc, rows.data_ptr(), batch, f, act, slope))
     return out
 
 
@@ -307,14 +310,13 @@ def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspac
         if workspace is not None and stream is not None:
             # memory of the current stream, which would take it back before the other stream is done with it
             _bad("a call on a stream of its own needs its workspace (see sort_workspace_for)")
+    nbytes = 0
     if workspace is not None:
-        if not workspace.is_cuda:
-            _bad("workspace is not on a GPU")
         _packed("workspace", workspace)
-    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    with _gpu_of(ids, positions, counts, workspace):
-        moe_sort(ids.shape[0], ids.shape[1], ids, _rows_ld("ids", ids), f, experts, capacity, positions, counts,
-                 workspace, nbytes, stream)
+        nbytes = workspace.numel() * workspace.element_size()
+    _launch("moe_sort", stream, (ids, positions, counts, workspace),
+            (ids.shape[0], ids.shape[1], ids.data_ptr(), _rows_ld("ids", ids), f, experts, capacity,
+             positions.data_ptr(), counts.data_ptr(), _at(workspace), nbytes))
     return positions, counts
 
 
@@ -355,9 +357,9 @@ def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale
         _packed("out_scale", out_scale)
     elif out_scale is not None:
         _bad("out_scale without scale")
-    with _gpu_of(x, out, positions, scale, out_scale):
-        moe_dispatch(x.shape[0], positions.shape[1], x.shape[1], x, _rows_ld("x", x), f, scale, positions,
-                     out.shape[0], out, _rows_ld("out", out), out_scale, stream)
+    _launch("moe_dispatch", stream, (x, out, positions, scale, out_scale),
+            (x.shape[0], positions.shape[1], x.shape[1], x.data_ptr(), _rows_ld("x", x), f, _at(scale),
+             positions.data_ptr(), out.shape[0], out.data_ptr(), _rows_ld("out", out), _at(out_scale)))
     return out if scale is None else (out, out_scale)
 
 
@@ -373,9 +375,9 @@ def combine_tokens(slabs, positions, weights=None, *, out=None, stream=None):
     if weights is not None:
         _wants("weights", weights, (TSM_F32,), positions.shape)
         _packed("weights", weights)
-    with _gpu_of(slabs, out, positions, weights):
-        moe_combine(tokens, positions.shape[1], hidden, slabs, _rows_ld("slabs", slabs), slabs.shape[0], f,
-                    positions, weights, out, _rows_ld("out", out), stream)
+    _launch("moe_combine", stream, (slabs, out, positions, weights),
+            (tokens, positions.shape[1], hidden, slabs.data_ptr(), _rows_ld("slabs", slabs), slabs.shape[0], f,
+             positions.data_ptr(), _at(weights), out.data_ptr(), _rows_ld("out", out)))
     return out
 
 
@@ -403,8 +405,8 @@ def combine_tokens_backward(dy, slabs, positions, weights=None, *, out=None, dwe
     if weights is not None:
         _wants("weights", weights, (TSM_F32,), positions.shape)
         _packed("weights", weights)
-    with _gpu_of(dy, slabs, out, positions, weights, dweights):
-        moe_combine_backward(dy.shape[0], positions.shape[1], dy.shape[1], dy, _rows_ld("dy", dy), slabs,
-                             _rows_ld("slabs", slabs), slabs.shape[0], f, positions, weights, out, _rows_ld("out", out),
-                             dweights, stream)
+    _launch("moe_combine_backward", stream, (dy, slabs, out, positions, weights, dweights),
+            (dy.shape[0], positions.shape[1], dy.shape[1], dy.data_ptr(), _rows_ld("dy", dy), slabs.data_ptr(),
+             _rows_ld("slabs", slabs), slabs.shape[0], f, positions.data_ptr(), _at(weights), out.data_ptr(),
+             _rows_ld("out", out), dweights.data_ptr()))
     return out, dweights

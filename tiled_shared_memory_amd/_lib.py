@@ -144,13 +144,9 @@ def _lookups():
 
         torch.cuda.current_stream()  # initialises the device
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _LOOKUPS = (torch.cuda.current_device, raw or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+        _LOOKUPS = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                    raw or (lambda device: torch.cuda.current_stream(device).cuda_stream))
     return _LOOKUPS
-
-
-def current_device():
-    """Index of torch's current GPU."""
-    return _lookups()[0]()
 
 
 def _current_stream():
