@@ -1,15 +1,13 @@
 // Int8 products of few rows (decoding steps) for gfx950: bound by reading the
 // weights once.
 //
-// A workgroup owns 16 MB rows x 16 NB columns of C; its W waves share out K in
-// steps of 256 codes, and their int32 sums (exact, so the split does not show)
-// meet in LDS and leave once, scaled.  Two kernels:
+// A workgroup owns a block of C; its waves share out K in steps of 256 codes,
+// and their int32 sums (exact, so the split does not show) meet in LDS and leave
+// once, scaled.  Two kernels:
 //  * stream: each wave copies its steps into an LDS ring of its own and
 //    multiplies from there; for 16-byte aligned operands, K a multiple of 16.
-//  * skinny: operands straight into registers, at any alignment; also the
-//    faster one for up to 4 rows of K <= 4096, where a wave has few steps and a
-//    ring to fill first (4 x 28672 x 4096: 24.1 us against 25.8; 1 x 4096 x
-//    4096: 5.9 against 6.3; at K = 8192 1 x 16384: 33.6 against 25.2).
+//  * skinny: operands straight into registers, at any alignment.
+// i8_skinny_plan has the rule between them and the general kernel.
 // Measured on weights that no cache holds, launch included: 16 x 16384 x 8192
 // 27.3 us (5.0 TB/s), 1 x 8192 x 8192 15.0 us, 256 experts of 1024 x 2048 86 us
 // (6.2 TB/s).
@@ -22,66 +20,38 @@ namespace {
 constexpr int STEP = 256;
 
 // ---- any alignment: operands straight into registers --------------------------
-// Wave w takes steps w, w + W, ...; a wave-wide load covers 16 rows x 64 bytes,
-// the layout the matrix instruction wants, and a step's four loads per block
-// cover the lines whole.  D steps are in flight per wave.
-template <int N>
-struct Step {
-  u32x4 v[N][4];
-};
+// 16 rows x 16 columns on W waves; wave w takes steps w, w + W, ...  A wave-wide
+// load covers 16 rows x 64 bytes, the layout the matrix instruction wants, and a
+// step's four loads cover the lines whole.  D steps are in flight per wave.
+constexpr int kSkinnyWaves = 4;
 
-template <int MB, int NB, int W, int D, int FMT>
-__global__ __launch_bounds__(W * 64) void gemm_i8_skinny_kernel(I8Args p) {
-  __shared__ i32x4 part[W][MB * NB][64];
+template <int FMT>
+__global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_i8_skinny_kernel(I8Args p) {
+  constexpr int W = kSkinnyWaves, D = 4;
+  __shared__ i32x4 part[W][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int tm, tn;
   int64_t z;
-  if (!i8_tile_of<16 * MB>(p, 1, z, tm, tn)) return;  // uniform
-  const int64_t M = i8_rows(p, z), m0 = (int64_t)tm * (16 * MB), n0 = (int64_t)tn * (16 * NB);
-  const int mb = (int)(M - m0 >= 16 * MB ? MB : (M - m0 + 15) / 16);  // row blocks that hold rows
+  if (!i8_tile_of<16>(p, 1, z, tm, tn)) return;  // uniform
+  const int64_t M = i8_rows(p, z), m0 = (int64_t)tm * 16, n0 = (int64_t)tn * 16;
 
   // rows past M or N read the last one: their results are not stored
-  const int r = lane & 15, kc = (lane >> 4) * 16;
-  const int8_t *ap[MB], *bp[NB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int64_t m = m0 + 16 * i + r;
-    ap[i] = p.A + z * p.strideA + (m < M ? m : M - 1) * p.lda;
-  }
-#pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int64_t n = n0 + 16 * j + r;
-    bp[j] = p.B + z * p.strideB + (n < p.N ? n : p.N - 1) * p.ldb;
-  }
+  const int64_t mr = m0 + (lane & 15), nr = n0 + (lane & 15);
+  const int8_t *const ap = p.A + z * p.strideA + (mr < M ? mr : M - 1) * p.lda;
+  const int8_t *const bp = p.B + z * p.strideB + (nr < p.N ? nr : p.N - 1) * p.ldb;
+  const int kc = (lane >> 4) * 16;
 
-  i32x4 acc[MB][NB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{};
-
-  Step<MB> a[D];
-  Step<NB> b[D];
+  i32x4 acc{};
+  u32x4 a[D][4], b[D][4];
   const int whole = (int)(p.K / STEP);
   auto fetch = [&](int d, int s) {
     const int64_t k = (int64_t)s * STEP + kc;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-#pragma unroll
-      for (int j = 0; j < NB; ++j) b[d].v[j][u] = load16(bp[j] + k + 64 * u);
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-        if (i < mb) a[d].v[i][u] = load16(ap[i] + k + 64 * u);
-    }
+    for (int u = 0; u < 4; ++u) b[d][u] = load16(bp + k + 64 * u), a[d][u] = load16(ap + k + 64 * u);
   };
   auto mma = [&](int d) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-        if (i < mb)
-#pragma unroll
-          for (int j = 0; j < NB; ++j) acc[i][j] = mfma_i8(b[d].v[j][u], a[d].v[i][u], acc[i][j]);
+    for (int u = 0; u < 4; ++u) acc = mfma_i8(b[d][u], a[d][u], acc);
   };
 #pragma unroll
   for (int d = 0; d < D; ++d)
@@ -98,47 +68,34 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_skinny_kernel(I8Args p) {
   if ((int64_t)whole * STEP < p.K && wave == whole % W) {
     const int64_t k = (int64_t)whole * STEP + kc;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-#pragma unroll
-      for (int j = 0; j < NB; ++j) b[0].v[j][u] = load_tail(bp[j], k + 64 * u, p.K);
-#pragma unroll
-      for (int i = 0; i < MB; ++i) a[0].v[i][u] = load_tail(ap[i], k + 64 * u, p.K);
-    }
+    for (int u = 0; u < 4; ++u) b[0][u] = load_tail(bp, k + 64 * u, p.K), a[0][u] = load_tail(ap, k + 64 * u, p.K);
     mma(0);
   }
 
-#pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) part[wave][i * NB + j][lane] = acc[i][j];
+  part[wave][lane] = acc;
   __syncthreads();
-  const Epilogue ep{p.act, p.slope, false};
-  const float *sa = p.sa ? p.sa + z * p.stride_sa : nullptr;
-  for (int q = threadIdx.x; q < MB * NB * 64; q += W * 64) {
-    const int blk = q >> 6, l = q & 63;
-    const int64_t m = m0 + 16 * (blk / NB) + (l & 15), n = n0 + 16 * (blk % NB) + 4 * (l >> 4);
-    if (m >= M || n >= p.N) continue;
-    i32x4 sum = part[0][blk][l];
+  const int64_t m = m0 + (lane & 15), n = n0 + kc / 4;
+  if (wave != 0 || m >= M || n >= p.N) return;
+  i32x4 sum = part[0][lane];
 #pragma unroll
-    for (int w = 1; w < W; ++w) sum += part[w][blk][l];
-    float cb[4];
-    channel_scales(p, z, n, cb);
-    store_i8<FMT>(p, ep, (char *)p.C + (z * p.strideC + m * p.ldc) * fmt_bytes(FMT), n, sa ? sa[m] : 1.f, cb, sum);
-  }
+  for (int w = 1; w < W; ++w) sum += part[w][lane];
+  float cb[4];
+  channel_scales(p, z, n, cb);
+  store_i8<FMT>(p, Epilogue{p.act, p.slope, false}, (char *)p.C + (z * p.strideC + m * p.ldc) * fmt_bytes(FMT), n,
+                p.sa ? p.sa[z * p.stride_sa + m] : 1.f, cb, sum);
 }
 
-template <int MB, int NB, int W, int D>
 hipError_t skinny_t(const I8Args &p, hipStream_t stream) {
-  return over_tiles(p, 16 * MB, 16 * NB, W * 64, [&](const I8Args &a, dim3 grid) {
+  constexpr int T = kSkinnyWaves * 64;
+  return over_tiles(p, 16, 16, T, [&](const I8Args &a, dim3 grid) {
     if (a.fmt == FMT_F32)
-      hipLaunchKernelGGL((gemm_i8_skinny_kernel<MB, NB, W, D, FMT_F32>), grid, dim3(W * 64), 0, stream, a);
+      hipLaunchKernelGGL((gemm_i8_skinny_kernel<FMT_F32>), grid, dim3(T), 0, stream, a);
     else if (a.fmt == FMT_F16)
-      hipLaunchKernelGGL((gemm_i8_skinny_kernel<MB, NB, W, D, FMT_F16>), grid, dim3(W * 64), 0, stream, a);
+      hipLaunchKernelGGL((gemm_i8_skinny_kernel<FMT_F16>), grid, dim3(T), 0, stream, a);
     else
-      hipLaunchKernelGGL((gemm_i8_skinny_kernel<MB, NB, W, D, FMT_BF16>), grid, dim3(W * 64), 0, stream, a);
+      hipLaunchKernelGGL((gemm_i8_skinny_kernel<FMT_BF16>), grid, dim3(T), 0, stream, a);
   });
 }
-
 
 // ---- 16-byte aligned operands, K a multiple of 16 -----------------------------
 // Loading the operand layout straight from memory (above) touches 16 rows per
@@ -178,12 +135,12 @@ __device__ __forceinline__ Place stream_tile(const I8Args &p, int t, const int *
   return e;
 }
 
-template <int AR, int NB, int W, int S, int FMT>
+template <int AR, int NB, int W, int FMT>
 __device__ __forceinline__ void stream(const I8Args &p) {
   constexpr int MB = AR / 16;
   constexpr int LA = AR / 4, LB = 4 * NB, L = LA + LB;  // wave-loads (1 KiB: 4 rows) per step
   constexpr int BYTES = L * 1024;
-  __shared__ __attribute__((aligned(1024))) char s0[W * BYTES], s1[W * BYTES], s2[S > 2 ? W * BYTES : 16];
+  __shared__ __attribute__((aligned(1024))) char s0[W * BYTES], s1[W * BYTES];  // the ring's two stages
   __shared__ int first[kMaxGroups];
   static_assert(MB * NB <= L, "a wave's sums fit one stage");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -209,14 +166,14 @@ __device__ __forceinline__ void stream(const I8Args &p) {
 #pragma unroll
   for (int g = 0; g < L; ++g) off[g] = (uint32_t)(row_of(g) * (g < LA ? p.lda : p.ldb) + chunk_of(g));
   const int steps = (int)((p.K + STEP - 1) / STEP);
-  const int turns = (steps + S * W - 1) / (S * W);  // of the ring, per tile
+  const int turns = (steps + 2 * W - 1) / (2 * W);  // of the ring, per tile
   // (kept out of the compiler's sight: every copy's LDS address held in a scalar register of its own would spill them)
   int mine = wave * BYTES;
   auto stage = [&](int d) -> char * {
     asm volatile("" : "+s"(mine));
-    return (d == 0 ? s0 : d == 1 ? s1 : s2) + mine;
+    return (d == 0 ? s0 : s1) + mine;
   };
-  // The copies run S - 1 steps ahead of the products: step fq of tile ft, through resources over its valid rows
+  // The copies run one step ahead of the products: step fq of tile ft, through resources over its valid rows
   // (others lie past them, since leading dimensions are at least K, and load as zeros).
   __amdgpu_buffer_rsrc_t ra, rb;
   int ft = blockIdx.x, fq = 0;
@@ -236,15 +193,14 @@ __device__ __forceinline__ void stream(const I8Args &p) {
     for (int g = 0; g < L; ++g)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(g < LA ? ra : rb, (lds_void *)(to + g * 1024), 16,
                                                chunk_of(g) < left ? off[g] : kOutside, left ? s * STEP : 0, 0, 0);
-    if (++fq == turns * S) {
+    if (++fq == turns * 2) {
       fq = 0;
       ft += gridDim.x;
       if (ft < tiles) open(ft);
     }
   };
   open(t);
-#pragma unroll
-  for (int d = 0; d < S - 1; ++d) fetch(d);
+  fetch(0);
   for (; t < tiles; t += gridDim.x) {
     i32x4 acc[MB][NB];
 #pragma unroll
@@ -253,11 +209,11 @@ __device__ __forceinline__ void stream(const I8Args &p) {
       for (int j = 0; j < NB; ++j) acc[i][j] = i32x4{};
     for (int q = 0; q < turns; ++q) {
 #pragma unroll
-      for (int d = 0; d < S; ++d) {
+      for (int d = 0; d < 2; ++d) {
         // the stage read in the last turn is free (its reads are done): refill it
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        fetch((d + S - 1) % S);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 1) * L) : "memory");
+        fetch(1 - d);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L) : "memory");
         const char *a = stage(d), *b = a + LA * 1024;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -282,7 +238,7 @@ __device__ __forceinline__ void stream(const I8Args &p) {
     for (int i = 0; i < MB; ++i)
 #pragma unroll
       // (the stage just read is refilled only in the next tile)
-      for (int j = 0; j < NB; ++j) *reinterpret_cast<i32x4 *>(stage(S - 1) + ((i * NB + j) * 64 + lane) * 16) = acc[i][j];
+      for (int j = 0; j < NB; ++j) *reinterpret_cast<i32x4 *>(stage(1) + ((i * NB + j) * 64 + lane) * 16) = acc[i][j];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -294,14 +250,13 @@ __device__ __forceinline__ void stream(const I8Args &p) {
     const Place o = stream_tile<AR, NB>(e, t, first, lane);
     const Epilogue ep{e.act, e.slope, false};
     const float *sa = e.sa ? e.sa + o.z * e.stride_sa : nullptr;
-    const char *const last = S == 2 ? s1 : s2;
     for (int k = threadIdx.x; k < MB * NB * 64; k += W * 64) {
       const int blk = k >> 6, l = k & 63;
       const int64_t m = o.m0 + 16 * (blk / NB) + (l & 15), n = o.n0 + 16 * (blk % NB) + 4 * (l >> 4);
       if (m >= o.M || m >= o.m0 + AR || n >= e.N) continue;
       i32x4 sum{};
 #pragma unroll
-      for (int w = 0; w < W; ++w) sum += *reinterpret_cast<const i32x4 *>(last + w * BYTES + k * 16);
+      for (int w = 0; w < W; ++w) sum += *reinterpret_cast<const i32x4 *>(s1 + w * BYTES + k * 16);
       float cb[4];
       channel_scales(e, o.z, n, cb);
       store_i8<FMT>(e, ep, (char *)e.C + (o.z * e.strideC + m * e.ldc) * fmt_bytes(FMT), n, sa ? sa[m] : 1.f, cb, sum);
@@ -313,14 +268,14 @@ __device__ __forceinline__ void stream(const I8Args &p) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the copies of zeros past the end
 }
 
-template <int AR, int NB, int W, int S, int FMT>
+template <int AR, int NB, int W, int FMT>
 __global__ __launch_bounds__(W * 64) void gemm_i8_stream_kernel(I8Args p) {
-  stream<AR, NB, W, S, FMT>(p);
+  stream<AR, NB, W, FMT>(p);
 }
 
-template <int AR, int NB, int W, int S>
+template <int AR, int NB, int W>
 hipError_t stream_t(I8Args a, hipStream_t st) {
-  constexpr int LDS = S * W * (AR / 4 + 4 * NB) * 1024 + 4 * kMaxGroups + 64;
+  constexpr int LDS = 2 * W * (AR / 4 + 4 * NB) * 1024 + 4 * kMaxGroups + 64;
   a.tiles_m = (int32_t)((a.M + AR - 1) / AR);
   a.tiles_n = (int32_t)((a.N + 16 * NB - 1) / (16 * NB));
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
@@ -333,11 +288,11 @@ hipError_t stream_t(I8Args a, hipStream_t st) {
     a.nz = (int32_t)(a.batch - z0 < most ? a.batch - z0 : most);
     const dim3 grid((unsigned)(tiles * a.nz < resident ? tiles * a.nz : resident));
     if (a.fmt == FMT_F32)
-      hipLaunchKernelGGL((gemm_i8_stream_kernel<AR, NB, W, S, FMT_F32>), grid, dim3(W * 64), 0, st, a);
+      hipLaunchKernelGGL((gemm_i8_stream_kernel<AR, NB, W, FMT_F32>), grid, dim3(W * 64), 0, st, a);
     else if (a.fmt == FMT_F16)
-      hipLaunchKernelGGL((gemm_i8_stream_kernel<AR, NB, W, S, FMT_F16>), grid, dim3(W * 64), 0, st, a);
+      hipLaunchKernelGGL((gemm_i8_stream_kernel<AR, NB, W, FMT_F16>), grid, dim3(W * 64), 0, st, a);
     else
-      hipLaunchKernelGGL((gemm_i8_stream_kernel<AR, NB, W, S, FMT_BF16>), grid, dim3(W * 64), 0, st, a);
+      hipLaunchKernelGGL((gemm_i8_stream_kernel<AR, NB, W, FMT_BF16>), grid, dim3(W * 64), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -346,8 +301,19 @@ hipError_t stream_t(I8Args a, hipStream_t st) {
 
 }  // namespace
 
-// Rows per workgroup (16, 32 or 64), blocks of 16 columns and waves.  Timed on
+// Which kernel, and the streaming one's rows per workgroup (16 or 32), blocks of
+// 16 columns and waves.  kernel None: the general one
+// (64 x 64 tiles).  Timed on
 // weights past the caches; "tiles" are blocks of 16 columns over all problems.
+//  * Operands that the ring's copies cannot take, up to 16 rows: registers while
+//    a CU has one tile (16 x 4096 x 4095 18.0 us against 23.0 in the general
+//    kernel, 16 x 4096 x 8191 31.9 against 40.6); past that 16 rows at odd
+//    addresses crowd the L1 (16 x 8192 x 8191 59.5 against 43.6), and more rows
+//    always (32 x 4096 x 4095 32.6 against 22.9).
+//  * Others, up to 4 rows of K <= 4096: registers too, since a wave has few steps
+//    and a ring to fill first (4 x 28672 x 4096 24.4 us against 26.7 streamed,
+//    1 x 128256 x 4096 88 against 102; 1 x 65536 x 2048 28.2 against 25.0; at
+//    K = 8192 1 x 16384: 33.6 against 25.2).
 //  * One wave per workgroup (no barrier, no split of K) once the tiles keep
 //    every CU's memory queue full, four while they do not: 16 rows, 16384 x 8192
 //    (1024 tiles) 28.4 us on four waves against 30.7 on one, 28672 x 4096 30.5
@@ -355,11 +321,13 @@ hipError_t stream_t(I8Args a, hipStream_t st) {
 //    against 12.6.
 //  * 17-32 rows: 28672 x 4096 30.7 us on two column blocks and one wave, 32.3 on
 //    one and two; 8192 x 8192 23.9 against 19.6.
-//  * 33-64 rows: as 32-row blocks they read the weights twice (the second time
-//    from L2): 4096 x 4096 9.7 us against 11-17 in 64-row blocks, 8192 x 8192 25.2
-//    against 28.6, 16384 x 8192 43.4 against 43.0, 8 x 2048 x 4096 27.1 against
-//    22.7.  Grouped calls, whose counts mostly lie far below the capacity, keep
-//    32 (256 groups of 1024 x 2048, 16 rows each of 64: 112 us against 137).
+//  * 33-64 rows read the weights twice in 32-row blocks (the second time from
+//    L2): 8192 x 8192 26 us against 34 in the general kernel, whose 64 x 64 tiles
+//    win once most CUs have one: 12288 x 4096 23.5 against 21.2, 16384 x 8192 42
+//    against 39, 64 batches of 1024 x 2048 40 against 34, 256 of them 165 against
+//    137.  Grouped calls, whose counts mostly lie far below the capacity, keep 32
+//    (256 groups of 1024 x 2048, 16 rows each of 64: 112 us against 137 in 64-row
+//    blocks).
 I8Skinny i8_skinny_plan(const I8Args &p) {
   I8Skinny s;
   // (more columns than workgroups of 256 fit a launch go to the general kernel)
@@ -367,31 +335,35 @@ I8Skinny i8_skinny_plan(const I8Args &p) {
   const bool aligned = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && p.K % 16 == 0 && p.lda % 16 == 0 &&
                        p.ldb % 16 == 0 && p.strideA % 16 == 0 && p.strideB % 16 == 0;
   // 32-bit offsets over a block's rows
-  const bool fits = 64 * p.lda + p.K < (int64_t)1 << 30 && 64 * p.ldb + p.K < (int64_t)1 << 30;
+  const bool fits = 32 * p.lda + p.K < (int64_t)1 << 30 && 32 * p.ldb + p.K < (int64_t)1 << 30;
   s.can_stream = aligned && fits;
-  s.stream = s.can_stream && !(p.M <= 4 && p.K <= 4096 && !p.rows);
   const int64_t per = (p.N + 15) / 16;
+  s.can_skinny = (p.M + 15) / 16 * per <= 0xffffffffLL / 256;
   const int64_t tiles = per > ((int64_t)1 << 40) / p.batch ? (int64_t)1 << 40 : per * p.batch;
   if (p.M <= 16) {
     s.rows = 16;
     s.nb = 1;
     s.waves = tiles >= 1024 && tiles >= p.K / 4 ? 1 : 4;
   } else {
-    s.rows = p.M > 32 && tiles >= 1024 && !p.rows ? 64 : 32;
+    s.rows = 32;
     s.nb = tiles >= (p.M > 32 ? 512 : 1536) ? 2 : 1;
     s.waves = s.nb == 2 ? 1 : 2;
   }
+  if (!s.can_stream)
+    s.kernel = p.M <= 16 && tiles <= 256 ? I8Kernel::Skinny : I8Kernel::None;
+  else if (p.M <= 4 && p.K <= 4096 && !p.rows)
+    s.kernel = I8Kernel::Skinny;
+  else
+    s.kernel = p.M > 32 && tiles >= 768 && !p.rows ? I8Kernel::None : I8Kernel::Stream;
   return s;
 }
 
-hipError_t launch_i8_skinny(const I8Args &p, const I8Skinny &s, hipStream_t st) {
-  if (s.stream) {
-    if (s.rows == 16) return s.waves == 1 ? stream_t<16, 1, 1, 2>(p, st) : stream_t<16, 1, 4, 2>(p, st);
-    if (s.rows == 32) return s.nb == 1 ? stream_t<32, 1, 2, 2>(p, st) : stream_t<32, 2, 1, 2>(p, st);
-    return stream_t<64, 2, 1, 2>(p, st);
-  }
-  if (s.rows == 16) return skinny_t<1, 1, 4, 4>(p, st);
-  return p.M <= 32 ? skinny_t<2, 2, 4, 2>(p, st) : skinny_t<4, 2, 4, 2>(p, st);
+hipError_t launch_i8_stream(const I8Args &p, hipStream_t st) {
+  const I8Skinny s = i8_skinny_plan(p);
+  if (s.rows == 16) return s.waves == 1 ? stream_t<16, 1, 1>(p, st) : stream_t<16, 1, 4>(p, st);
+  return s.nb == 1 ? stream_t<32, 1, 2>(p, st) : stream_t<32, 2, 1>(p, st);
 }
+
+hipError_t launch_i8_skinny(const I8Args &p, hipStream_t st) { return skinny_t(p, st); }
 
 }  // namespace tsm

@@ -13,8 +13,6 @@
 namespace tsm {
 namespace {
 
-enum class I8Kernel { None, Block128, Block64, Tile, Stream, Skinny };
-
 const char *i8_name(I8Kernel k) {
   switch (k) {
     case I8Kernel::Block128:
@@ -117,17 +115,23 @@ int i8_plan(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64
   p->vec_store = (uintptr_t)C % (uintptr_t)(4 * es) == 0 && ldc % 4 == 0 && strideC % 4 == 0;
 
   // 64-tiles up to 128 of 128 x 128 (512 x 4096 x 4096, 128 tiles: 24.6 us
-  // against 26.3; 640 x 4096 x 2048, 160: 19.0 against 15.5), 256-tiles from 72
+  // against 26.3; 640 x 4096 x 2048, 160: 19.0 against 15.5) and up to 64 rows
+  // (48 x 28672 x 4096 31.6 against 34.5), 256-tiles from 72
   // (2304 x 2304 x 1024, 81: 19.4 against 21.1; 2048 x 2048 x 2048, 64: 27.7
-  // against 17.3), the streaming kernels up to 64 rows.
+  // against 17.3) unless rows fill half of them at most and 128-tiles take one
+  // round (128 x 32768 x 8192, 256 of those: 88 us against 69; 128 x 128256 x
+  // 4096, 1002: 123 against 141; 16 batches of 100 x 2048 x 4096: 55 against 40);
+  // up to 64 rows see i8_skinny_plan.
   const int64_t tiles128 = ((M + 127) / 128) * ((N + 127) / 128), tiles64 = ((M + 63) / 64) * ((N + 63) / 64);
-  *kernel = tiles128 * batch <= 128 ? I8Kernel::Block64 : I8Kernel::Block128;
+  const bool small = tiles128 * batch <= 128 || (M <= 64 && tiles64 * 512 <= 0xffffffffLL);
+  *kernel = small ? I8Kernel::Block64 : I8Kernel::Block128;
   if ((*kernel == I8Kernel::Block64 ? tiles64 : tiles128) * 512 > 0xffffffffLL)
     return fail(TSM_ERROR_NOT_SUPPORTED, "tile grid too large");
+  const bool half = M <= 128 && tiles128 * batch <= 256;  // 256-tiles half empty, and a round of 128-tiles does it
   const int64_t tiles256 = ((M + 255) / 256) * ((N + 255) / 256) * batch;
-  if (tiles256 >= kFewTiles && i8_tile_supports(*p)) *kernel = I8Kernel::Tile;
+  if (M > 64 && !half && tiles256 >= kFewTiles && i8_tile_supports(*p)) *kernel = I8Kernel::Tile;
   const I8Skinny sk = i8_skinny_plan(*p);
-  if (sk.rows) *kernel = sk.stream ? I8Kernel::Stream : I8Kernel::Skinny;
+  if (sk.kernel != I8Kernel::None) *kernel = sk.kernel;
   // TSM_GEMM_KERNEL=<name> forces a variant (tests and tuning); names of other
   // families are left alone, a variant that cannot run the problem is an error.
   const char *force = getenv("TSM_GEMM_KERNEL");
@@ -136,8 +140,8 @@ int i8_plan(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64
     for (I8Kernel k : {I8Kernel::Block128, I8Kernel::Block64, I8Kernel::Tile, I8Kernel::Stream, I8Kernel::Skinny})
       if (strcmp(force, i8_name(k)) == 0) want = k;
     if (want == I8Kernel::None) return fail(TSM_ERROR_INVALID_VALUE, "TSM_GEMM_KERNEL=%s names no kernel", force);
-    if ((want == I8Kernel::Tile && !i8_tile_supports(*p)) || (want == I8Kernel::Stream && !(sk.rows && sk.can_stream)) ||
-        (want == I8Kernel::Skinny && !sk.rows))
+    if ((want == I8Kernel::Tile && !i8_tile_supports(*p)) || (want == I8Kernel::Stream && !sk.can_stream) ||
+        (want == I8Kernel::Skinny && !sk.can_skinny))
       return fail(TSM_ERROR_NOT_SUPPORTED, "TSM_GEMM_KERNEL=%s cannot run this problem", force);
     *kernel = want;
     *forced = true;
@@ -161,12 +165,11 @@ int i8_run(const I8Args &p, I8Kernel k, bool forced, void *stream) {
       e = launch_i8_tile(p, !forced, s);
       break;
     case I8Kernel::Stream:
-    case I8Kernel::Skinny: {
-      I8Skinny sk = i8_skinny_plan(p);
-      sk.stream = k == I8Kernel::Stream;
-      e = launch_i8_skinny(p, sk, s);
+      e = launch_i8_stream(p, s);
       break;
-    }
+    case I8Kernel::Skinny:
+      e = launch_i8_skinny(p, s);
+      break;
   }
   if (e != hipSuccess) return fail(TSM_ERROR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
   return TSM_SUCCESS;

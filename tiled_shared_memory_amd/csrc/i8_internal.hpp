@@ -43,14 +43,16 @@ bool i8_tile_supports(const I8Args &p);
 hipError_t launch_i8_tile(const I8Args &p, bool whole_only, hipStream_t stream);
 // The 256 x 256 tiles that whole_rounds leaves of a launch (tiles_m, tiles_n, z0 and nz set), as 128 x 128 ones.
 hipError_t launch_i8_rest(const I8Args &a, hipStream_t stream);
-// Few rows (up to 64): `rows` of them (0: not for this problem) by 16 nb columns per workgroup of `waves` waves.
+enum class I8Kernel { None, Block128, Block64, Tile, Stream, Skinny };
+// Few rows (up to 64).
 struct I8Skinny {
-  int rows = 0, nb = 0, waves = 0;
-  bool can_stream = false;  // the operands allow the streaming kernel
-  bool stream = false;      // and the rule takes it
+  I8Kernel kernel = I8Kernel::None;  // the rule's choice; None: the general kernel
+  bool can_skinny = false, can_stream = false;  // what the problem allows
+  int rows = 0, nb = 0, waves = 0;  // streaming: rows by 16 nb columns per workgroup of `waves` waves
 };
 I8Skinny i8_skinny_plan(const I8Args &p);
-hipError_t launch_i8_skinny(const I8Args &p, const I8Skinny &s, hipStream_t stream);
+hipError_t launch_i8_stream(const I8Args &p, hipStream_t stream);
+hipError_t launch_i8_skinny(const I8Args &p, hipStream_t stream);
 hipError_t launch_i8_block(const I8Args &p, int tile, hipStream_t stream);
 
 struct QuantArgs {
