@@ -401,3 +401,33 @@ def test_linear_layer_on_a_side_stream_and_replayed():
             eq, es = tsm.quantize(x)
             e = tsm.matmul_i8(eq, es, w.t(), sw)
             assert torch.equal(q, eq) and torch.equal(s, es) and torch.equal(c, e)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K,pad", [
+    (33, 12304, 1040, 0), (64, 14000, 272, 16), (16, 4096, 2047, 0), (9, 8200, 1023, 3), (40, 520, 4096, 0),
+    (128, 200, 4224, 0), (65, 136, 4352, 1), (50, 100, 4480 + 77, 0), (100, 70, 8191, 0), (65, 18500, 256, 0),
+    (128, 32700, 128, 0)])
+def test_borders_of_the_selection(M, N, K, pad, out):
+    """Few rows of many columns on 64-tiles, odd addresses, every phase of the deeper loop, 128-tiles half as wide as
+    a 256-tile; plain, as two batches, and grouped."""
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    a, b = padded(M, K, K + pad, g), padded(N, K, K + pad, g)
+    sa, sb = scales(M, g), scales(N, g) / K ** 0.5
+    say(f"[gpu] i8 borders {M}x{N}x{K} {out}")
+    buf = torch.full((M + 1, N + 3), 77.0, dtype=dtypes()[out], device="cuda")
+    tsm.matmul_i8(a, sa, b.t(), sb, out=buf[:M, :N])
+    check(buf[:M, :N], reference(a, sa, b, sb), out)
+    assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
+    a2 = torch.randint(-128, 128, (2, M, K), generator=g, device="cuda", dtype=torch.int8)
+    b2 = torch.stack([b, b.flip(0)])
+    s2 = scales((2, M), g)
+    plain = tsm.matmul_i8(a2, s2, b2.transpose(1, 2), None, out_dtype=dtypes()[out])
+    c = torch.full((2, M, N), 55.0, dtype=dtypes()[out], device="cuda")
+    tsm.matmul_i8(a2, s2, b2.transpose(1, 2), None, rows=torch.tensor([M - 1, M + 9], dtype=torch.int32, device="cuda"),
+                  out=c)
+    for z, m in enumerate([M - 1, M]):
+        check(plain[z], reference(a2[z], s2[z], b2[z], None), out)
+        assert torch.equal(c[z, :m], plain[z, :m]) and (c[z, m:] == 55.0).all()

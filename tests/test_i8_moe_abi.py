@@ -188,3 +188,35 @@ def test_wrappers_refuse_tensors_they_cannot_read():
         with pytest.raises(tsm.TsmError) as ei:
             call()
         assert ei.value.status == tsm.TSM_ERROR_INVALID_VALUE and needle in ei.value.detail
+
+
+@pytest.mark.parametrize("M,N,K,batch,grouped,off,want", [
+    (1, 8192, 8192, 1, 0, 0, "i8_stream"), (4, 28672, 4096, 1, 0, 0, "i8_skinny"),
+    (4, 28672, 4112, 1, 0, 0, "i8_stream"), (4, 1024, 4096, 4, 1, 0, "i8_stream"),
+    (16, 4096, 4095, 1, 0, 0, "i8_skinny"), (16, 4112, 4095, 1, 0, 0, "i8_block_64x64x128"),
+    (1, 4096, 4096, 2, 0, 1, "i8_block_64x64x128"), (17, 64, 256, 1, 0, 1, "i8_block_64x64x128"),
+    (32, 65536, 4096, 1, 0, 0, "i8_stream"), (33, 12272, 4096, 1, 0, 0, "i8_stream"),
+    (33, 12288, 4096, 1, 0, 0, "i8_block_64x64x128"), (64, 32768, 8192, 1, 0, 0, "i8_block_64x64x128"),
+    (64, 1024, 2048, 64, 0, 0, "i8_block_64x64x128"), (64, 1024, 2048, 64, 1, 0, "i8_stream"),
+    (128, 16384, 8192, 1, 0, 0, "i8_block_64x64x128"), (128, 32768, 8192, 1, 0, 0, "i8_block_128x128x128"),
+    (128, 32896, 8192, 1, 0, 0, "i8_tile_256x256x128"), (129, 18432, 4096, 1, 0, 0, "i8_tile_256x256x128"),
+    (129, 16384, 4096, 1, 0, 0, "i8_block_128x128x128"), (2304, 2304, 1024, 1, 0, 0, "i8_tile_256x256x128")])
+def test_i8_routing(monkeypatch, M, N, K, batch, grouped, off, want):
+    """The kernel on either side of each border of the selection's rule."""
+    monkeypatch.delenv("TSM_GEMM_KERNEL", raising=False)
+    rows = P0 if grouped else None
+    assert tsm.tsm_gemm_i8_kernel_name(M, N, K, A0 + off, K, M * K, B0, K, N * K, C0, N, M * N, batch, rows, 0) == want
+
+
+def test_i8_routing_of_very_wide_products(monkeypatch):
+    """Past the columns that one launch of the few-row kernels or of 64-tiles holds: 128-tiles."""
+    monkeypatch.delenv("TSM_GEMM_KERNEL", raising=False)
+
+    def route(M, N, K=16):
+        return tsm.tsm_gemm_i8_kernel_name(M, N, K, A0, K, 0, B0, K, 0, 1 << 60, N, 0, 1, None, 1)
+
+    assert route(40, (1 << 28) + 64) == "i8_block_64x64x128"
+    assert route(40, 1 << 29) == "i8_block_128x128x128"
+    monkeypatch.setenv("TSM_GEMM_KERNEL", "i8_skinny")
+    assert route(16, 1 << 27) == "i8_skinny"
+    assert route(40, (1 << 28) - 64) is None  # 3 x 2^24 blocks: cannot run

@@ -17,7 +17,10 @@
 // zeros in both operands.  Odd row addresses cost memory throughput (1000 x 1500:
 // 12.4 us at K = 777, 7.9 at K = 768); loading the dwords that cover a vector and
 // realigning them took as long (11.7 us; 2047^3 28.4 us against 27.4).
-// Two slabs ahead: four were slower where K is short (1000 x 1500 x 768 8.5 us).
+// Two slabs ahead; four for up to 128 rows of K >= 4096, where the weights come
+// from memory and a CU has one or two workgroups to wait for them (128 x 8192 x
+// 8192 30.2 us, 34.3 with two; 64 x 16384 x 8192 38.5, 41.4; 64 x 32768 x 8192
+// 60.2, 64.3; but 256 x 8192 x 8192 44.2, 43.0, and 1000 x 1500 x 777 13.6, 12.2).
 #include "i8_common.hpp"
 
 namespace tsm {
@@ -26,10 +29,10 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int BK = 128;         // codes per slab
 constexpr int PITCH = BK + 16;  // LDS row pitch: the 16 rows of a fragment read fall on distinct banks
-constexpr int D = 2;            // slabs in flight in registers (even: the LDS buffers alternate)
 
-// REST: the workgroups take the quarters of the 256-tiles that whole_rounds leaves.
-template <int T, int FMT, bool REST = false>
+// D: slabs in flight in registers (even: the LDS buffers alternate).  REST: the
+// workgroups take the quarters of the 256-tiles that whole_rounds leaves.
+template <int T, int FMT, int D, bool REST = false>
 __global__ __launch_bounds__(kThreads) void gemm_i8_block_kernel(I8Args p) {
   constexpr int W = T / 2, NB = W / 16;            // wave tile, 16 x 16 blocks per dimension
   constexpr int PR = BK / 16, RP = kThreads / PR;  // vectors per row, rows per pass (64)
@@ -177,15 +180,15 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_block_kernel(I8Args p) {
   }
 }
 
-template <int T>
+template <int T, int D>
 hipError_t block_t(const I8Args &p, hipStream_t stream) {
   return over_tiles(p, T, T, kThreads, [&](const I8Args &a, dim3 grid) {
     if (a.fmt == FMT_F32)
-      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_F32>), grid, dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_F32, D>), grid, dim3(kThreads), 0, stream, a);
     else if (a.fmt == FMT_F16)
-      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_F16>), grid, dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_F16, D>), grid, dim3(kThreads), 0, stream, a);
     else
-      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_BF16>), grid, dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((gemm_i8_block_kernel<T, FMT_BF16, D>), grid, dim3(kThreads), 0, stream, a);
   });
 }
 
@@ -194,16 +197,17 @@ hipError_t block_t(const I8Args &p, hipStream_t stream) {
 hipError_t launch_i8_rest(const I8Args &a, hipStream_t stream) {
   const dim3 grid(4 * (kFewTiles - 1)), block(kThreads);
   if (a.fmt == FMT_F32)
-    hipLaunchKernelGGL((gemm_i8_block_kernel<128, FMT_F32, true>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_block_kernel<128, FMT_F32, 2, true>), grid, block, 0, stream, a);
   else if (a.fmt == FMT_F16)
-    hipLaunchKernelGGL((gemm_i8_block_kernel<128, FMT_F16, true>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_block_kernel<128, FMT_F16, 2, true>), grid, block, 0, stream, a);
   else
-    hipLaunchKernelGGL((gemm_i8_block_kernel<128, FMT_BF16, true>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((gemm_i8_block_kernel<128, FMT_BF16, 2, true>), grid, block, 0, stream, a);
   return hipPeekAtLastError();
 }
 
 hipError_t launch_i8_block(const I8Args &p, int tile, hipStream_t stream) {
-  return tile == 128 ? block_t<128>(p, stream) : block_t<64>(p, stream);
+  if (tile == 128) return block_t<128, 2>(p, stream);
+  return p.M <= 128 && p.K >= 4096 ? block_t<64, 4>(p, stream) : block_t<64, 2>(p, stream);
 }
 
 }  // namespace tsm

@@ -130,10 +130,6 @@ __device__ __forceinline__ void find_group(const I8Args &p, int lane, int &t, in
   }
 }
 
-// Where a workgroup of a flat grid works: problem z, tile (tm, tn) in the
-// grouped tile order, the grid regrouped per XCD.  Grouped calls number only
-// the tiles that hold rows, so the real work spreads evenly over the XCDs;
-// false: nothing to do.  WHOLE: only the tiles of whole_rounds.
 // Fewer than this many 256-tiles left over from whole rounds of the CUs run as
 // 128-tiles in a second launch: a round takes as long for one tile as for all
 // (2304 x 2304 x 1024, 81 tiles: 19.4 us against 21.1 in 128-tiles; 2048 x 2048 x
@@ -169,6 +165,10 @@ __device__ __forceinline__ int i8_tiles(const I8Args &p) {
   return (p.rows ? all_group_tiles<BM>(p, threadIdx.x & 63) : p.tiles_m * p.nz) * p.tiles_n;
 }
 
+// Where a workgroup of a flat grid works: problem z, tile (tm, tn) in the
+// grouped tile order, the grid regrouped per XCD.  Grouped calls number only
+// the tiles that hold rows, so the real work spreads evenly over the XCDs;
+// false: nothing to do.  WHOLE: only the tiles of whole_rounds.
 template <int BM, bool WHOLE = false>
 __device__ __forceinline__ bool i8_tile_of(const I8Args &p, int group_m, int64_t &z, int &tm, int &tn) {
   int V = i8_tiles<BM>(p);
