@@ -47,10 +47,11 @@ def log(msg):
 
 # Sources that define each kernel family's device code (with the shared headers
 # below): a counter record stays valid while these are unchanged.
-KERNEL_FILES = {"tile_": ("gemm_tile.hip",), "skinny_": ("gemm_skinny.hip",),
-                "hybrid_": ("gemm_tile.hip", "gemm_ksplit.hip"), "streamk_": ("gemm_tile.hip", "gemm_ksplit.hip"),
-                "band_": ("gemm_tile.hip", "gemm_masked.hip", "gemm_skinny.hip", "gemm_splitk.hip"),
-                "ksplit_": ("gemm_skinny.hip", "gemm_ksplit.hip", "gemm_tile.hip"),
+KERNEL_FILES = {"tile_": ("gemm_tile.hip", "lds_ring.hpp"), "skinny_": ("gemm_skinny.hip",),
+                "hybrid_": ("gemm_tile.hip", "lds_ring.hpp", "gemm_ksplit.hip"),
+                "streamk_": ("gemm_tile.hip", "lds_ring.hpp", "gemm_ksplit.hip"),
+                "band_": ("gemm_tile.hip", "lds_ring.hpp", "gemm_masked.hip", "gemm_skinny.hip", "gemm_splitk.hip"),
+                "ksplit_": ("gemm_skinny.hip", "gemm_ksplit.hip", "gemm_tile.hip", "lds_ring.hpp"),
                 "splitk_": ("gemm_splitk.hip",), "masked_": ("gemm_masked.hip",), "rowsum_": ("rowsum.hip",)}
 SHARED_FILES = ("gemm_internal.hpp", "mfma.hpp")
 

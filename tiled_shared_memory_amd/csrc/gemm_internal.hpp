@@ -86,9 +86,6 @@ __device__ __forceinline__ void tile_order(int pid, int tiles_m, int tiles_n, in
   tn = in_group / gm;
 }
 
-// CUs of the current device (gemm_api.hip).
-int device_cus();
-
 // Largest grid.y a launch uses for the batch; bigger batches are split.
 constexpr int64_t kMaxGridY = 65535;
 

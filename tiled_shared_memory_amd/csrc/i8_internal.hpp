@@ -43,6 +43,9 @@ bool i8_tile_supports(const I8Args &p);
 hipError_t launch_i8_tile(const I8Args &p, bool whole_only, hipStream_t stream);
 // The 256 x 256 tiles that whole_rounds leaves of a launch (tiles_m, tiles_n, z0 and nz set), as 128 x 128 ones.
 hipError_t launch_i8_rest(const I8Args &a, hipStream_t stream);
+// CUs of the current device (gemm_api.hip).
+int device_cus();
+
 enum class I8Kernel { None, Block128, Block64, Tile, Stream, Skinny };
 // Few rows (up to 64).
 struct I8Skinny {
