@@ -220,3 +220,63 @@ def test_i8_routing_of_very_wide_products(monkeypatch):
     monkeypatch.setenv("TSM_GEMM_KERNEL", "i8_skinny")
     assert route(16, 1 << 27) == "i8_skinny"
     assert route(40, (1 << 28) - 64) is None  # 3 x 2^24 blocks: cannot run
+
+
+def test_allocations_are_made_and_filled_on_the_stream_of_the_call(monkeypatch):
+    """What a call on a stream of its own allocates is that stream's memory, and zeros are written there (the launch
+    and the streams are stand-ins here)."""
+    import contextlib
+
+    import torch
+
+    class OnGpu(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    active, made = [], []
+
+    @contextlib.contextmanager
+    def under(stream):
+        active.append(stream)
+        yield
+        active.pop()
+
+    def recorded(make):
+        def f(*a, **kw):
+            made.append(active[-1] if active else None)
+            return make(*a, **kw)
+
+        return f
+
+    def on_gpu(*shape, dtype=torch.float32):
+        return torch.ones(shape, dtype=dtype).as_subclass(OnGpu)
+
+    x, q, pos = on_gpu(4, 8), on_gpu(4, 8, dtype=torch.int8), on_gpu(4, 2, dtype=torch.int32)
+    s, b = on_gpu(4), on_gpu(6, 8, dtype=torch.int8)
+    monkeypatch.setattr(torch.cuda, "stream", under)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: (handle, device))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: ("default", device))
+    monkeypatch.setattr(tsm, "_launch", lambda *a: None)
+    monkeypatch.setattr(torch, "empty", recorded(torch.empty))
+    monkeypatch.setattr(torch, "zeros", recorded(torch.zeros))
+    for handle, want in ((1234, (1234, 0)), (0, ("default", 0)), (None, None)):
+        for n, call in [
+            (2, lambda: tsm.quantize(x, stream=handle)), (1, lambda: tsm.matmul_i8(q, s, b.t(), None, stream=handle)),
+            (2, lambda: tsm.sort_tokens(pos, 3, 4, stream=handle)),
+            (2, lambda: tsm.dispatch_tokens(q, pos, slots=9, scale=s, stream=handle)),
+            (1, lambda: tsm.combine_tokens(x, pos, stream=handle)),
+            (1, lambda: tsm.dispatch_tokens_backward(x, pos, stream=handle)),
+            (2, lambda: tsm.combine_tokens_backward(x, x, pos, stream=handle))]:
+            made.clear()
+            call()
+            assert made == [want] * n
+
+
+def test_calls_on_a_stream_refuse_tensors_off_the_gpu():
+    import torch
+
+    x, pos = torch.zeros((4, 8)), torch.zeros((4, 2), dtype=torch.int32)
+    for call in (lambda: tsm.quantize(x, stream=1234), lambda: tsm.combine_tokens_backward(x, x, pos, stream=1234)):
+        with pytest.raises(tsm.TsmError) as ei:
+            call()
+        assert ei.value.status == tsm.TSM_ERROR_INVALID_VALUE and "not on a GPU" in ei.value.detail

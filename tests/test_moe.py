@@ -430,3 +430,49 @@ def test_expert_layer(T, k, E, cap, H, F):
         torch.cuda.synchronize()
         assert torch.equal(ya, layer(x, ids, w, up, down, E, cap))
         assert torch.equal(yb, layer_i8(x, ids, w, qup, qdown, E, cap))
+
+
+@pytest.mark.parametrize("as_handle", [False, True], ids=["stream", "handle"])
+def test_results_on_a_stream_of_their_own(as_handle):
+    """Calls on a side stream that allocate their results, while the current stream is busy and then writes into blocks
+    that it has given back to torch: every result is that of the same call on the current stream."""
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(4)
+    T, k, E, cap, H, N = 300, 2, 8, 90, 512, 256
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda")
+    x, dy = value((T, H), torch.float32, g), value((T, H), torch.float32, g)
+    slab = value((E * cap, H), torch.float32, g)
+    wt = torch.rand((T, k), generator=g, device="cuda")
+    w = torch.randint(-128, 128, (N, H), generator=g, device="cuda", dtype=torch.int8)
+    pos, _ = tsm.sort_tokens(ids, E, cap)
+    q, s = tsm.quantize(x)
+    held = torch.zeros(E * cap, dtype=torch.bool, device="cuda")
+    held[pos[pos >= 0].long()] = True
+    calls = {
+        "quantize": lambda **kw: tsm.quantize(x, **kw),
+        "matmul_i8": lambda **kw: (tsm.matmul_i8(q, s, w.t(), None, **kw),),
+        "sort": lambda **kw: tsm.sort_tokens(ids, E, cap, **kw),
+        "dispatch": lambda **kw: tuple(t[held] for t in tsm.dispatch_tokens(q, pos, slots=E * cap, scale=s, **kw)),
+        "combine": lambda **kw: (tsm.combine_tokens(slab, pos, wt, **kw),),
+        "dispatch gradient": lambda **kw: (tsm.dispatch_tokens_backward(slab, pos, **kw),),
+        "combine gradients": lambda **kw: tsm.combine_tokens_backward(dy, slab, pos, wt, **kw)}
+    big = torch.randn((4096, 4096), generator=g, device="cuda")
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        say(f"[gpu] {name} on a side stream")
+        want = call()
+        torch.cuda.synchronize()
+        for _ in range(6):
+            torch.mm(big, big)
+        blocks = [torch.empty_like(t) for t in want for _ in range(4)]
+        for b in blocks:
+            b.fill_(77)
+        del blocks, b
+        if name == "dispatch":  # (its rows are picked on the stream, too)
+            with torch.cuda.stream(side):
+                got = call(stream=side.cuda_stream if as_handle else side)
+        else:
+            got = call(stream=side.cuda_stream if as_handle else side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name

@@ -71,7 +71,8 @@ def matmul(a, b, *, out=None, out_dtype=None, activation=None, slope=0.01, works
     float32 (default), float16 or bfloat16.  ``activation`` is None, "relu" or
     "leaky_relu" (with ``slope``), fused into the kernels' epilogue.  With a
     ``workspace`` (see ``workspace_for``) products with few output tiles and
-    deep K split K through it.
+    deep K split K through it.  On a ``stream`` other than the current one give
+    ``out``: a result allocated here is memory of the current stream.
     """
     import torch
 
@@ -106,6 +107,10 @@ def matmul(a, b, *, out=None, out_dtype=None, activation=None, slope=0.01, works
 
 
 # ---- int8 products and expert routing --------------------------------------------------------------------------
+#
+# ``stream`` (a torch stream or its handle): None is the current stream of the tensors' GPU.  What a call given one
+# allocates is memory of that stream, as inside ``torch.cuda.stream``: another stream waits for it before it uses the
+# result, and ``record_stream`` tells torch of that use.
 
 
 def _bad(text):
@@ -149,12 +154,32 @@ def _packed(what, t):
         _bad(f"{what} must be contiguous")
 
 
-def _new(like, shape, dtype, fill=None):
-    """A tensor of a dtype (torch's, or its name) on the GPU of ``like``."""
+def _under(stream, d):
+    """Context in which torch allocates and fills for a call on ``stream`` (a torch stream or its handle) of GPU d."""
+    import torch
+
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    # (a handle of 0 would make ExternalStream take a stream of torch's pool)
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=d) if handle else torch.cuda.default_stream(d))
+
+
+def _new(like, shape, dtype, stream, fill=None):
+    """A tensor of a dtype (torch's, or its name) on the GPU of ``like``, zeros with ``fill``.  With a stream it is that
+    stream's memory, and the zeros are written there: on the current stream nothing would order them, or work that
+    still uses the block's last tensor, before the call."""
     import torch
 
     dtype = getattr(torch, dtype) if isinstance(dtype, str) else dtype
-    return (torch.empty if fill is None else torch.zeros)(shape, dtype=dtype, device=like.device)
+    make = torch.zeros if fill else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=like.device)
+    d = like.get_device()
+    if d < 0:
+        _bad("tensors must be on a GPU (the first is not on a GPU)")
+    with _under(stream, d):
+        return make(shape, dtype=dtype, device=like.device)
 
 
 def _at(t):
@@ -202,9 +227,9 @@ def quantize(x, *, rows=None, out=None, scale=None, stream=None):
         _bad("x must be 2-D or 3-D")
     f = _wants("x", x, _FLOATS)
     if out is None:
-        out = _new(x, x.shape, "int8")
+        out = _new(x, x.shape, "int8", stream)
     if scale is None:
-        scale = _new(x, x.shape[:-1], "float32")
+        scale = _new(x, x.shape[:-1], "float32", stream)
     _wants("out", out, (TSM_I8,), x.shape)
     _wants("scale", scale, (TSM_F32,), x.shape[:-1])
     G = x.shape[0] if x.dim() == 3 else 1
@@ -244,7 +269,7 @@ def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, ac
     batch = ba if bb == 1 else bb
     shape = (batch, M, N) if batched else (M, N)
     if out is None:
-        out = _new(a, shape, out_dtype or "float32")
+        out = _new(a, shape, out_dtype or "float32", stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         _bad(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
     f = _wants("out", out, _FLOATS, shape)
@@ -283,7 +308,7 @@ def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, ac
 def sort_workspace_for(ids, experts):
     """A CUDA tensor for ``sort_tokens(..., workspace=...)``, or None when the sizes need none."""
     n = moe_sort_workspace_bytes(ids.shape[0], ids.shape[1], experts)
-    return _new(ids, (n,), "uint8") if n else None
+    return _new(ids, (n,), "uint8", None) if n else None
 
 
 def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspace=None, stream=None):
@@ -298,9 +323,9 @@ def sort_tokens(ids, experts, capacity, *, positions=None, counts=None, workspac
         _bad("ids must be 2-D")
     f = _wants("ids", ids, (TSM_I32, TSM_I64))
     if positions is None:
-        positions = _new(ids, ids.shape, "int32")
+        positions = _new(ids, ids.shape, "int32", stream)
     if counts is None:
-        counts = _new(ids, (experts,), "int32")
+        counts = _new(ids, (experts,), "int32", stream)
     _wants("positions", positions, (TSM_I32,), ids.shape)
     _wants("counts", counts, (TSM_I32,), (experts,))
     _packed("positions", positions)
@@ -343,7 +368,7 @@ def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale
     if out is None:
         if slots is None:
             _bad("slots or out is needed")
-        out = _new(x, (slots, x.shape[1]), x.dtype)
+        out = _new(x, (slots, x.shape[1]), x.dtype, stream)
     elif slots is not None and out.shape[0] != slots:
         _bad(f"out has {out.shape[0]} rows, slots is {slots}")
     _slab_args("out", out, positions, x.shape[0], x.shape[1])
@@ -352,7 +377,7 @@ def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale
         _wants("scale", scale, (TSM_F32,), (x.shape[0],))
         _packed("scale", scale)
         if out_scale is None:
-            out_scale = _new(x, (out.shape[0],), "float32")
+            out_scale = _new(x, (out.shape[0],), "float32", stream)
         _wants("out_scale", out_scale, (TSM_F32,), (out.shape[0],))
         _packed("out_scale", out_scale)
     elif out_scale is not None:
@@ -370,7 +395,7 @@ def combine_tokens(slabs, positions, weights=None, *, out=None, stream=None):
     f = _wants("slabs", slabs, _FLOATS)
     tokens, hidden = positions.shape[0], slabs.shape[1]
     if out is None:
-        out = _new(slabs, (tokens, hidden), slabs.dtype)
+        out = _new(slabs, (tokens, hidden), slabs.dtype, stream)
     _wants("out", out, (f,), (tokens, hidden))
     if weights is not None:
         _wants("weights", weights, (TSM_F32,), positions.shape)
@@ -396,10 +421,10 @@ def combine_tokens_backward(dy, slabs, positions, weights=None, *, out=None, dwe
     _slab_args("slabs", slabs, positions, dy.shape[0], dy.shape[1])
     _wants("slabs", slabs, (f,))
     if out is None:
-        out = _new(slabs, slabs.shape, slabs.dtype, 0)
+        out = _new(slabs, slabs.shape, slabs.dtype, stream, fill=True)
     _wants("out", out, (f,), slabs.shape)
     if dweights is None:
-        dweights = _new(dy, positions.shape, "float32")
+        dweights = _new(dy, positions.shape, "float32", stream)
     _wants("dweights", dweights, (TSM_F32,), positions.shape)
     _packed("dweights", dweights)
     if weights is not None:
