@@ -321,7 +321,9 @@ int64_t gemm_noalloc_scratch_bytes(void);
  * ties to even, so X[r][c] is Q[r][c] * scale[r] to within half a step.  The
  * codes are those of the exact quotient (no intermediate rounding).  A row of
  * zeros gets scale 0 and codes 0; a row that holds a NaN or an infinity gets
- * scale NaN and codes 0, so every product with it is NaN.
+ * scale NaN and codes 0, so every product with it is NaN.  (A scale below the
+ * normal float32 range, of an m below 127 * 2^-126, is rounded to that range's
+ * steps, and X then differs by as much more.)
  *   R, C       : rows and columns per group, >= 0.  C = 0 writes scales of 0.
  *   X, ldx     : X[g*strideX + r*ldx + c], format xdtype (TSM_F32, TSM_F16 or
  *                TSM_BF16), aligned to its element; ldx >= 0 (rows may overlap
@@ -357,7 +359,8 @@ int gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const
 /*
  * gemm_i8_strided_batched -- `batch` such products at element strides (0 shares
  * an operand or its scales; strideC keeps the outputs disjoint), with the fused
- * activation of gemm_strided_batched_act applied after the scales.
+ * activation of gemm_strided_batched_act applied after the scales.  A NaN (of a
+ * scale) stays NaN with every activation; the 16-bit products' ReLU gives 0.
  */
 int gemm_i8_strided_batched(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64_t strideA,
                             const float *scale_a, int64_t stride_sa, const int8_t *B, int64_t ldb, int64_t strideB,

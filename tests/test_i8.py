@@ -431,3 +431,41 @@ def test_borders_of_the_selection(M, N, K, pad, out):
     for z, m in enumerate([M - 1, M]):
         check(plain[z], reference(a2[z], s2[z], b2[z], None), out)
         assert torch.equal(c[z, :m], plain[z, :m]) and (c[z, m:] == 55.0).all()
+
+
+@pytest.mark.parametrize("act", ["relu", "leaky_relu"])
+@pytest.mark.parametrize("kernel,M,N,K", [("i8_skinny", 4, 40, 272), ("i8_stream", 20, 130, 272),
+                                          ("i8_block_64x64x128", 70, 100, 133), ("i8_block_128x128x128", 150, 140, 256),
+                                          ("i8_tile_256x256x128", 300, 264, 256)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_nan_scales_pass_the_activation(monkeypatch, kernel, act, M, N, K, out):
+    """A token (or channel) whose scale is NaN gives NaN results with an activation too, in every kernel; the others
+    are as they were."""
+    import torch
+
+    monkeypatch.setenv("TSM_GEMM_KERNEL", kernel)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    a, b = padded(M, K, (K + 15) // 16 * 16, g), padded(N, K, (K + 15) // 16 * 16, g)
+    sa, sb = scales(M, g), scales(N, g)
+    sa[1], sb[N - 2] = float("nan"), float("nan")
+    say(f"[gpu] {kernel} {act} of NaN scales {out}")
+    c = tsm.matmul_i8(a, sa, b.t(), sb, out_dtype=dtypes()[out], activation=act, slope=0.5)
+    rows = torch.arange(M, device="cuda") != 1
+    cols = torch.arange(N, device="cuda") != N - 2
+    assert torch.isnan(c[~rows]).all() and torch.isnan(c[:, ~cols]).all()
+    check(c[rows][:, cols], reference(a[rows], sa[rows], b[cols], sb[cols], act, 0.5), out, 4)
+
+
+def test_a_token_of_nan_shows_in_an_expert_layers_hidden_rows():
+    """quantize, product with ReLU, quantize, product: the token's result is NaN, its neighbours' are not."""
+    import torch
+
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((5, 96), generator=g, device="cuda")
+    x[2, 7] = float("nan")
+    up, down = (tsm.quantize(torch.randn(s, generator=g, device="cuda")) for s in ((128, 96), (96, 128)))
+    say("[gpu] i8 layer of a NaN token")
+    h = tsm.matmul_i8(*tsm.quantize(x), up[0].t(), up[1], activation="relu", out_dtype=torch.bfloat16)
+    y = tsm.matmul_i8(*tsm.quantize(h), down[0].t(), down[1])
+    bad = torch.isnan(y)
+    assert bad[2].all() and not bad[[0, 1, 3, 4]].any()

@@ -252,7 +252,8 @@ def matmul_i8(a, scale_a, b, scale_b, *, rows=None, out=None, out_dtype=None, ac
     ``a`` has contiguous rows and ``b`` is column-major (``w.t()`` of a weight stored N x K).  ``scale_a`` (..., M) and
     ``scale_b`` (..., N) are float32 (None: ones).  2-D operands give one product, 3-D ones a strided batch (a batch
     dim of size 1 broadcasts); with ``rows`` (int32 counts on the GPU, one per problem) the grouped product over a
-    mixture of experts' slabs.  The result is float32 (default), float16 or bfloat16; ``activation`` as for ``matmul``.
+    mixture of experts' slabs.  The result is float32 (default), float16 or bfloat16; ``activation`` as for ``matmul``,
+    but a NaN stays NaN.
     """
     if a.dim() not in (2, 3) or b.dim() not in (2, 3):
         _bad("a and b must be 2-D or 3-D")

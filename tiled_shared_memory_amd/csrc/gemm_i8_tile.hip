@@ -192,7 +192,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
       for (int i = 0; i < 8; ++i) {
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = ep.apply((float)acc.v[i][j2][e] * ca[i] * cb[j2][e]);
+        for (int e = 0; e < 4; ++e) v[e] = act_i8(ep, (float)acc.v[i][j2][e] * ca[i] * cb[j2][e]);
         *reinterpret_cast<u32x2 *>(q + (16 * i + t) * 256 + ((32 * j2 + 8 * g) ^ (16 * t))) =
             u32x2{f32_elem<FMT>(v[0]) | (f32_elem<FMT>(v[1]) << 16), f32_elem<FMT>(v[2]) | (f32_elem<FMT>(v[3]) << 16)};
       }
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
       for (int i = 0; i < 8; ++i) {
         f32x4 v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = ep.apply((float)acc.v[i][j2][e] * ca[i] * cb[j2][e]);
+        for (int e = 0; e < 4; ++e) v[e] = act_i8(ep, (float)acc.v[i][j2][e] * ca[i] * cb[j2][e]);
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rc, off + (uint32_t)(16 * i * ldc * 4), 0, 0);
       }
     }

@@ -51,6 +51,13 @@ __device__ __forceinline__ u32x4 load_tail(const int8_t *row, int64_t k, int64_t
   return v;
 }
 
+// The activation of a scaled sum.  Epilogue::apply, except that a NaN stays one
+// with every activation (a token of NaN scale must show in its results).
+__device__ __forceinline__ float act_i8(const Epilogue &ep, float v) {
+  if (ep.act == 0) return v;
+  return v <= 0.f ? (ep.act == 1 ? 0.f : v * ep.slope) : v;
+}
+
 // Four results of one row of C, columns n .. n+3 (n < N): each sum to float32
 // once, times the token's scale, times the channel's, then the activation and
 // the output's rounding.
@@ -59,7 +66,7 @@ __device__ __forceinline__ void store_i8(const I8Args &p, const Epilogue &ep, ch
                                          const float (&sb)[4], i32x4 acc) {
   float v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = ep.apply((float)acc[i] * sa * sb[i]);
+  for (int i = 0; i < 4; ++i) v[i] = act_i8(ep, (float)acc[i] * sa * sb[i]);
   if (p.vec_store && n + 4 <= p.N) {
     if constexpr (FMT == FMT_F32) {
       *reinterpret_cast<f32x4 *>(row + n * 4) = f32x4{v[0], v[1], v[2], v[3]};
