@@ -476,3 +476,15 @@ def test_results_on_a_stream_of_their_own(as_handle):
             got = call(stream=side.cuda_stream if as_handle else side)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
+@pytest.mark.parametrize("T,k", [(10, 3), (5000, 2), (137500, 8)])
+def test_sort_without_experts(T, k):
+    """No experts: every position is -1, however many workgroups the entries take."""
+    import torch
+
+    ids = torch.zeros((T, k), dtype=torch.int64, device="cuda")
+    pos = torch.full((T + 1, k), 7, dtype=torch.int32, device="cuda")
+    say(f"[gpu] sort {T}x{k} of no experts")
+    _, counts = tsm.sort_tokens(ids, 0, 5, positions=pos[:T])
+    assert counts.numel() == 0 and (pos[:T] == -1).all() and (pos[T] == 7).all()

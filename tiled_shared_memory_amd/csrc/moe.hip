@@ -465,9 +465,12 @@ hipError_t backward_fmt(const MoveArgs &a, hipStream_t stream) {
 
 hipError_t launch_sort(const SortArgs &args, hipStream_t stream) {
   SortArgs a = args;
-  const int64_t blocks = sort_blocks(a.tokens * a.topk);
+  // without a workspace (no more entries than one workgroup sorts, or no experts, when there is nothing to count and
+  // any number of workgroups writes its -1s) the tiles are those of one workgroup
+  const int64_t n = a.tokens * a.topk;
+  const int64_t blocks = a.hist ? sort_blocks(n) : n ? (n + SortInfo::kOneBlock - 1) / SortInfo::kOneBlock : 1;
   const size_t lds = (size_t)(kSortWaves + 1) * a.experts * 4;
-  if (blocks > 1) {
+  if (a.hist) {
     if (a.id64)
       hipLaunchKernelGGL(sort_count_kernel<true>, dim3((unsigned)blocks), dim3(kSortThreads), (size_t)a.experts * 4, stream, a);
     else
