@@ -347,7 +347,6 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(MoveArgs a) 
         }
       }
     }
-    if (!a.dweights) continue;
 #pragma unroll
     for (int j = 0; j < JB; ++j) dot[j] = wave_add(dot[j]);
     if constexpr (TPR > 64) {

@@ -42,7 +42,7 @@ struct MoveArgs {
   const float *weights;  // [tokens][topk], or null (ones)
   const float *scale;    // dispatch: a float per token, or null
   float *slab_scale;     // dispatch: a float per slab row
-  float *dweights;       // backward: [tokens][topk], or null
+  float *dweights;       // backward: [tokens][topk]
 };
 hipError_t launch_dispatch(const MoveArgs &a, hipStream_t stream);
 hipError_t launch_combine(const MoveArgs &a, hipStream_t stream);
