@@ -280,3 +280,14 @@ def test_calls_on_a_stream_refuse_tensors_off_the_gpu():
         with pytest.raises(tsm.TsmError) as ei:
             call()
         assert ei.value.status == tsm.TSM_ERROR_INVALID_VALUE and "not on a GPU" in ei.value.detail
+
+
+def test_a_forced_variant_past_its_grid_is_refused(monkeypatch):
+    """4096 x 2050 tiles of 64 x 64 on 512 threads pass 2^32 work-items, 2048 x 1025 of 128 x 128 do not."""
+    args = (262144, 131200, 16, A0, 16, 0, B0, 16, 0, 1 << 60, 131200, 0, 1, None, 1)
+    monkeypatch.setenv("TSM_GEMM_KERNEL", "i8_block_128x128x128")
+    assert tsm.tsm_gemm_i8_kernel_name(*args) == "i8_block_128x128x128"
+    monkeypatch.setenv("TSM_GEMM_KERNEL", "i8_block_64x64x128")
+    assert tsm.tsm_gemm_i8_kernel_name(*args) is None
+    refused(gemm, dict(M=262144, N=131200, K=16, lda=16, ldb=16, ldc=131200, C=1 << 60, dt=1, sca=None, scb=None), 2,
+            "i8_block_64x64x128")

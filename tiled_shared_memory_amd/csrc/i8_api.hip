@@ -140,7 +140,9 @@ int i8_plan(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, int64
     for (I8Kernel k : {I8Kernel::Block128, I8Kernel::Block64, I8Kernel::Tile, I8Kernel::Stream, I8Kernel::Skinny})
       if (strcmp(force, i8_name(k)) == 0) want = k;
     if (want == I8Kernel::None) return fail(TSM_ERROR_INVALID_VALUE, "TSM_GEMM_KERNEL=%s names no kernel", force);
-    if ((want == I8Kernel::Tile && !i8_tile_supports(*p)) || (want == I8Kernel::Stream && !sk.can_stream) ||
+    // (128-tiles fit: they are fewer, and what is checked above where the rule takes them)
+    if ((want == I8Kernel::Block64 && tiles64 * 512 > 0xffffffffLL) ||
+        (want == I8Kernel::Tile && !i8_tile_supports(*p)) || (want == I8Kernel::Stream && !sk.can_stream) ||
         (want == I8Kernel::Skinny && !sk.can_skinny))
       return fail(TSM_ERROR_NOT_SUPPORTED, "TSM_GEMM_KERNEL=%s cannot run this problem", force);
     *kernel = want;
