@@ -469,3 +469,49 @@ def test_a_token_of_nan_shows_in_an_expert_layers_hidden_rows():
     y = tsm.matmul_i8(*tsm.quantize(h), down[0].t(), down[1])
     bad = torch.isnan(y)
     assert bad[2].all() and not bad[[0, 1, 3, 4]].any()
+
+
+def many_counts(G, M, kind):
+    """Row counts of G groups: mixed ones, long runs of empty groups, or the last group alone."""
+    rng = np.random.default_rng(G + M)
+    if kind == "last":
+        rows = np.zeros(G, np.int64)
+        rows[-1] = M
+        return rows
+    rows = rng.choice([0, 1, M // 2, M - 1, M, M + 3, -2], G)
+    if kind == "runs":
+        for z in range(0, G, 64):
+            if z // 64 % 2 == 0:
+                rows[z:z + 64] = 0  # whole trips of the search over 64 counts without a row
+        rows[-1] = max(1, M // 3)
+    return rows
+
+
+@pytest.mark.parametrize("kind", ["mixed", "runs", "last"])
+@pytest.mark.parametrize("G", [65, 200, 513, 600])
+@pytest.mark.parametrize("kernel,M,N,K", [
+    ("i8_stream", 3, 40, 272), ("i8_stream", 16, 100, 528), ("i8_stream", 20, 40, 272), ("i8_stream", 40, 72, 272),
+    ("i8_skinny", 5, 40, 100), ("i8_block_64x64x128", 70, 72, 133), ("i8_block_128x128x128", 130, 136, 133),
+    ("i8_tile_256x256x128", 260, 264, 128), (None, 130, 264, 128)], ids=str)
+def test_many_groups(monkeypatch, kernel, M, N, K, G, kind):
+    """More groups than one trip of the search over the counts (64), than the streaming kernel takes in a launch (512),
+    and (without a forced kernel) the 256-tiles with their second launch; rows past the counts untouched."""
+    import torch
+
+    if kernel:
+        monkeypatch.setenv("TSM_GEMM_KERNEL", kernel)
+    rows = many_counts(G, M, kind)
+    g = torch.Generator(device="cuda").manual_seed(G + M)
+    a = torch.randint(-128, 128, (G, M, K), generator=g, device="cuda", dtype=torch.int8)
+    b = torch.randint(-128, 128, (G, N, K), generator=g, device="cuda", dtype=torch.int8)
+    sa, sb = scales((G, M), g), scales((G, N), g)
+    r = torch.from_numpy(rows.astype(np.int32)).cuda()
+    c = torch.full((G, M, N), 55.0, dtype=torch.float16, device="cuda")
+    name = tsm.tsm_gemm_i8_kernel_name(M, N, K, a, K, M * K, b, K, N * K, c, N, M * N, G, r, 1)
+    say(f"[gpu] i8 {G} groups {kind} {M}x{N}x{K} {name}")
+    assert name == (kernel or "i8_tile_256x256x128")
+    tsm.matmul_i8(a, sa, b.transpose(1, 2), sb, rows=r, out=c)
+    held = torch.arange(M, device="cuda")[None, :] < r[:, None]
+    ref = torch.bmm(a.double(), b.double().transpose(1, 2).contiguous()) * sa.double()[..., None] * sb.double()[:, None]
+    check(c[held], ref[held], "f16")
+    assert (c[~held] == 55.0).all()
