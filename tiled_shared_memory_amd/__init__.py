@@ -111,6 +111,9 @@ def matmul(a, b, *, out=None, out_dtype=None, activation=None, slope=0.01, works
 # ``stream`` (a torch stream or its handle): None is the current stream of the tensors' GPU.  What a call given one
 # allocates is memory of that stream, as inside ``torch.cuda.stream``: another stream waits for it before it uses the
 # result, and ``record_stream`` tells torch of that use.
+#
+# No function here records anything for autograd: results never require a gradient, whatever the inputs do.  Training
+# calls the ``_backward`` functions, for instance from a ``torch.autograd.Function`` of the model's own.
 
 
 def _bad(text):
@@ -362,6 +365,8 @@ def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale
 
     ``out`` keeps its other rows; without it the slabs are allocated with ``slots`` rows (the others unset).  With
     ``scale`` (float32, one per token) also the slab rows' scales: returns (slabs, scales).
+
+    Not recorded for autograd: the gradient of ``x`` is ``dispatch_tokens_backward``.
     """
     if x.dim() != 2:
         _bad("x must be 2-D")
@@ -391,7 +396,10 @@ def dispatch_tokens(x, positions, *, slots=None, out=None, scale=None, out_scale
 
 def combine_tokens(slabs, positions, weights=None, *, out=None, stream=None):
     """Y[t] = sum_j weights[t, j] * slabs[positions[t, j]] over the choices with a position, float32 sums in the order
-    of j; ``weights`` float32 (tokens, topk), None for ones.  Y has the slabs' dtype (float32, float16 or bfloat16)."""
+    of j; ``weights`` float32 (tokens, topk), None for ones.  Y has the slabs' dtype (float32, float16 or bfloat16).
+
+    Not recorded for autograd: the gradients of ``slabs`` and ``weights`` are ``combine_tokens_backward``.
+    """
     _slab_args("slabs", slabs, positions, None, None)
     f = _wants("slabs", slabs, _FLOATS)
     tokens, hidden = positions.shape[0], slabs.shape[1]

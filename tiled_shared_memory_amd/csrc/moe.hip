@@ -205,6 +205,10 @@ __device__ __forceinline__ void place(const MoveArgs &a, int64_t &t, int64_t &c)
   c = (int64_t)seg * (TPR * U) + threadIdx.x % TPR;
 }
 
+// Rows are read and written non-temporally at every size, unlike the combine's (past_caches).  Timed with the grouped
+// product that reads the slabs behind it, non-temporal against cached: 64 x 8 rows of 4096 bf16 (4 MB) 124.1 us
+// against 128.0, 512 x 2 of 4096 int8 codes (4 MB) 34.1 against 34.7, 2048 x 2 of 4096 codes (17 MB) 59.2 against
+// 59.4; 34 MB lose (2048 x 2 of 4096 bf16 95.8 against 94.3, 16384 x 2 of 512 bf16 48.0 against 45.6), 134 MB are equal.
 template <int FMT, int TPR, int U>
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(MoveArgs a) {
   constexpr int ES = fmt_bytes(FMT), N = 16 / ES;
