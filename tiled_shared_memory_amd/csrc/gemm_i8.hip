@@ -9,14 +9,17 @@
 // team's LDS reads with the other's MFMAs where a grid of one workgroup per CU
 // would leave each SIMD a single wave (1024 x 4096 x 4096: 29.1 us, 34.7 with one
 // team; 2048^3 17.3 us, 21.9).  Bound by the slabs' chain of LDS writes, barrier,
-// reads and MFMAs while a CU has one workgroup, by LDS bandwidth once it has two.
+// reads and MFMAs: counters show the MFMAs busy in 20% of the cycles and the LDS in
+// 31% with one workgroup per CU (1024 x 4096 x 4096), 34% and 52% with two (8192^3);
+// a third of the LDS's cycles are bank conflicts.
 //
 // Any sizes and any alignment: a thread's 16 codes come with one load at any
 // byte address; rows past M or N read the last row (their products are never
 // stored); the codes past K are shifted out of the last vectors, so they are
 // zeros in both operands.  Odd row addresses cost memory throughput (1000 x 1500:
-// 12.4 us at K = 777, 7.9 at K = 768); loading the dwords that cover a vector and
-// realigning them took as long (11.7 us; 2047^3 28.4 us against 27.4).
+// 12.4 us at K = 777, 7.9 at K = 768, by the counters 3.3 times the L1 accesses);
+// loading the dwords that cover a vector and realigning them took as long (11.7 us;
+// 2047^3 28.4 us against 27.4).
 // Two slabs ahead; four for up to 128 rows of K >= 4096, where the weights come
 // from memory and a CU has one or two workgroups to wait for them (128 x 8192 x
 // 8192 30.2 us, 34.3 with two; 64 x 16384 x 8192 38.5, 41.4; 64 x 32768 x 8192
@@ -28,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int BK = 128;         // codes per slab
-constexpr int PITCH = BK + 16;  // LDS row pitch: the 16 rows of a fragment read fall on distinct banks
+constexpr int PITCH = BK + 16;  // LDS row pitch, so that a fragment read's rows do not all start on one bank
 
 // D: slabs in flight in registers (even: the LDS buffers alternate).  REST: the
 // workgroups take the quarters of the 256-tiles that whole_rounds leaves.

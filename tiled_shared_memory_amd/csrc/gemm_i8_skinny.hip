@@ -99,7 +99,8 @@ hipError_t skinny_t(const I8Args &p, hipStream_t stream) {
 
 // ---- 16-byte aligned operands, K a multiple of 16 -----------------------------
 // Loading the operand layout straight from memory (above) touches 16 rows per
-// wave-load, and rows a power of two apart fall into one set of the L1 cache.
+// wave-load: four times the L1 accesses of the copies here (16 x 8192 x 8192: 8.4
+// million against 2.1).
 // Here each wave copies its own steps into LDS (rows of 256 bytes, whole lines)
 // and reads the operands from there; nothing is shared until a tile's end, so
 // the loop has no barrier, only the wave's own wait for its oldest copies.  The
@@ -302,14 +303,14 @@ hipError_t stream_t(I8Args a, hipStream_t st) {
 }  // namespace
 
 // Which kernel, and the streaming one's rows per workgroup (16 or 32), blocks of
-// 16 columns and waves.  kernel None: the general one
-// (64 x 64 tiles).  Timed on
+// 16 columns and waves.  kernel None: the general one (64 x 64 tiles).  Timed on
 // weights past the caches; "tiles" are blocks of 16 columns over all problems.
 //  * Operands that the ring's copies cannot take, up to 16 rows: registers while
 //    a CU has one tile (16 x 4096 x 4095 18.0 us against 23.0 in the general
-//    kernel, 16 x 4096 x 8191 31.9 against 40.6); past that 16 rows at odd
-//    addresses crowd the L1 (16 x 8192 x 8191 59.5 against 43.6), and more rows
-//    always (32 x 4096 x 4095 32.6 against 22.9).
+//    kernel, 16 x 4096 x 8191 31.9 against 40.6); past that the L1
+//    accesses of 16 rows at odd addresses, four times those of aligned ones, cost
+//    more (16 x 8192 x 8191 59.5 against 43.6), and those of more rows always
+//    (32 x 4096 x 4095 32.6 against 22.9).
 //  * Others, up to 4 rows of K <= 4096: registers too, since a wave has few steps
 //    and a ring to fill first (4 x 28672 x 4096 24.4 us against 26.7 streamed,
 //    1 x 128256 x 4096 88 against 102; 1 x 65536 x 2048 28.2 against 25.0; at
@@ -321,13 +322,13 @@ hipError_t stream_t(I8Args a, hipStream_t st) {
 //    against 12.6.
 //  * 17-32 rows: 28672 x 4096 30.7 us on two column blocks and one wave, 32.3 on
 //    one and two; 8192 x 8192 23.9 against 19.6.
-//  * 33-64 rows read the weights twice in 32-row blocks (the second time from
-//    L2): 8192 x 8192 26 us against 34 in the general kernel, whose 64 x 64 tiles
-//    win once most CUs have one: 12288 x 4096 23.5 against 21.2, 16384 x 8192 42
-//    against 39, 64 batches of 1024 x 2048 40 against 34, 256 of them 165 against
-//    137.  Grouped calls, whose counts mostly lie far below the capacity, keep 32
-//    (256 groups of 1024 x 2048, 16 rows each of 64: 112 us against 137 in 64-row
-//    blocks).
+//  * 33-64 rows read the weights twice in 32-row blocks (past L2 both times, by
+//    the counters: neighbours run on different XCDs): 8192 x 8192 26 us against
+//    34 in the general kernel, whose 64 x 64 tiles win once most CUs have one:
+//    12288 x 4096 23.5 against 21.2, 16384 x 8192 42 against 39, 64 batches of
+//    1024 x 2048 40 against 34, 256 of them 165 against 137.  Grouped calls, whose
+//    counts mostly lie far below the capacity, keep 32 (256 groups of 1024 x
+//    2048, 16 rows each of 64: 112 us against 137 in 64-row blocks).
 I8Skinny i8_skinny_plan(const I8Args &p) {
   I8Skinny s;
   // (more columns than workgroups of 256 fit a launch go to the general kernel)

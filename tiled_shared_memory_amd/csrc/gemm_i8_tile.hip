@@ -15,11 +15,13 @@
 // by its token's and its channel's scale on the way out; a 16-bit C leaves
 // through LDS as whole non-temporal lines.
 //
-// 8192^3 with bf16 output: 0.371-0.381 ms = 2.9 POP/s, one round of 256 tiles 93 us
-// of which the MFMAs' own time is 55 (the rest: LDS reads and copies at 75% of the
-// LDS bandwidth, the first slabs' wait and the output's stores per round).  The
-// scales are requested together at the end of the loop; one column block after
-// another they cost 3% (0.382 against 0.371 ms on one box).
+// 8192^3 with bf16 output: 0.371-0.397 ms = 2.8-3.0 POP/s over boxes.  The MFMAs'
+// own time is 55 us of the 93 per round of 256 tiles at 2.4 GHz; under sustained
+// load the clock is lower, and by the counters the MFMAs are busy in 72% of its
+// cycles, the LDS with reads in 20% (3% of that bank conflicts).  What is left is
+// waits: at each slab's barrier, for the first slabs and the output's stores of
+// each round.  The scales are requested together at the end of the loop; one column
+// block after another they cost 3% (0.382 against 0.371 ms on one box).
 #include "i8_common.hpp"
 #include "lds_ring.hpp"
 
