@@ -1,6 +1,7 @@
 /*
  * tsm_gemm.h -- C ABI of the MI355X (gfx950) blocked GEMM library.
- * (The int8 products and the expert routing have a section of their own below.)
+ * (The int8 and 4-bit products, the expert routing and the router have sections of
+ * their own below.)
  *
  * The operation is the blocked matrix product C = A.B with 16-bit floating-point
  * operands (f16 or bf16), float32 accumulation and a float32 or f16 result.  It
@@ -440,6 +441,131 @@ int moe_combine(int64_t tokens, int64_t topk, int64_t hidden, const void *slabs,
 int moe_combine_backward(int64_t tokens, int64_t topk, int64_t hidden, const void *dY, int64_t lddy, const void *slabs,
                          int64_t ld_slabs, int64_t slots, int dtype, const int32_t *positions, const float *weights,
                          void *dslabs, int64_t ld_dslabs, float *dweights, void *stream);
+
+/* ---- Microscaled 4-bit products --------------------------------------------------
+ * A row of C elements in microscaled 4-bit form (mx4: the MXFP4 of the OCP
+ * Microscaling Formats specification) is
+ *   codes  : (C + 1) / 2 bytes, element 2i in the low half of byte i and 2i + 1 in
+ *            the high half: bit 3 the sign, bits 0..2 one of 0, 0.5, 1, 1.5, 2, 3,
+ *            4, 6.  The last high half of an odd C is 0 and is never looked at.
+ *   scales : (C + 31) / 32 bytes, one per block of 32 elements: E stands for
+ *            2^(E - 127), and 255 for a block of NaN whatever its codes.
+ * Leading dimensions and strides of codes and scales are in bytes; neither needs
+ * any alignment (rows at multiples of 16 and 4 bytes are faster to read).
+ *
+ * mx4_quantize -- rows to that form: of each block's largest magnitude m
+ *     E := max(0, 127 + floor(log2 m) - 2),   code := nearest to |X| / 2^(E - 127),
+ * ties to the even code, magnitudes above 6 (m up to 8 scales) to 6.  A block of
+ * zeros gets E = 0; one that holds a NaN or an infinity E = 255 and codes of 0, so
+ * every product with it is NaN.
+ *   R, C       : rows and elements per row, of each of `groups` matrices.
+ *   layout     : TSM_ROW: X[g*strideX + r*ldx + c]; TSM_COL: X[g*strideX + c*ldx + r]
+ *                (blocks along the rows of the stored matrix: the operands of a
+ *                weight gradient).  Format xdtype (TSM_F32, TSM_F16 or TSM_BF16).
+ *   rows       : NULL, or a DEVICE array of `groups` int32 counts: rows at and past
+ *                rows[g] are neither read nor written.
+ * Errors and stream semantics as for quantize_i8.
+ */
+int mx4_quantize(int64_t R, int64_t C, const void *X, int64_t ldx, int layout, int64_t strideX, int xdtype, uint8_t *Q,
+                 int64_t ldq, int64_t strideQ, uint8_t *scale, int64_t ld_scale, int64_t stride_scale,
+                 const int32_t *rows, int64_t groups, void *stream);
+
+/* mx4_dequantize -- the values of codes and scales, Y[g*strideY + r*ldy + c], each
+ * rounded once to ydtype (to infinity where it is too large for that). */
+int mx4_dequantize(int64_t R, int64_t C, const uint8_t *Q, int64_t ldq, int64_t strideQ, const uint8_t *scale,
+                   int64_t ld_scale, int64_t stride_scale, void *Y, int64_t ldy, int64_t strideY, int ydtype,
+                   const int32_t *rows, int64_t groups, void *stream);
+
+/*
+ * gemm_mx4 -- C[i][j] := sum_k A[i][k] * B[j][k] for operands in mx4 form, A of M
+ * rows and B of N rows (a weight stored N x K) of K elements each.  Products of two
+ * elements are exact, sums are float32; |C - exact| <= K * 2^-24 * sum |a b|, plus
+ * the rounding to out_dtype (TSM_F32, TSM_F16 or TSM_BF16).  K = 0 gives zeros.
+ * Errors and stream semantics as for gemm; C must not overlap an operand.
+ */
+int gemm_mx4(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const uint8_t *scale_a, int64_t ld_sa,
+             const uint8_t *B, int64_t ldb, const uint8_t *scale_b, int64_t ld_sb, void *C, int64_t ldc, int out_dtype,
+             void *stream);
+
+/* gemm_mx4_strided_batched, gemm_mx4_grouped -- as gemm_i8_strided_batched and
+ * gemm_i8_grouped: `batch` products at strides (0 shares an operand), or experts'
+ * slabs with row counts in device memory; an activation, in which a NaN stays one. */
+int gemm_mx4_strided_batched(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int64_t strideA,
+                             const uint8_t *scale_a, int64_t ld_sa, int64_t stride_sa, const uint8_t *B, int64_t ldb,
+                             int64_t strideB, const uint8_t *scale_b, int64_t ld_sb, int64_t stride_sb, void *C,
+                             int64_t ldc, int64_t strideC, int64_t batch, int out_dtype, int activation, float slope,
+                             void *stream);
+int gemm_mx4_grouped(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int64_t strideA,
+                     const uint8_t *scale_a, int64_t ld_sa, int64_t stride_sa, const uint8_t *B, int64_t ldb,
+                     int64_t strideB, const uint8_t *scale_b, int64_t ld_sb, int64_t stride_sb, void *C, int64_t ldc,
+                     int64_t strideC, const int32_t *rows, int64_t groups, int out_dtype, int activation, float slope,
+                     void *stream);
+
+/*
+ * gemm_mx4_float_a -- mx4_quantize of activations X (TSM_ROW, format xdtype) and
+ * their product with B in one call: the same bits as the two calls.
+ *   rows      : NULL (a strided batch, strideX = 0 shares X), or counts as
+ *               gemm_mx4_grouped takes them.
+ *   workspace : DEVICE memory of gemm_mx4_float_a_workspace_bytes(M, K, batch)
+ *               bytes (with strideX = 0, of batch 1), 16-byte aligned, overlapping
+ *               nothing else, its contents irrelevant before and after.  Calls in
+ *               flight at once must not share one.
+ */
+int gemm_mx4_float_a(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx, int64_t strideX, int xdtype,
+                     const uint8_t *B, int64_t ldb, int64_t strideB, const uint8_t *scale_b, int64_t ld_sb,
+                     int64_t stride_sb, void *C, int64_t ldc, int64_t strideC, int64_t batch, const int32_t *rows,
+                     int out_dtype, int activation, float slope, void *workspace, int64_t workspace_bytes,
+                     void *stream);
+int64_t gemm_mx4_float_a_workspace_bytes(int64_t M, int64_t K, int64_t batch);
+
+/* tsm_gemm_mx4_kernel_name -- the kernel a gemm_mx4_strided_batched call (rows
+ * NULL) or a gemm_mx4_grouped call would launch, or NULL. */
+const char *tsm_gemm_mx4_kernel_name(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int64_t strideA,
+                                     const uint8_t *scale_a, int64_t ld_sa, int64_t stride_sa, const uint8_t *B,
+                                     int64_t ldb, int64_t strideB, const uint8_t *scale_b, int64_t ld_sb,
+                                     int64_t stride_sb, void *C, int64_t ldc, int64_t strideC, int64_t batch,
+                                     const int32_t *rows, int out_dtype);
+
+/* ---- Expert router --------------------------------------------------------------- */
+#define TSM_SCORE_SOFTMAX 0
+#define TSM_SCORE_SIGMOID 1
+
+/*
+ * moe_route -- each token's experts and their weights, from the router's logits
+ * x (tokens x experts, format TSM_F32, TSM_F16 or TSM_BF16):
+ *   scores  : s_e = exp(x_e) / sum exp(x), or 1 / (1 + exp(-x_e)).
+ *   bias    : NULL, or a DEVICE float32 per expert, added to the scores to choose
+ *             (the key s_e + bias_e) and not to weigh (a bias for balance).
+ *   groups  : the experts stand in `groups` groups of equal size, one after another;
+ *             only those of the top_groups groups are chosen from whose group_best
+ *             (1 or 2) largest keys have the largest sum.  top_groups = groups: from all.
+ *   ids     : the topk experts of the largest keys, in that order (what moe_sort takes).
+ *   weights : factor * s_e, or with renormalize factor * s_e over the sum of the
+ *             chosen experts' s (finite, however small those are).
+ * Equal keys (and sums) go to the lowest index.  The choice is the one of exact
+ * scores, up to differences below 2^-50.  An expert whose logit (or bias) is -inf
+ * or NaN is never chosen, and where none is left the id is -1 and the weight 0: a
+ * padded token with a row of -inf gets no expert.  A row with a NaN (or, for a
+ * softmax, +inf) among its logits gets weights of NaN; its ids are those of its
+ * largest logits, whatever the bias and the groups.
+ * experts at most 512, topk and the groups to choose from at most 64, topk at most
+ * the experts of top_groups groups.  ids and weights are tokens x topk, packed.
+ */
+int moe_route(int64_t tokens, int64_t experts, int64_t topk, const void *logits, int64_t ld_logits, int dtype,
+              int scores, const float *bias, int64_t groups, int64_t top_groups, int group_best, int renormalize,
+              float factor, int32_t *ids, float *weights, void *stream);
+
+/*
+ * moe_route_backward -- the gradient of the logits from that of the weights, for
+ * chosen ids (which, and with them the bias, take no gradient):
+ *     dlogits[t][e] := sum_j dweights[t][j] * d weights[t][j] / d x_e,
+ * float32 sums, rounded once to the logits' format.  Ids outside [0, experts) have
+ * no weight; an id may occur more than once in a token's row.  An expert of logit
+ * -inf gets 0.  dlogits is written whole and must not overlap an input.
+ */
+int moe_route_backward(int64_t tokens, int64_t experts, int64_t topk, const float *dweights, const void *logits,
+                       int64_t ld_logits, int dtype, const int32_t *ids, int scores, int renormalize, float factor,
+                       void *dlogits, int64_t ld_dlogits, void *stream);
 
 /* Static text for a status code ("success", "invalid value", ...). */
 const char *tsm_status_string(int status);

@@ -1,0 +1,377 @@
+"""Microscaled 4-bit quantisation and products on the GPU, against float64.
+
+Codes, scales and values are compared bit for bit.  Products of two elements are
+exact, so a product carries the roundings of its float32 sums: at most K of them,
+each 2^-24 of the sum of magnitudes; a leaky ReLU adds one, a 16-bit output half
+a step of its format.
+"""
+
+import math
+
+import pytest
+
+import mx4_ref as ref
+from gpu_util import say
+from mx4_ref import check_product, dtypes
+
+import tiled_shared_memory_amd as tsm
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    import torch
+
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def strided(rows, cols, ld, fill=0xFF, dtype=None):
+    """A (rows, cols) view with leading dimension ld, one element into its buffer when ld is odd; and the buffer."""
+    import torch
+
+    off = ld % 2
+    buf = torch.full((rows * ld + off + 16,), fill, dtype=dtype or torch.uint8, device="cuda")
+    return buf[off:].as_strided((rows, cols), (ld, 1)), buf
+
+
+def operand(rows, C, pad_q, pad_s, g, lo=118, hi=134):
+    """Random codes and scales of rows of C elements in rows with padding, whatever lies behind them 0xff (scales of
+    NaN, odd half bytes that do not count); and their values."""
+    import torch
+
+    kb, nb = (C + 1) // 2, (C + 31) // 32
+    q, _ = strided(rows, kb, kb + pad_q)
+    s, _ = strided(rows, nb, nb + pad_s)
+    q.copy_(torch.randint(0, 256, (rows, kb), generator=g, device="cuda", dtype=torch.uint8))
+    s.copy_(torch.randint(lo, hi, (rows, nb), generator=g, device="cuda", dtype=torch.uint8))
+    return q, s, ref.values(q, s, C)
+
+
+# ---- quantisation ---------------------------------------------------------------------------------------------
+
+
+def special(rows, C, dtype, g):
+    """Values over the whole range: ties, blocks of zeros, of subnormals, of the largest, of NaN and infinities."""
+    import torch
+
+    x = torch.randn((rows, C), generator=g, device="cuda")
+    kind = torch.randint(0, 8, (rows, (C + 31) // 32), generator=g, device="cuda").repeat_interleave(32, -1)[:, :C]
+    grid = torch.tensor([0, 0.125, 0.25, 0.375, 0.5, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 5.5, 6, 7, 7.5], device="cuda")
+    ties = grid[torch.randint(0, 15, (rows, C), generator=g, device="cuda")] * torch.sign(x)
+    x = torch.where(kind == 1, ties, x)
+    x = torch.where(kind == 2, 0.0 * x, x)
+    top = torch.finfo(dtype).max
+    x = torch.where(kind == 3, (x.clamp(-1, 1) * 0.99).double() * top, x.double())
+    x = torch.where(kind == 4, x * torch.finfo(dtype).smallest_normal, x)
+    x = torch.where((kind == 5) & (torch.rand(x.shape, generator=g, device="cuda") < 0.03), math.nan, x)
+    x = torch.where((kind == 6) & (torch.rand(x.shape, generator=g, device="cuda") < 0.03), -math.inf, x)
+    return x.to(dtype)
+
+
+QUANT_SHAPES = [(1, 1), (1, 32), (3, 31), (5, 33), (64, 100), (17, 777), (65, 256), (2, 4096), (300, 1027), (9, 8200),
+                (129, 64), (1, 40000), (4097, 40)]
+
+
+@pytest.mark.parametrize("R,C", QUANT_SHAPES)
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("turned", [False, True], ids=["rows", "columns"])
+def test_quantize(R, C, fmt, turned):
+    """Codes and scales bit for bit, in rows of any alignment whose padding stays as it was."""
+    import torch
+
+    g = gen(R * 3 + C)
+    say(f"[gpu] quantize_mx4 {R}x{C} {fmt} {'columns' if turned else 'rows'}")
+    x = special(R, C, dtypes()[fmt], g)
+    if turned:
+        store, _ = strided(C, R, R + 3, 0, x.dtype)
+        store.copy_(x.t())
+        x = store.t()
+    else:
+        store, _ = strided(R, C, C + 5, 0, x.dtype)
+        store.copy_(x)
+        x = store
+    q, qbuf = strided(R, (C + 1) // 2, (C + 1) // 2 + 3, 0xA5)
+    s, sbuf = strided(R, (C + 31) // 32, (C + 31) // 32 + 2, 0x5A)
+    q0, s0 = qbuf.clone(), sbuf.clone()
+    tsm.quantize_mx4(x, out=q, scale=s)
+    code, e = ref.quantize(x)
+    assert torch.equal(s.long(), e)
+    assert torch.equal(q, ref.pack(code))
+    q.fill_(0xA5)
+    s.fill_(0x5A)
+    assert torch.equal(qbuf, q0) and torch.equal(sbuf, s0)
+
+
+def test_quantize_groups_and_counts():
+    """Only the rows below each count are read (the others hold NaN) and written, in both layouts."""
+    import torch
+
+    g = gen(5)
+    G, R, C = 5, 70, 200
+    rows = torch.tensor([70, 0, 1, 65, 90], dtype=torch.int32, device="cuda")
+    held = torch.arange(R, device="cuda")[None, :] < rows[:, None]
+    x = torch.where(held[..., None], torch.randn((G, R, C), generator=g, device="cuda"), math.nan)
+    code, e = ref.quantize(x)
+    for turned in (False, True):
+        v = x.transpose(1, 2).contiguous().transpose(1, 2) if turned else x
+        q = torch.full((G, R, C // 2), 7, dtype=torch.uint8, device="cuda")
+        s = torch.full((G, R, 7), 9, dtype=torch.uint8, device="cuda")
+        say(f"[gpu] quantize_mx4 groups turned={turned}")
+        tsm.quantize_mx4(v, rows=rows, out=q, scale=s)
+        assert torch.equal(q[held], ref.pack(code)[held]) and torch.equal(s[held].long(), e[held])
+        assert (q[~held] == 7).all() and (s[~held] == 9).all()
+        y = torch.full((G, R, C), 3.0, device="cuda")
+        tsm.dequantize_mx4(q, s, rows=rows, out=y)
+        assert torch.equal(y[held].double(), ref.values(q[held], s[held], C)) and (y[~held] == 3.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+def test_dequantize_every_code_and_scale(fmt):
+    """Every code in every place with every scale, rounded once."""
+    import torch
+
+    q = torch.arange(256, dtype=torch.uint8, device="cuda").repeat(16)[:256 * 16].reshape(1, -1)
+    q = q.expand(256, -1).contiguous()  # 8192 elements a row
+    s = torch.arange(256, dtype=torch.uint8, device="cuda")[:, None].expand(-1, 256).contiguous()
+    say(f"[gpu] dequantize_mx4 every scale {fmt}")
+    y = tsm.dequantize_mx4(q, s, out_dtype=dtypes()[fmt])
+    want = ref.values(q, s, 8192).to(dtypes()[fmt])
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(y), torch.nan_to_num(want))
+    assert torch.equal(torch.signbit(y[:255]), torch.signbit(want[:255]))
+
+
+@pytest.mark.parametrize("R,C", [(1, 1), (3, 31), (33, 777), (5, 8191), (70, 64)])
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+def test_round_trip(R, C, fmt):
+    """Back to values, in rows with padding; quantising them again changes nothing."""
+    import torch
+
+    g = gen(R + C)
+    say(f"[gpu] mx4 round trip {R}x{C} {fmt}")
+    x = torch.randn((R, C), generator=g, device="cuda").to(dtypes()[fmt])
+    q, s = tsm.quantize_mx4(x)
+    y, buf = strided(R, C, C + 3, 3.0, x.dtype)
+    before = buf.clone()
+    tsm.dequantize_mx4(q, s, out=y)
+    assert torch.equal(y.double(), ref.values(q, s, C))
+    again, s2 = tsm.quantize_mx4(y)
+    assert torch.equal(tsm.dequantize_mx4(again, s2, columns=C).double(), y.double())
+    y.fill_(3.0)
+    assert torch.equal(buf, before)
+
+
+# ---- products -------------------------------------------------------------------------------------------------
+
+SHAPES = [  # M, N, K, padding of codes' and scales' rows, ldc - N
+    (1, 1, 1, 0, 0, 0), (1, 8192, 8192, 0, 0, 0), (1, 130, 4096, 0, 0, 0), (1, 33, 15, 0, 0, 0), (3, 100, 17, 1, 2, 3),
+    (16, 512, 2048, 0, 0, 0), (16, 1000, 777, 0, 0, 0), (7, 640, 1024, 16, 16, 0), (33, 65, 129, 3, 1, 0),
+    (64, 128, 128, 0, 0, 0), (48, 4096, 512, 0, 0, 0), (100, 300, 4099, 5, 3, 1), (128, 256, 16384, 0, 0, 0),
+    (256, 256, 8192, 0, 0, 0), (1000, 1500, 777, 0, 0, 0), (513, 770, 1024, 0, 0, 6), (2048, 2560, 1280, 0, 0, 0),
+    (2300, 4104, 640, 16, 4, 8), (2049, 4090, 256, 0, 0, 0), (3000, 5000, 100, 0, 0, 0), (5, 70000, 64, 0, 0, 0),
+    (70000, 5, 64, 0, 0, 0), (40, 40, 100001, 0, 0, 0), (17, 33, 255, 0, 0, 0), (64, 64, 257, 7, 5, 0)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s[:3])) + ("" if not any(s[3:]) else "_ld"))
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+def test_product(shape, out):
+    """Every kernel's shapes; what lies behind the operands' rows does not count, C's padding stays as it was."""
+    import torch
+
+    M, N, K, pq, ps, pc = shape
+    g = gen(M * 7 + N * 3 + K)
+    a, sa, va = operand(M, K, pq, ps, g)
+    b, sb, vb = operand(N, K, pq, ps, g, 112, 124)
+    buf = torch.full((M + 1, N + pc), 77.0, dtype=dtypes()[out], device="cuda")
+    c = buf[:M, :N]
+    name = tsm.tsm_gemm_mx4_kernel_name(M, N, K, a, a.shape[1] + pq, 0, sa, sa.shape[1] + ps, 0, b, b.shape[1] + pq, 0,
+                                        sb, sb.shape[1] + ps, 0, c, N + pc, 0, 1, None, 0)
+    say(f"[gpu] mx4 product {shape} {out} {name}")
+    tsm.gemm_mx4(M, N, K, a, a.shape[1] + pq, sa, sa.shape[1] + ps, b, b.shape[1] + pq, sb, sb.shape[1] + ps, c, N + pc,
+                 {"f32": tsm.TSM_F32, "f16": tsm.TSM_F16, "bf16": tsm.TSM_BF16}[out])
+    check_product(c, *ref.product(va, vb), K, out)
+    assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
+
+
+@pytest.mark.parametrize("act", [None, "relu", "leaky_relu"])
+@pytest.mark.parametrize("M,N,K", [(5, 200, 512), (64, 512, 4096), (300, 520, 777), (2304, 2304, 512)])
+def test_nan_blocks_and_activations(M, N, K, act):
+    """A block of scale 255 makes its row (column) NaN with every activation, whatever its codes; others are sound."""
+    import torch
+
+    g = gen(M + K)
+    a, sa, _ = operand(M, K, 0, 0, g)
+    b, sb, _ = operand(N, K, 0, 0, g, 112, 124)
+    sa[M // 2, -1] = 255
+    sb[N - 1, 0] = 255
+    a[M // 2] = 0  # codes of 0, as the quantisation leaves them
+    say(f"[gpu] mx4 NaN blocks {M}x{N}x{K} {act}")
+    c = tsm.matmul_mx4(a, sa, b.t(), sb, columns=K, activation=act, slope=-0.5)
+    want, mag = ref.product(ref.values(a, sa, K), ref.values(b, sb, K), act, -0.5)
+    bad = torch.isnan(want)
+    assert bad[M // 2].all() and bad[:, N - 1].all() and int(bad.sum()) == M + N - 1
+    assert torch.equal(torch.isnan(c), bad)
+    check_product(c[~bad], want[~bad], mag[~bad], K, "f32", 2.0 ** -24)
+
+
+def test_scales_at_the_ends_of_their_range():
+    """Scales whose product passes float32's range on either side: infinities where the sum is one, no NaN."""
+    import torch
+
+    g = gen(3)
+    for lo, hi in ((0, 3), (250, 255), (0, 255), (60, 190)):
+        a, sa, va = operand(40, 512, 0, 0, g, lo, hi)
+        b, sb, vb = operand(64, 512, 0, 0, g, lo, hi)
+        say(f"[gpu] mx4 scales {lo}..{hi}")
+        c = tsm.matmul_mx4(a, sa, b.t(), sb)
+        want, mag = ref.product(va, vb)
+        ok = mag < 2.0 ** 127
+        assert not torch.isnan(c[ok]).any()
+        check_product(c[ok], want[ok], mag[ok], 512, "f32")
+        far = want.abs() > 2.0 ** 129
+        assert not torch.isfinite(c[far]).any()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 64, 512), (16, 256, 1024), (40, 100, 333), (128, 512, 256), (600, 512, 768)])
+def test_batches_and_groups(M, N, K):
+    """Strided batches, a shared operand either side, and counts: rows past them are neither read nor written."""
+    import torch
+
+    g = gen(M + N + K)
+    G = 5
+    a, sa, va = operand(G * M, K, 0, 0, g)
+    b, sb, vb = operand(G * N, K, 0, 0, g, 112, 124)
+    a3, sa3, va3 = (t.reshape(G, M, -1) for t in (a, sa, va))
+    b3, sb3, vb3 = (t.reshape(G, N, -1) for t in (b, sb, vb))
+    say(f"[gpu] mx4 batches {M}x{N}x{K}")
+    plain = tsm.matmul_mx4(a3, sa3, b3.transpose(1, 2), sb3, columns=K)
+    for z in range(G):
+        check_product(plain[z], *ref.product(va3[z], vb3[z]), K, "f32")
+    shared_b = tsm.matmul_mx4(a3, sa3, b3[0].t(), sb3[0], columns=K)
+    shared_a = tsm.matmul_mx4(a3[0], sa3[0], b3.transpose(1, 2), sb3, columns=K)
+    for z in range(G):
+        check_product(shared_b[z], *ref.product(va3[z], vb3[0]), K, "f32")
+        check_product(shared_a[z], *ref.product(va3[0], vb3[z]), K, "f32")
+    counts = [M, 0, (M + 1) // 2, M + 5, -1]
+    rows = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    stale = torch.arange(M, device="cuda")[None, :] >= rows[:, None]
+    sa3 = torch.where(stale[..., None], 255, sa3.long()).to(torch.uint8)  # scales of NaN where nothing may be read
+    c = torch.full((G, M, N), 55.0, device="cuda")
+    tsm.matmul_mx4(a3, sa3, b3.transpose(1, 2), sb3, columns=K, rows=rows, out=c)
+    assert torch.equal(c[~stale], plain[~stale]) and (c[stale] == 55.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 300, 4096), (1, 64, 33), (5, 100, 777), (16, 512, 2048), (64, 256, 512),
+                                   (500, 512, 1024)])
+def test_product_of_activations(M, N, K, fmt):
+    """Activations quantised within the call: the bits of the two calls, with and without a workspace, in a batch, with
+    a shared operand and with counts."""
+    import torch
+
+    g = gen(M + N + K)
+    x = torch.randn((3, M, K), generator=g, device="cuda").to(dtypes()[fmt])
+    w, ws = tsm.quantize_mx4(torch.randn((3, N, K), generator=g, device="cuda"))
+    say(f"[gpu] mx4 product of activations {M}x{N}x{K} {fmt}")
+    q, s = tsm.quantize_mx4(x)
+    # the codes in rows that the call would use: the same kernel multiplies them
+    want = torch.stack([tsm.matmul_mx4(x[z], None, w[z].t(), ws[z]) for z in range(3)])
+    for z in range(3):
+        check_product(want[z], *ref.product(ref.values(q[z], s[z], K), ref.values(w[z], ws[z], K)), K, "f32")
+    got = tsm.matmul_mx4(x, None, w.transpose(1, 2), ws, workspace=tsm.mx4_workspace_for(x))
+    for z in range(3):
+        check_product(got[z], *ref.product(ref.values(q[z], s[z], K), ref.values(w[z], ws[z], K)), K, "f32")
+    shared = tsm.matmul_mx4(x[0], None, w.transpose(1, 2), ws)
+    for z in range(3):
+        check_product(shared[z], *ref.product(ref.values(q[0], s[0], K), ref.values(w[z], ws[z], K)), K, "f32")
+    counts = [M, 0, (M + 1) // 2]
+    rows = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    stale = torch.arange(M, device="cuda")[None, :] >= rows[:, None]
+    c = torch.full((3, M, N), 55.0, device="cuda")
+    tsm.matmul_mx4(torch.where(stale[..., None], math.nan, x), None, w.transpose(1, 2), ws, rows=rows, out=c)
+    for z, m in enumerate(counts):
+        check_product(c[z, :m], *ref.product(ref.values(q[z, :m], s[z, :m], K), ref.values(w[z], ws[z], K)), K, "f32")
+        assert (c[z, m:] == 55.0).all()
+
+
+def test_empty_sums_and_sizes():
+    import torch
+
+    a, b = torch.empty((3, 0), dtype=torch.uint8, device="cuda"), torch.empty((0, 5), dtype=torch.uint8, device="cuda")
+    s, t = torch.empty((3, 0), dtype=torch.uint8, device="cuda"), torch.empty((5, 0), dtype=torch.uint8, device="cuda")
+    say("[gpu] mx4 empty")
+    c = torch.full((3, 5), 9.0, device="cuda")
+    assert (tsm.matmul_mx4(a, s, b, t, out=c) == 0).all()
+    c.fill_(9.0)
+    assert (tsm.matmul_mx4(torch.empty((3, 0), device="cuda"), None, b, t, out=c) == 0).all()
+    q, e = tsm.quantize_mx4(torch.empty((0, 40), device="cuda"))
+    assert q.shape == (0, 20) and e.shape == (0, 2)
+    assert tsm.matmul_mx4(q, e, b.new_empty((20, 5)).t().contiguous().t(), t.new_empty((5, 2))).shape == (0, 5)
+
+
+def test_operands_past_4_gib():
+    """Codes, scales, results and activations whose offsets pass 32 bits."""
+    import torch
+
+    g = gen(8)
+    K, N, M = 256, 64, 96
+    step = (1 << 32) + 4096
+    say("[gpu] mx4 operands past 4 GiB")
+    big = torch.zeros(step + (1 << 20), dtype=torch.uint8, device="cuda")
+
+    def far(rows, cols):
+        return big.as_strided((2, rows, cols), (step, cols, 1))
+
+    b, sb = tsm.quantize_mx4(torch.randn((2, N, K), generator=g, device="cuda"))
+    x = torch.randn((2, M, K), generator=g, device="cuda")
+    a, sa = tsm.quantize_mx4(x)
+    want = tsm.matmul_mx4(a, sa, b.transpose(1, 2), sb)
+    for what, t in (("b", b), ("sb", sb), ("a", a), ("sa", sa)):
+        v = far(t.shape[1], t.shape[2])
+        v.copy_(t)
+        p = {"a": a, "sa": sa, "b": b, "sb": sb, what: v}
+        assert torch.equal(tsm.matmul_mx4(p["a"], p["sa"], p["b"].transpose(1, 2), p["sb"]), want), what
+    c = big.view(torch.float32).as_strided((2, M, N), (step // 4, N, 1))
+    tsm.matmul_mx4(a, sa, b.transpose(1, 2), sb, out=c)
+    assert torch.equal(c, want)
+    xs = big.view(torch.float32).as_strided((2, M, K), (step // 4, K, 1))
+    xs.copy_(x)
+    q, s = tsm.quantize_mx4(xs)
+    assert torch.equal(q, a) and torch.equal(s, sa)
+    # rows that lie a GiB apart
+    wide = big.as_strided((3, K // 2), (step // 3 // 16 * 16, 1))
+    wide.copy_(a[0, :3])
+    assert torch.equal(tsm.matmul_mx4(wide, sa[0, :3].contiguous(), b[0].t(), sb[0]),
+                       tsm.matmul_mx4(a[0, :3].contiguous(), sa[0, :3].contiguous(), b[0].t(), sb[0]))
+
+
+def test_calls_on_another_stream_and_captured():
+    """On a stream of their own, with the memory that they allocate there; captured, and replayed over new inputs."""
+    import torch
+
+    g = gen(11)
+    M, N, K = 24, 512, 1024
+    w, ws = tsm.quantize_mx4(torch.randn((N, K), generator=g, device="cuda"))
+    x = torch.randn((M, K), generator=g, device="cuda")
+    want = tsm.matmul_mx4(x, None, w.t(), ws)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    say("[gpu] mx4 streams")
+    busy = torch.randn((4096, 4096), device="cuda")
+    for _ in range(8):
+        busy = busy @ busy * 1e-3  # the current stream is busy; the side stream does not wait for it
+    got = tsm.matmul_mx4(x, None, w.t(), ws, stream=side)
+    q, s = tsm.quantize_mx4(x, stream=side)
+    y = tsm.dequantize_mx4(q, s, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(y.double(), ref.values(q, s, K))
+    torch.cuda.synchronize()
+    room, c = tsm.mx4_workspace_for(x), torch.empty((M, N), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tsm.matmul_mx4(x, None, w.t(), ws, out=c, workspace=room)
+    for k in range(4):
+        x.copy_(torch.randn((M, K), generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c, tsm.matmul_mx4(x, None, w.t(), ws)), k

@@ -12,12 +12,15 @@ from __future__ import annotations
 from ._lib import (TSM_ACT_LEAKY_RELU, TSM_ACT_NONE, TSM_ACT_RELU, TSM_BF16, TSM_BF16_BF16,  # noqa: F401
                    TSM_BF16_F16, TSM_BF16_F32, TSM_COL, TSM_ERROR_INVALID_VALUE, TSM_ERROR_LAUNCH,
                    TSM_ERROR_NOT_SUPPORTED, TSM_F16, TSM_F16_BF16, TSM_F16_F16, TSM_F16_F32, TSM_F32, TSM_I8, TSM_I32,
-                   TSM_I64, TSM_ROW, TSM_ROWSUM_BF16, TSM_ROWSUM_F16, TSM_ROWSUM_F32, TSM_SUCCESS, TsmError,
-                   _check, _lookups, gemm, gemm_ex, gemm_grouped, gemm_i8, gemm_i8_grouped, gemm_i8_strided_batched,
+                   TSM_I64, TSM_ROW, TSM_ROWSUM_BF16, TSM_ROWSUM_F16, TSM_ROWSUM_F32, TSM_SCORE_SIGMOID,
+                   TSM_SCORE_SOFTMAX, TSM_SUCCESS, TsmError, _check, _lookups, gemm, gemm_ex, gemm_grouped, gemm_i8,
+                   gemm_i8_grouped, gemm_i8_strided_batched, gemm_mx4, gemm_mx4_float_a,
+                   gemm_mx4_float_a_workspace_bytes, gemm_mx4_grouped, gemm_mx4_strided_batched,
                    gemm_noalloc_scratch_bytes, gemm_strided_batched, gemm_strided_batched_act, gemm_strided_batched_ex,
                    gemm_strided_batched_noalloc, gemm_strided_batched_ws, gemm_workspace_bytes, load, moe_combine,
-                   moe_combine_backward, moe_dispatch, moe_sort, moe_sort_workspace_bytes, quantize_i8, rowsum,
-                   tsm_gemm_grouped_kernel_name, tsm_gemm_i8_kernel_name, tsm_gemm_kernel_name,
+                   moe_combine_backward, moe_dispatch, moe_route, moe_route_backward, moe_sort,
+                   moe_sort_workspace_bytes, mx4_dequantize, mx4_quantize, quantize_i8, rowsum,
+                   tsm_gemm_grouped_kernel_name, tsm_gemm_i8_kernel_name, tsm_gemm_kernel_name, tsm_gemm_mx4_kernel_name,
                    tsm_gemm_ws_kernel_name, tsm_last_error_detail, tsm_rowsum_kernel_name, tsm_status_string)
 
 
@@ -444,3 +447,232 @@ def combine_tokens_backward(dy, slabs, positions, weights=None, *, out=None, dwe
              _rows_ld("slabs", slabs), slabs.shape[0], f, positions.data_ptr(), _at(weights), out.data_ptr(),
              _rows_ld("out", out), dweights.data_ptr()))
     return out, dweights
+
+
+# ---- microscaled 4-bit products and the expert router --------------------------------------------------------------
+
+
+def _u8(what, t, shape):
+    import torch
+
+    if t.dtype != torch.uint8:
+        _bad(f"{what} has dtype {t.dtype}, torch.uint8 wanted")
+    if t.shape != shape:
+        _bad(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} wanted")
+
+
+def _group_stride(t, groups):
+    return t.stride(0) if t.dim() == 3 and groups > 1 else 0
+
+
+def _group_rows(rows, groups):
+    if rows is not None:
+        _wants("rows", rows, (TSM_I32,), (groups,))
+        _packed("rows", rows)
+
+
+def quantize_mx4(x, *, rows=None, out=None, scale=None, stream=None):
+    """(codes, scales) of the rows of ``x`` (..., R, C) in float32, float16 or bfloat16, in microscaled 4-bit form
+    (see ``include/tsm_gemm.h``): uint8 of shapes (..., R, ceil(C / 2)) and (..., R, ceil(C / 32)).
+
+    2-D or 3-D, row-major or column-major in its last two dims (``x.t()``: blocks along the rows of what is stored).
+    With ``rows`` (int32, one count per matrix of a 3-D ``x``, on the GPU) only the first rows of each are read and
+    written.  A block with a NaN or an infinity becomes one of NaN.
+    """
+    if x.dim() not in (2, 3):
+        _bad("x must be 2-D or 3-D")
+    f = _wants("x", x, _FLOATS)
+    R, C = x.shape[-2], x.shape[-1]
+    G = x.shape[0] if x.dim() == 3 else 1
+    q_shape, s_shape = (*x.shape[:-1], (C + 1) // 2), (*x.shape[:-1], (C + 31) // 32)
+    if out is None:
+        out = _new(x, q_shape, "uint8", stream)
+    if scale is None:
+        scale = _new(x, s_shape, "uint8", stream)
+    _u8("out", out, q_shape)
+    _u8("scale", scale, s_shape)
+    _group_rows(rows, G)
+    layout, ldx = TSM_ROW, max(1, C)
+    if x.numel():
+        if C == 1 or x.stride(-1) == 1:
+            ldx = x.stride(-2) if R > 1 else max(1, C)
+        elif R == 1 or x.stride(-2) == 1:
+            layout, ldx = TSM_COL, x.stride(-1)
+        else:
+            _bad("x must be row- or column-major in its last two dims")
+    _launch("mx4_quantize", stream, (x, out, scale, rows),
+            (R, C, x.data_ptr(), ldx, layout, _group_stride(x, G), f, out.data_ptr(), _rows_ld("out", out),
+             _group_stride(out, G), scale.data_ptr(), _rows_ld("scale", scale), _group_stride(scale, G), _at(rows), G))
+    return out, scale
+
+
+def dequantize_mx4(codes, scales, *, columns=None, rows=None, out=None, out_dtype=None, stream=None):
+    """The values of microscaled 4-bit ``codes`` and ``scales`` (as ``quantize_mx4`` returns them), float32 (default),
+    float16 or bfloat16, each rounded once.
+
+    ``columns`` elements a row: where neither it nor ``out`` says, two per byte of codes.  ``rows`` as for
+    ``quantize_mx4``.
+    """
+    if codes.dim() not in (2, 3):
+        _bad("codes must be 2-D or 3-D")
+    C = columns if columns is not None else out.shape[-1] if out is not None else 2 * codes.shape[-1]
+    shape = (*codes.shape[:-1], C)
+    G = codes.shape[0] if codes.dim() == 3 else 1
+    if out is None:
+        out = _new(codes, shape, out_dtype or "float32", stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        _bad(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
+    f = _wants("out", out, _FLOATS, shape)
+    _u8("codes", codes, (*shape[:-1], (C + 1) // 2))
+    _u8("scales", scales, (*shape[:-1], (C + 31) // 32))
+    _group_rows(rows, G)
+    _launch("mx4_dequantize", stream, (codes, scales, out, rows),
+            (codes.shape[-2], C, codes.data_ptr(), _rows_ld("codes", codes), _group_stride(codes, G),
+             scales.data_ptr(), _rows_ld("scales", scales), _group_stride(scales, G), out.data_ptr(),
+             _rows_ld("out", out), _group_stride(out, G), f, _at(rows), G))
+    return out
+
+
+def mx4_workspace_for(a):
+    """A CUDA tensor for ``matmul_mx4(a, None, ..., workspace=...)`` of activations ``a``."""
+    G = a.shape[0] if a.dim() == 3 else 1
+    return _new(a, (max(16, gemm_mx4_float_a_workspace_bytes(a.shape[-2], a.shape[-1], G)),), "uint8", None)
+
+
+def matmul_mx4(a, scale_a, b, scale_b, *, columns=None, rows=None, out=None, out_dtype=None, activation=None,
+               slope=0.01, workspace=None, stream=None):
+    """C = act(A.B) of operands in microscaled 4-bit form, or of activations and such a weight.
+
+    ``a`` are codes (..., M, ceil(K / 2)) with their scales ``scale_a`` (..., M, ceil(K / 32)), both uint8 with
+    contiguous rows; or, with ``scale_a`` None, float32, float16 or bfloat16 activations (..., M, K), which the call
+    quantises as ``quantize_mx4`` does, through a ``workspace`` (see ``mx4_workspace_for``; allocated where none is
+    given).  ``b`` (..., ceil(K / 2), N) is column-major (``q.transpose(-1, -2)`` of a weight's codes, stored N x K),
+    ``scale_b`` its scales as ``quantize_mx4`` returns them (..., N, ceil(K / 32)).  K is that of the activations, or
+    ``columns``, or two per byte of codes (the last half byte of an odd K holds 0 as ``quantize_mx4`` leaves it).
+    Batches, ``rows``, results and ``activation`` as for ``matmul_i8``.
+    """
+    if a.dim() not in (2, 3) or b.dim() not in (2, 3):
+        _bad("a and b must be 2-D or 3-D")
+    floats = scale_a is None
+    _u8("b", b, b.shape)
+    if floats:
+        fx = _wants("a", a, _FLOATS)
+        K = a.shape[-1]
+    else:
+        K = 2 * a.shape[-1] if columns is None else columns
+        _u8("a", a, (*a.shape[:-1], (K + 1) // 2))
+    if columns is not None and K != columns:
+        _bad(f"columns is {columns}, a has {K}")
+    M, KB, NB, N = a.shape[-2], (K + 1) // 2, (K + 31) // 32, b.shape[-1]
+    if b.shape[-2] != KB:
+        _bad(f"inner sizes differ: {KB} bytes of codes vs {b.shape[-2]}")
+    batched = a.dim() == 3 or b.dim() == 3
+    ba, bb = (a.shape[0] if a.dim() == 3 else 1), (b.shape[0] if b.dim() == 3 else 1)
+    if ba != bb and ba != 1 and bb != 1:
+        _bad(f"batch sizes differ: {ba} vs {bb}")
+    batch = ba if bb == 1 else bb
+    shape = (batch, M, N) if batched else (M, N)
+    if out is None:
+        out = _new(a, shape, out_dtype or "float32", stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        _bad(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
+    f = _wants("out", out, _FLOATS, shape)
+    if activation not in _ACTIVATIONS:
+        _bad(f"unknown activation {activation!r}")
+    if N > 0 and KB > 1 and b.stride(-2) != 1:
+        _bad("b must be column-major (the transpose of codes stored N x K)")
+    _u8("scale_b", scale_b, (*b.shape[:-2], N, NB))
+    if rows is not None:
+        _group_rows(rows, batch)
+    act = _ACTIVATIONS[activation]
+    weight = (b.data_ptr(), _rows_ld("b", b.transpose(-1, -2)), b.stride(0) if bb > 1 else 0, scale_b.data_ptr(),
+              _rows_ld("scale_b", scale_b), scale_b.stride(0) if bb > 1 else 0)
+    result = (out.data_ptr(), _rows_ld("out", out), out.stride(0) if batched else 0)
+    sa = a.stride(0) if ba > 1 else 0
+    if floats:
+        need = gemm_mx4_float_a_workspace_bytes(M, K, ba) if workspace is None else 0
+        if need:
+            workspace = _new(a, (need,), "uint8", stream)
+        nbytes = 0
+        if workspace is not None:
+            _packed("workspace", workspace)
+            nbytes = workspace.numel() * workspace.element_size()
+        _launch("gemm_mx4_float_a", stream, (a, b, out, scale_b, rows, workspace),
+                (M, N, K, a.data_ptr(), _rows_ld("a", a), sa, fx, *weight, *result, batch, _at(rows), f, act, slope,
+                 _at(workspace), nbytes))
+        return out
+    _u8("scale_a", scale_a, (*a.shape[:-1], NB))
+    codes = (a.data_ptr(), _rows_ld("a", a), sa, scale_a.data_ptr(), _rows_ld("scale_a", scale_a),
+             scale_a.stride(0) if ba > 1 else 0)
+    if rows is None:
+        _launch("gemm_mx4_strided_batched", stream, (a, b, out, scale_a, scale_b),
+                (M, N, K, *codes, *weight, *result, batch, f, act, slope))
+    else:
+        _launch("gemm_mx4_grouped", stream, (a, b, out, scale_a, scale_b, rows),
+                (M, N, K, *codes, *weight, *result, _at(rows), batch, f, act, slope))
+    return out
+
+
+_SCORES = {"softmax": TSM_SCORE_SOFTMAX, "sigmoid": TSM_SCORE_SIGMOID}
+
+
+def route_tokens(logits, topk, *, score="softmax", bias=None, groups=1, top_groups=None, group_best=2,
+                 renormalize=True, factor=1.0, ids=None, weights=None, stream=None):
+    """(ids, weights) of the experts that a router's ``logits`` (tokens, experts) choose for each token, int32 and
+    float32 (tokens, topk), the best first; ``ids`` go to ``sort_tokens``, ``weights`` to ``combine_tokens``.
+
+    ``score`` "softmax" or "sigmoid" of the logits; ``bias`` (float32, one per expert) is added to the scores to
+    choose, not to weigh.  With ``top_groups`` below ``groups`` only experts of the groups with the largest sums of
+    their ``group_best`` (1 or 2) best keys are chosen.  Weights are ``factor`` times the scores, with ``renormalize``
+    over the sum of the chosen ones'.  Ties go to the lowest index.  An expert of logit -inf is never chosen; where
+    none is left the id is -1 and the weight 0.  A NaN among a token's logits makes its weights NaN.
+
+    Not recorded for autograd: the gradient of ``logits`` is ``route_tokens_backward``.
+    """
+    if logits.dim() != 2:
+        _bad("logits must be 2-D")
+    f = _wants("logits", logits, _FLOATS)
+    if score not in _SCORES:
+        _bad(f"unknown score {score!r}")
+    tokens, experts = logits.shape
+    if bias is not None:
+        _wants("bias", bias, (TSM_F32,), (experts,))
+        _packed("bias", bias)
+    if ids is None:
+        ids = _new(logits, (tokens, topk), "int32", stream)
+    if weights is None:
+        weights = _new(logits, (tokens, topk), "float32", stream)
+    _wants("ids", ids, (TSM_I32,), (tokens, topk))
+    _wants("weights", weights, (TSM_F32,), (tokens, topk))
+    _packed("ids", ids)
+    _packed("weights", weights)
+    _launch("moe_route", stream, (logits, bias, ids, weights),
+            (tokens, experts, topk, logits.data_ptr(), _rows_ld("logits", logits), f, _SCORES[score], _at(bias),
+             groups, groups if top_groups is None else top_groups, group_best, bool(renormalize), factor,
+             ids.data_ptr(), weights.data_ptr()))
+    return ids, weights
+
+
+def route_tokens_backward(dweights, logits, ids, *, score="softmax", renormalize=True, factor=1.0, out=None,
+                          stream=None):
+    """The gradient of ``route_tokens``' ``logits``, in their format, from ``dweights`` (float32, tokens x topk): what
+    ``combine_tokens_backward`` gives.  ``ids`` are the chosen experts; they, and the bias, take no gradient."""
+    if logits.dim() != 2:
+        _bad("logits must be 2-D")
+    f = _wants("logits", logits, _FLOATS)
+    if score not in _SCORES:
+        _bad(f"unknown score {score!r}")
+    if ids.dim() != 2 or ids.shape[0] != logits.shape[0]:
+        _bad(f"ids must be 2-D with {logits.shape[0]} rows")
+    _wants("ids", ids, (TSM_I32,))
+    _wants("dweights", dweights, (TSM_F32,), ids.shape)
+    _packed("ids", ids)
+    _packed("dweights", dweights)
+    if out is None:
+        out = _new(logits, logits.shape, logits.dtype, stream)
+    _wants("out", out, (f,), logits.shape)
+    _launch("moe_route_backward", stream, (logits, out, ids, dweights),
+            (logits.shape[0], logits.shape[1], ids.shape[1], dweights.data_ptr(), logits.data_ptr(),
+             _rows_ld("logits", logits), f, ids.data_ptr(), _SCORES[score], bool(renormalize), factor, out.data_ptr(),
+             _rows_ld("out", out)))
+    return out

@@ -46,6 +46,9 @@ TSM_I8 = 3
 TSM_I32 = 4
 TSM_I64 = 5
 
+TSM_SCORE_SOFTMAX = 0
+TSM_SCORE_SIGMOID = 1
+
 # Every function the header declares, with its ctypes signature.
 _I64, _PTR, _INT = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
 SIGNATURES = {
@@ -89,6 +92,24 @@ SIGNATURES = {
     "moe_combine": ([_I64, _I64, _I64, _PTR, _I64, _I64, _INT, _PTR, _PTR, _PTR, _I64, _PTR], _INT),
     "moe_combine_backward": ([_I64, _I64, _I64, _PTR, _I64, _PTR, _I64, _I64, _INT, _PTR, _PTR, _PTR, _I64, _PTR,
                               _PTR], _INT),
+    "mx4_quantize": ([_I64, _I64, _PTR, _I64, _INT, _I64, _INT, _PTR, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _PTR],
+                     _INT),
+    "mx4_dequantize": ([_I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64, _INT, _PTR, _I64, _PTR],
+                       _INT),
+    "gemm_mx4": ([_I64, _I64, _I64, _PTR, _I64, _PTR, _I64, _PTR, _I64, _PTR, _I64, _PTR, _I64, _INT, _PTR], _INT),
+    "gemm_mx4_strided_batched": ([_I64, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64, _PTR,
+                                  _I64, _I64, _PTR, _I64, _I64, _I64, _INT, _INT, ctypes.c_float, _PTR], _INT),
+    "gemm_mx4_grouped": ([_I64, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64,
+                          _PTR, _I64, _I64, _PTR, _I64, _INT, _INT, ctypes.c_float, _PTR], _INT),
+    "gemm_mx4_float_a": ([_I64, _I64, _I64, _PTR, _I64, _I64, _INT, _PTR, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64,
+                          _I64, _I64, _PTR, _INT, _INT, ctypes.c_float, _PTR, _I64, _PTR], _INT),
+    "gemm_mx4_float_a_workspace_bytes": ([_I64, _I64, _I64], _I64),
+    "tsm_gemm_mx4_kernel_name": ([_I64, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64, _PTR, _I64, _I64, _PTR,
+                                  _I64, _I64, _PTR, _I64, _I64, _I64, _PTR, _INT], ctypes.c_char_p),
+    "moe_route": ([_I64, _I64, _I64, _PTR, _I64, _INT, _INT, _PTR, _I64, _I64, _INT, _INT, ctypes.c_float, _PTR,
+                   _PTR, _PTR], _INT),
+    "moe_route_backward": ([_I64, _I64, _I64, _PTR, _PTR, _I64, _INT, _PTR, _INT, _INT, ctypes.c_float, _PTR, _I64,
+                            _PTR], _INT),
 }
 
 
@@ -337,3 +358,77 @@ def moe_combine_backward(tokens, topk, hidden, dY, lddy, slabs, ld_slabs, slots,
     return _check(lib, lib.moe_combine_backward(tokens, topk, hidden, _ptr(dY), lddy, _ptr(slabs), ld_slabs, slots,
                                                 dtype, _ptr(positions), _ptr(weights), _ptr(dslabs), ld_dslabs,
                                                 _ptr(dweights), _stream(stream)))
+
+
+def mx4_quantize(R, C, X, ldx, layout, strideX, xdtype, Q, ldq, strideQ, scale, ld_scale, stride_scale, rows, groups,
+                 stream=None):
+    lib = load()
+    return _check(lib, lib.mx4_quantize(R, C, _ptr(X), ldx, layout, strideX, xdtype, _ptr(Q), ldq, strideQ,
+                                        _ptr(scale), ld_scale, stride_scale, _ptr(rows), groups, _stream(stream)))
+
+
+def mx4_dequantize(R, C, Q, ldq, strideQ, scale, ld_scale, stride_scale, Y, ldy, strideY, ydtype, rows, groups,
+                   stream=None):
+    lib = load()
+    return _check(lib, lib.mx4_dequantize(R, C, _ptr(Q), ldq, strideQ, _ptr(scale), ld_scale, stride_scale, _ptr(Y),
+                                          ldy, strideY, ydtype, _ptr(rows), groups, _stream(stream)))
+
+
+def gemm_mx4(M, N, K, A, lda, scale_a, ld_sa, B, ldb, scale_b, ld_sb, C, ldc, out_dtype, stream=None):
+    lib = load()
+    return _check(lib, lib.gemm_mx4(M, N, K, _ptr(A), lda, _ptr(scale_a), ld_sa, _ptr(B), ldb, _ptr(scale_b), ld_sb,
+                                    _ptr(C), ldc, out_dtype, _stream(stream)))
+
+
+def gemm_mx4_strided_batched(M, N, K, A, lda, strideA, scale_a, ld_sa, stride_sa, B, ldb, strideB, scale_b, ld_sb,
+                             stride_sb, C, ldc, strideC, batch, out_dtype, activation, slope, stream=None):
+    lib = load()
+    return _check(lib, lib.gemm_mx4_strided_batched(M, N, K, _ptr(A), lda, strideA, _ptr(scale_a), ld_sa, stride_sa,
+                                                    _ptr(B), ldb, strideB, _ptr(scale_b), ld_sb, stride_sb, _ptr(C),
+                                                    ldc, strideC, batch, out_dtype, activation, slope,
+                                                    _stream(stream)))
+
+
+def gemm_mx4_grouped(M, N, K, A, lda, strideA, scale_a, ld_sa, stride_sa, B, ldb, strideB, scale_b, ld_sb, stride_sb,
+                     C, ldc, strideC, rows, groups, out_dtype, activation, slope, stream=None):
+    lib = load()
+    return _check(lib, lib.gemm_mx4_grouped(M, N, K, _ptr(A), lda, strideA, _ptr(scale_a), ld_sa, stride_sa, _ptr(B),
+                                            ldb, strideB, _ptr(scale_b), ld_sb, stride_sb, _ptr(C), ldc, strideC,
+                                            _ptr(rows), groups, out_dtype, activation, slope, _stream(stream)))
+
+
+def gemm_mx4_float_a(M, N, K, X, ldx, strideX, xdtype, B, ldb, strideB, scale_b, ld_sb, stride_sb, C, ldc, strideC,
+                     batch, rows, out_dtype, activation, slope, workspace, workspace_bytes, stream=None):
+    lib = load()
+    return _check(lib, lib.gemm_mx4_float_a(M, N, K, _ptr(X), ldx, strideX, xdtype, _ptr(B), ldb, strideB,
+                                            _ptr(scale_b), ld_sb, stride_sb, _ptr(C), ldc, strideC, batch, _ptr(rows),
+                                            out_dtype, activation, slope, _ptr(workspace), workspace_bytes,
+                                            _stream(stream)))
+
+
+def gemm_mx4_float_a_workspace_bytes(M, K, batch):
+    return int(load().gemm_mx4_float_a_workspace_bytes(M, K, batch))
+
+
+def tsm_gemm_mx4_kernel_name(M, N, K, A, lda, strideA, scale_a, ld_sa, stride_sa, B, ldb, strideB, scale_b, ld_sb,
+                             stride_sb, C, ldc, strideC, batch, rows, out_dtype):
+    r = load().tsm_gemm_mx4_kernel_name(M, N, K, _ptr(A), lda, strideA, _ptr(scale_a), ld_sa, stride_sa, _ptr(B), ldb,
+                                        strideB, _ptr(scale_b), ld_sb, stride_sb, _ptr(C), ldc, strideC, batch,
+                                        _ptr(rows), out_dtype)
+    return r.decode() if r else None
+
+
+def moe_route(tokens, experts, topk, logits, ld_logits, dtype, scores, bias, groups, top_groups, group_best,
+              renormalize, factor, ids, weights, stream=None):
+    lib = load()
+    return _check(lib, lib.moe_route(tokens, experts, topk, _ptr(logits), ld_logits, dtype, scores, _ptr(bias), groups,
+                                     top_groups, group_best, renormalize, factor, _ptr(ids), _ptr(weights),
+                                     _stream(stream)))
+
+
+def moe_route_backward(tokens, experts, topk, dweights, logits, ld_logits, dtype, ids, scores, renormalize, factor,
+                       dlogits, ld_dlogits, stream=None):
+    lib = load()
+    return _check(lib, lib.moe_route_backward(tokens, experts, topk, _ptr(dweights), _ptr(logits), ld_logits, dtype,
+                                              _ptr(ids), scores, renormalize, factor, _ptr(dlogits), ld_dlogits,
+                                              _stream(stream)))

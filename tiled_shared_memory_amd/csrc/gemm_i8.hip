@@ -47,16 +47,16 @@ __global__ __launch_bounds__(kThreads) void gemm_i8_block_kernel(I8Args p) {
   int tm, tn;
   int64_t z;
   if constexpr (REST) {
-    const int V = i8_tiles<2 * T>(p), pid = (int)whole_rounds(V, p.cus) + (int)(blockIdx.x >> 2);
+    const int V = tiles_of<2 * T>(p), pid = (int)whole_rounds(V, p.cus) + (int)(blockIdx.x >> 2);
     if (pid >= V) return;  // uniform
-    i8_tile_at<2 * T>(p, pid, i8_tile_group(p), z, tm, tn);
+    tile_at<2 * T>(p, pid, tile_group(p), z, tm, tn);
     tm = 2 * tm + ((int)blockIdx.x >> 1 & 1);
     tn = 2 * tn + ((int)blockIdx.x & 1);
   } else {
-    if (!i8_tile_of<T>(p, 8, z, tm, tn)) return;  // uniform
+    if (!tile_of<T>(p, 8, z, tm, tn)) return;  // uniform
   }
   const int64_t m0 = (int64_t)tm * T, n0 = (int64_t)tn * T;
-  const int64_t M = i8_rows(p, z);
+  const int64_t M = valid_rows(p, z);
   if (REST && (m0 >= M || n0 >= p.N)) return;  // uniform
 
   // the scales, long before they are needed: of the rows this wave stores (see the end) and of its columns

@@ -32,8 +32,8 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_i8_skinny_kernel(I8Arg
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int tm, tn;
   int64_t z;
-  if (!i8_tile_of<16>(p, 1, z, tm, tn)) return;  // uniform
-  const int64_t M = i8_rows(p, z), m0 = (int64_t)tm * 16, n0 = (int64_t)tn * 16;
+  if (!tile_of<16>(p, 1, z, tm, tn)) return;  // uniform
+  const int64_t M = valid_rows(p, z), m0 = (int64_t)tm * 16, n0 = (int64_t)tn * 16;
 
   // rows past M or N read the last one: their results are not stored
   const int64_t mr = m0 + (lane & 15), nr = n0 + (lane & 15);
@@ -123,14 +123,14 @@ __device__ __forceinline__ Place stream_tile(const I8Args &p, int t, const int *
     for (int i = 0; i < p.nz; i += 64) g += __popcll(__ballot(first[i + lane] <= t));
     g = min(g, p.nz) - 1;
     const int f = __builtin_amdgcn_readfirstlane(first[g]);
-    tm = (int)((i8_rows(p, p.z0 + g) + AR - 1) / AR);
+    tm = (int)((valid_rows(p, p.z0 + g) + AR - 1) / AR);
     t -= f;
   } else {
     g = t / (tm * p.tiles_n);
     t -= g * (tm * p.tiles_n);
   }
   e.z = p.z0 + g;
-  e.M = i8_rows(p, e.z);
+  e.M = valid_rows(p, e.z);
   e.m0 = (int64_t)(t % tm) * AR;
   e.n0 = (int64_t)(t / tm) * (16 * NB);
   return e;

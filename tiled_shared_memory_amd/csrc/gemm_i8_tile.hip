@@ -115,7 +115,7 @@ template <int FMT>
 __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
   int tm, tn;
   int64_t z;
-  if (!i8_tile_of<BM, true>(p, i8_tile_group(p), z, tm, tn)) return;  // uniform
+  if (!tile_of<BM, true>(p, tile_group(p), z, tm, tn)) return;  // uniform
   Ctx c;
   c.lane = threadIdx.x & 63;
   c.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
   c.wn = c.wave & 1;
   const int lane = c.lane, wm = c.wm, wn = c.wn;
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
-  const int64_t M = i8_rows(p, z);
+  const int64_t M = valid_rows(p, z);
   const int vr = (int)(M - m0 < BM ? M - m0 : BM), vc = (int)(p.N - n0 < BN ? p.N - n0 : BN);
   // resources over the valid rows of the two panels (rows past them load as zeros); the host keeps each below 1 GiB
   c.ra = make_rsrc(p.A + z * p.strideA + m0 * p.lda, (uint32_t)((vr - 1) * p.lda + p.K));
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
       for (int i = 0; i < 8; ++i) {
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = act_i8(ep, (float)acc.v[i][j2][e] * ca[i] * cb[j2][e]);
+        for (int e = 0; e < 4; ++e) v[e] = act_codes(ep, (float)acc.v[i][j2][e] * ca[i] * cb[j2][e]);
         *reinterpret_cast<u32x2 *>(q + (16 * i + t) * 256 + ((32 * j2 + 8 * g) ^ (16 * t))) =
             u32x2{f32_elem<FMT>(v[0]) | (f32_elem<FMT>(v[1]) << 16), f32_elem<FMT>(v[2]) | (f32_elem<FMT>(v[3]) << 16)};
       }
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(256, 1) void gemm_i8_tile_kernel(I8Args p) {
       for (int i = 0; i < 8; ++i) {
         f32x4 v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = act_i8(ep, (float)acc.v[i][j2][e] * ca[i] * cb[j2][e]);
+        for (int e = 0; e < 4; ++e) v[e] = act_codes(ep, (float)acc.v[i][j2][e] * ca[i] * cb[j2][e]);
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rc, off + (uint32_t)(16 * i * ldc * 4), 0, 0);
       }
     }

@@ -27,13 +27,6 @@ struct I8Args {
   int32_t cus;      // 256 x 256 tiles: CUs, one tile each per round (0: no second launch)
 };
 
-// Rows of problem z (a grouped call's count, clamped to [0, M]).
-__device__ __forceinline__ int64_t i8_rows(const I8Args &p, int64_t z) {
-  if (!p.rows) return p.M;
-  const int64_t r = p.rows[z];
-  return r < 0 ? 0 : (r > p.M ? p.M : r);
-}
-
 // |sum| <= K * 128 * 128 stays below 2^31
 constexpr int64_t kI8MaxK = 131071;
 

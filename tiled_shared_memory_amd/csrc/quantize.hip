@@ -17,6 +17,7 @@
 // The row stays in registers, so it is read once: bound by memory (16384 rows of
 // 4096 bf16 35 us = 5.7 TB/s, 8192 of 8192 32.5 us = 6.2 TB/s; with a division, a
 // rounding and a conversion per element and a workgroup per row 50 us).
+#include "chunk.hpp"
 #include "elems.hpp"
 #include "i8_internal.hpp"
 
@@ -119,55 +120,6 @@ __device__ __forceinline__ bool row_at(const QuantArgs &a, int64_t &z, int64_t &
   if (z >= a.groups || r >= a.R) return false;
   return !a.rows || r < a.rows[z];
 }
-
-// A chunk is 8 elements (16 bytes, or two vectors of float32), kept as loaded; its codes are 8 bytes.
-template <int FMT>
-struct Chunk {
-  static constexpr int V = FMT == FMT_F32 ? 2 : 1;
-  Raw16 raw[V];
-  __device__ __forceinline__ void load(const char *x, int64_t c) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) raw[i] = *(const Raw16 *)(x + (c * V + i) * 16);
-  }
-  // the first n elements at x, zeros behind them
-  __device__ __forceinline__ void load_part(const char *x, int64_t c, int n) {
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = i < n ? elem_bits<FMT>(x, c * 8 + i) : 0u;
-#pragma unroll
-    for (int i = 0; i < 4 * V; ++i)
-      raw[i / 4].d[i % 4] = FMT == FMT_F32 ? w[i] : w[(2 * i) % 8] | (w[(2 * i + 1) % 8] << 16);
-  }
-  __device__ __forceinline__ void values(float (&v)[8]) const {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      Vec<FMT> u;
-      u.unpack(raw[i]);
-#pragma unroll
-      for (int j = 0; j < Vec<FMT>::N; ++j) v[i * Vec<FMT>::N + j] = u.v[j];
-    }
-  }
-  // bits of the largest magnitude as float32 (magnitudes of every format order like their bits)
-  __device__ __forceinline__ uint32_t top() const {
-    if constexpr (FMT == FMT_F32) {
-      uint32_t t = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t = max(t, raw[i / 4].d[i % 4] & 0x7fffffffu);
-      return t;
-    } else {
-      uint32_t lo = 0, hi = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo = max(lo, raw[0].d[i] & 0x7fffu);
-        hi = max(hi, raw[0].d[i] & 0x7fff0000u);
-      }
-      return __builtin_bit_cast(uint32_t, elem_f32<FMT>(max(lo, hi >> 16)));
-    }
-  }
-};
-struct __attribute__((packed, aligned(1))) Raw8 {
-  uint32_t d[2];
-};
 
 // The row stays in registers: TPR threads hold VPT chunks of 8 each.
 template <int FMT, int TPR, int VPT>
