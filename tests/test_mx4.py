@@ -193,6 +193,53 @@ def test_product(shape, out):
     assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,pad", [(256, 256, 256 * n, 0) for n in range(1, 28)]
+                         + [(1, 8, 256, 0), (257, 264, 768, 16), (700, 520, 256, 32), (255, 1032, 3328, 0)])
+def test_large_tiles(monkeypatch, M, N, K, pad, out):
+    """The 256 x 256 kernel, forced: every count of slabs in and after its loop, ragged M and N, padded rows, an
+    activation, a batch, and grouped counts."""
+    import torch
+
+    monkeypatch.setenv("TSM_GEMM_KERNEL", "mx4_tile_256x256x256")
+    g = gen(M + N + K)
+    dt = dtypes()[out]
+    a, sa, va = operand(M, K, pad, pad // 4, g)
+    b, sb, vb = operand(N, K, pad, pad // 4, g, 112, 124)
+    buf = torch.full((M + 1, N + 8), 77.0, dtype=dt, device="cuda")
+    say(f"[gpu] mx4 large tiles {M}x{N}x{K} {out}")
+    tsm.matmul_mx4(a, sa, b.t(), sb, out=buf[:M, :N], activation="leaky_relu", slope=0.5)
+    check_product(buf[:M, :N], *ref.product(va, vb, "leaky_relu", 0.5), K, out, 2.0 ** -24)
+    assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
+    a3, sa3, va3 = (t.reshape(5, M, -1) for t in operand(5 * M, K, 0, 0, g))
+    b3, sb3, vb3 = (t.reshape(5, N, -1) for t in operand(5 * N, K, 0, 0, g, 112, 124))
+    plain = tsm.matmul_mx4(a3, sa3, b3.transpose(1, 2), sb3, out_dtype=dt)
+    rows = torch.tensor([M, 0, M // 2, M + 5, 1], dtype=torch.int32, device="cuda")
+    c = torch.full((5, M, N), 55.0, dtype=dt, device="cuda")
+    tsm.matmul_mx4(a3, sa3, b3.transpose(1, 2), sb3, rows=rows, out=c)
+    for z, m in enumerate([M, 0, M // 2, M, 1]):
+        check_product(plain[z], *ref.product(va3[z], vb3[z]), K, out)
+        assert torch.equal(c[z, :m], plain[z, :m]) and (c[z, m:] == 55.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(4352, 4096, 256), (4100, 4360, 512), (2200, 2304, 768)])
+def test_tiles_past_whole_rounds(M, N, K):
+    """A few 256-tiles more than one per CU (272, 306), or fewer than a round: the two launches together write every
+    element once."""
+    import torch
+
+    g = gen(M)
+    a, sa, va = operand(M, K, 0, 0, g)
+    b, sb, vb = operand(N, K, 0, 0, g, 112, 124)
+    buf = torch.full((M + 1, N + 8), 77.0, dtype=torch.float16, device="cuda")
+    say(f"[gpu] mx4 tiles past whole rounds {M}x{N}x{K}")
+    assert tsm.tsm_gemm_mx4_kernel_name(M, N, K, a, K // 2, 0, sa, K // 32, 0, b, K // 2, 0, sb, K // 32, 0, buf, N + 8,
+                                        0, 1, None, 1) == "mx4_tile_256x256x256"
+    tsm.matmul_mx4(a, sa, b.t(), sb, out=buf[:M, :N])
+    check_product(buf[:M, :N], *ref.product(va, vb), K, "f16")
+    assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
+
+
 @pytest.mark.parametrize("act", [None, "relu", "leaky_relu"])
 @pytest.mark.parametrize("M,N,K", [(5, 200, 512), (64, 512, 4096), (300, 520, 777), (2304, 2304, 512)])
 def test_nan_blocks_and_activations(M, N, K, act):

@@ -19,6 +19,8 @@ const char *mx4_name(Mx4Kernel k) {
       return "mx4_block_128x128x256";
     case Mx4Kernel::Block64:
       return "mx4_block_64x64x256";
+    case Mx4Kernel::Tile:
+      return "mx4_tile_256x256x256";
     default:
       return nullptr;
   }
@@ -47,7 +49,7 @@ int operand_check(char name, int64_t rows, int64_t K, const uint8_t *codes, int6
 struct Call {
   Mx4Args p;
   Mx4Kernel kernel;
-  int64_t c_bytes;
+  bool forced;
 };
 
 // What the products of every form check of their sizes and of C.  false in *work: nothing to compute.
@@ -89,6 +91,7 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
              int64_t ld_sb, int64_t stride_sb, void *C, int64_t ldc, int64_t strideC, int64_t batch,
              const int32_t *rows, bool grouped, int out_dtype, int act, float slope, Call *call) {
   call->kernel = Mx4Kernel::None;
+  call->forced = false;
   int64_t c_bytes = 0;
   bool work;
   int st = result_check(M, N, K, C, ldc, &strideC, batch, rows, grouped, out_dtype, act, slope, &c_bytes, &work);
@@ -142,17 +145,22 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
   const bool small = tiles128 * batch <= 128 || (M <= 64 && tiles64 * 512 <= 0xffffffffLL);
   call->kernel = small ? Mx4Kernel::Block64 : Mx4Kernel::Block128;
   if ((small ? tiles64 : tiles128) * 512 > 0xffffffffLL) return fail(TSM_ERROR_NOT_SUPPORTED, "tile grid too large");
+  const bool half = M <= 128 && tiles128 * batch <= 256;  // 256-tiles half empty, and a round of 128-tiles does it
+  const int64_t tiles256 = ((M + 255) / 256) * ((N + 255) / 256) * batch;
+  if (M > 64 && !half && tiles256 >= kFewTiles && mx4_tile_supports(p)) call->kernel = Mx4Kernel::Tile;
   // TSM_GEMM_KERNEL=<name> forces a variant (tests and tuning); names of other
   // families are left alone, a variant that cannot run the problem is an error.
   const char *force = getenv("TSM_GEMM_KERNEL");
   if (force && strncmp(force, "mx4_", 4) == 0) {
     Mx4Kernel want = Mx4Kernel::None;
-    for (Mx4Kernel k : {Mx4Kernel::Block128, Mx4Kernel::Block64})
+    for (Mx4Kernel k : {Mx4Kernel::Block128, Mx4Kernel::Block64, Mx4Kernel::Tile})
       if (strcmp(force, mx4_name(k)) == 0) want = k;
     if (want == Mx4Kernel::None) return fail(TSM_ERROR_INVALID_VALUE, "TSM_GEMM_KERNEL=%s names no kernel", force);
-    if (want == Mx4Kernel::Block64 && tiles64 * 512 > 0xffffffffLL)
+    if ((want == Mx4Kernel::Block64 && tiles64 * 512 > 0xffffffffLL) ||
+        (want == Mx4Kernel::Tile && !mx4_tile_supports(p)))
       return fail(TSM_ERROR_NOT_SUPPORTED, "TSM_GEMM_KERNEL=%s cannot run this problem", force);
     call->kernel = want;
+    call->forced = true;
   }
   return TSM_SUCCESS;
 }
@@ -169,6 +177,8 @@ int mx4_run(const Call &c, void *stream) {
       return launched(launch_mx4_block(c.p, 128, s));
     case Mx4Kernel::Block64:
       return launched(launch_mx4_block(c.p, 64, s));
+    case Mx4Kernel::Tile:
+      return launched(launch_mx4_tile(c.p, !c.forced, s));
     default:
       return TSM_SUCCESS;
   }

@@ -18,6 +18,16 @@ __device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, uint32_t sa, u32x4 b, uint32_
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(va, vb, c, 4, 4, OA, (int)sa, OB, (int)sb);
 }
 
+// v_mfma_scale_f32_32x32x64_f8f6f4: D(32x32) += A(32x64) * B(64x32), row (column) lane % 32, block lane / 32, byte O of
+// both scale registers.  D as for the 32x32x16 forms.
+template <int O>
+__device__ __forceinline__ f32x16 mfma_mx4_32(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x16 c) {
+  typedef int i32x8 __attribute__((ext_vector_type(8)));
+  const i32x8 va = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 vb = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(va, vb, c, 4, 4, O, (int)sa, O, (int)sb);
+}
+
 // f(0) .. f(N - 1) with constants.
 template <int I>
 struct Const {
