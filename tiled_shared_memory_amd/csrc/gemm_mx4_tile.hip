@@ -240,37 +240,40 @@ __global__ __launch_bounds__(256, 1) void gemm_mx4_tile_kernel(Mx4Args p) {
 
   // ---- epilogue: acc.v[i][j], elements 4 q .. 4 q + 3, holds C[32 i + lane % 32][32 j + 8 q + 4 (lane / 32) + 0..3] of
   // the quadrant
-  const Epilogue ep{p.act, p.slope, false};
   const int r32 = lane & 31, h = lane >> 5, t = lane & 15, g = lane >> 4;
   constexpr int ES = fmt_bytes(FMT);
   const int64_t ldc = p.ldc;
   const __amdgpu_buffer_rsrc_t rc = make_rsrc((char *)p.C + (z * p.strideC + m0 * ldc + n0) * ES,
                                               (uint32_t)(((vr - 1) * ldc + vc) * ES));
+  const Epilogue ep{p.act, p.slope, false};
   if constexpr (FMT != FMT_F32) {
     __syncthreads();  // every wave is past its last fragment read and copy
-    // this wave's quadrant through LDS: 128 rows of 256 bytes, chunk c of row r at c ^ (r % 16)
+    // this wave's quadrant through LDS, 32 rows of 256 bytes at a time, chunk c of row r at c ^ (r % 16)
     char *const q = c.wave == 0 ? s_a0 : c.wave == 1 ? s_a1 : c.wave == 2 ? s_b0 : s_b1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int j2 = 0; j2 < 4; ++j2) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = act_codes(ep, acc.v[i][j2][4 * k + e]);
-          *reinterpret_cast<u32x2 *>(q + (32 * i + r32) * 256 + ((64 * j2 + 16 * k + 8 * h) ^ (16 * t))) =
-              u32x2{f32_elem<FMT>(v[0]) | (f32_elem<FMT>(v[1]) << 16), f32_elem<FMT>(v[2]) | (f32_elem<FMT>(v[3]) << 16)};
-        }
-      }
-    }
     const int col = wn * 128 + 8 * t;
     const uint32_t coff = col < vc ? (uint32_t)(col * 2) : kOutside;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const int row = 4 * k + g;
-      const u32x4 d = *reinterpret_cast<const u32x4 *>(q + row * 256 + (t ^ (row & 15)) * 16);
-      __builtin_amdgcn_raw_buffer_store_b128(d, rc, coff + (uint32_t)((wm * 128 + row) * ldc * 2), 0, kNonTemporal);
+    for (int i = 0; i < 4; ++i) {
+      char *const at = q + i * 8192;
+#pragma unroll
+      for (int j2 = 0; j2 < 4; ++j2) {
+        f32x16 v = acc.v[i][j2];
+        if (p.act) {  // uniform
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = act_codes(ep, v[e]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<u32x2 *>(at + r32 * 256 + ((64 * j2 + 16 * k + 8 * h) ^ (16 * t))) =
+              u32x2{pack2<FMT>(v[4 * k], v[4 * k + 1]), pack2<FMT>(v[4 * k + 2], v[4 * k + 3])};
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int row = 4 * k + g;
+        const u32x4 d = *reinterpret_cast<const u32x4 *>(at + row * 256 + (t ^ (row & 15)) * 16);
+        __builtin_amdgcn_raw_buffer_store_b128(d, rc, coff + (uint32_t)((wm * 128 + i * 32 + row) * ldc * 2), 0,
+                                               kNonTemporal);
+      }
     }
   } else {
 #pragma unroll

@@ -54,6 +54,19 @@ __device__ __forceinline__ u32x4 without_odd(u32x4 v, int64_t at, int64_t K) {
   return v;
 }
 
+// Two float32 values to 16-bit ones side by side, to nearest even (bf16: one instruction for both).
+template <int FMT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  if constexpr (FMT == FMT_BF16) {
+    typedef __bf16 pair __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), pair));
+  } else {
+    typedef _Float16 pair __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), pair));
+  }
+}
+
 // Four results of one row of C, columns n .. n+3 (n < N): activation, rounding, store.
 template <int FMT>
 __device__ __forceinline__ void store_mx4(const Mx4Args &p, const Epilogue &ep, char *row, int64_t n, f32x4 acc) {
