@@ -452,13 +452,41 @@ def combine_tokens_backward(dy, slabs, positions, weights=None, *, out=None, dwe
 # ---- microscaled 4-bit products and the expert router --------------------------------------------------------------
 
 
-def _u8(what, t, shape):
-    import torch
-
-    if t.dtype != torch.uint8:
+def _u8_rows(what, t, shape, groups):
+    """Check a uint8 tensor argument of contiguous rows, of the shape.  Returns its address, leading dimension and group
+    stride (sizes and strides read once: these calls take most of a small product's time)."""
+    if t.dtype is not _uint8():
         _bad(f"{what} has dtype {t.dtype}, torch.uint8 wanted")
     if t.shape != shape:
         _bad(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} wanted")
+    st, C = t.stride(), shape[-1]
+    if C > 1 and st[-1] != 1 and t.numel():
+        _bad(f"{what}: rows must be contiguous")
+    return t.data_ptr(), st[-2] if shape[-2] > 1 and C else max(1, C), st[0] if groups > 1 and len(st) == 3 else 0
+
+
+def _float_rows(what, t, shape, groups):
+    """The same of float32, float16 or bfloat16; and its format."""
+    f = (_FORMATS or _formats()).get(t.dtype)
+    if f not in _FLOATS:
+        _bad(f"{what} has dtype {t.dtype}")
+    if t.shape != shape:
+        _bad(f"{what} has shape {tuple(t.shape)}, {tuple(shape)} wanted")
+    st, C = t.stride(), shape[-1]
+    if C > 1 and st[-1] != 1 and t.numel():
+        _bad(f"{what}: rows must be contiguous")
+    return t.data_ptr(), st[-2] if shape[-2] > 1 and C else max(1, C), st[0] if groups > 1 and len(st) == 3 else 0, f
+
+
+_UINT8 = []
+
+
+def _uint8():
+    if not _UINT8:
+        import torch
+
+        _UINT8.append(torch.uint8)
+    return _UINT8[0]
 
 
 def _group_stride(t, groups):
@@ -489,8 +517,7 @@ def quantize_mx4(x, *, rows=None, out=None, scale=None, stream=None):
         out = _new(x, q_shape, "uint8", stream)
     if scale is None:
         scale = _new(x, s_shape, "uint8", stream)
-    _u8("out", out, q_shape)
-    _u8("scale", scale, s_shape)
+    codes, scales = _u8_rows("out", out, q_shape, G), _u8_rows("scale", scale, s_shape, G)
     _group_rows(rows, G)
     layout, ldx = TSM_ROW, max(1, C)
     if x.numel():
@@ -501,8 +528,7 @@ def quantize_mx4(x, *, rows=None, out=None, scale=None, stream=None):
         else:
             _bad("x must be row- or column-major in its last two dims")
     _launch("mx4_quantize", stream, (x, out, scale, rows),
-            (R, C, x.data_ptr(), ldx, layout, _group_stride(x, G), f, out.data_ptr(), _rows_ld("out", out),
-             _group_stride(out, G), scale.data_ptr(), _rows_ld("scale", scale), _group_stride(scale, G), _at(rows), G))
+            (R, C, x.data_ptr(), ldx, layout, _group_stride(x, G), f, *codes, *scales, _at(rows), G))
     return out, scale
 
 
@@ -522,14 +548,10 @@ def dequantize_mx4(codes, scales, *, columns=None, rows=None, out=None, out_dtyp
         out = _new(codes, shape, out_dtype or "float32", stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         _bad(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
-    f = _wants("out", out, _FLOATS, shape)
-    _u8("codes", codes, (*shape[:-1], (C + 1) // 2))
-    _u8("scales", scales, (*shape[:-1], (C + 31) // 32))
+    q, e = _u8_rows("codes", codes, (*shape[:-1], (C + 1) // 2), G), _u8_rows("scales", scales, (*shape[:-1], (C + 31) // 32), G)
+    y, ldy, sy, f = _float_rows("out", out, shape, G)
     _group_rows(rows, G)
-    _launch("mx4_dequantize", stream, (codes, scales, out, rows),
-            (codes.shape[-2], C, codes.data_ptr(), _rows_ld("codes", codes), _group_stride(codes, G),
-             scales.data_ptr(), _rows_ld("scales", scales), _group_stride(scales, G), out.data_ptr(),
-             _rows_ld("out", out), _group_stride(out, G), f, _at(rows), G))
+    _launch("mx4_dequantize", stream, (codes, scales, out, rows), (shape[-2], C, *q, *e, y, ldy, sy, f, _at(rows), G))
     return out
 
 
@@ -551,44 +573,43 @@ def matmul_mx4(a, scale_a, b, scale_b, *, columns=None, rows=None, out=None, out
     ``columns``, or two per byte of codes (the last half byte of an odd K holds 0 as ``quantize_mx4`` leaves it).
     Batches, ``rows``, results and ``activation`` as for ``matmul_i8``.
     """
-    if a.dim() not in (2, 3) or b.dim() not in (2, 3):
+    sha, shb = a.shape, b.shape
+    da, db = len(sha), len(shb)
+    if da not in (2, 3) or db not in (2, 3):
         _bad("a and b must be 2-D or 3-D")
     floats = scale_a is None
-    _u8("b", b, b.shape)
+    K = sha[-1] if floats else 2 * sha[-1] if columns is None else columns
+    M, KB, NB, N = sha[-2], (K + 1) // 2, (K + 31) // 32, shb[-1]
     if floats:
-        fx = _wants("a", a, _FLOATS)
-        K = a.shape[-1]
+        x, ldx, sx, fx = _float_rows("a", a, sha, sha[0])
+        if columns is not None and K != columns:
+            _bad(f"columns is {columns}, a has {K}")
     else:
-        K = 2 * a.shape[-1] if columns is None else columns
-        _u8("a", a, (*a.shape[:-1], (K + 1) // 2))
-    if columns is not None and K != columns:
-        _bad(f"columns is {columns}, a has {K}")
-    M, KB, NB, N = a.shape[-2], (K + 1) // 2, (K + 31) // 32, b.shape[-1]
-    if b.shape[-2] != KB:
-        _bad(f"inner sizes differ: {KB} bytes of codes vs {b.shape[-2]}")
-    batched = a.dim() == 3 or b.dim() == 3
-    ba, bb = (a.shape[0] if a.dim() == 3 else 1), (b.shape[0] if b.dim() == 3 else 1)
+        codes = (*_u8_rows("a", a, (*sha[:-1], KB), sha[0]), *_u8_rows("scale_a", scale_a, (*sha[:-1], NB), sha[0]))
+    if b.dtype is not _uint8():
+        _bad(f"b has dtype {b.dtype}, torch.uint8 wanted")
+    if shb[-2] != KB:
+        _bad(f"inner sizes differ: {KB} bytes of codes vs {shb[-2]}")
+    ba, bb = (sha[0] if da == 3 else 1), (shb[0] if db == 3 else 1)
     if ba != bb and ba != 1 and bb != 1:
         _bad(f"batch sizes differ: {ba} vs {bb}")
     batch = ba if bb == 1 else bb
-    shape = (batch, M, N) if batched else (M, N)
+    shape = (batch, M, N) if da == 3 or db == 3 else (M, N)
     if out is None:
         out = _new(a, shape, out_dtype or "float32", stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         _bad(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
-    f = _wants("out", out, _FLOATS, shape)
-    if activation not in _ACTIVATIONS:
+    c, ldc, sc, f = _float_rows("out", out, shape, batch)
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
         _bad(f"unknown activation {activation!r}")
-    if N > 0 and KB > 1 and b.stride(-2) != 1:
+    stb = b.stride()
+    if N > 0 and KB > 1 and stb[-2] != 1:
         _bad("b must be column-major (the transpose of codes stored N x K)")
-    _u8("scale_b", scale_b, (*b.shape[:-2], N, NB))
+    weight = (b.data_ptr(), stb[-1] if N > 1 and KB else max(1, KB), stb[0] if bb > 1 else 0,
+              *_u8_rows("scale_b", scale_b, (bb, N, NB) if db == 3 else (N, NB), bb))
     if rows is not None:
         _group_rows(rows, batch)
-    act = _ACTIVATIONS[activation]
-    weight = (b.data_ptr(), _rows_ld("b", b.transpose(-1, -2)), b.stride(0) if bb > 1 else 0, scale_b.data_ptr(),
-              _rows_ld("scale_b", scale_b), scale_b.stride(0) if bb > 1 else 0)
-    result = (out.data_ptr(), _rows_ld("out", out), out.stride(0) if batched else 0)
-    sa = a.stride(0) if ba > 1 else 0
     if floats:
         need = gemm_mx4_float_a_workspace_bytes(M, K, ba) if workspace is None else 0
         if need:
@@ -596,20 +617,16 @@ def matmul_mx4(a, scale_a, b, scale_b, *, columns=None, rows=None, out=None, out
         nbytes = 0
         if workspace is not None:
             _packed("workspace", workspace)
-            nbytes = workspace.numel() * workspace.element_size()
+            nbytes = workspace.nbytes
         _launch("gemm_mx4_float_a", stream, (a, b, out, scale_b, rows, workspace),
-                (M, N, K, a.data_ptr(), _rows_ld("a", a), sa, fx, *weight, *result, batch, _at(rows), f, act, slope,
-                 _at(workspace), nbytes))
+                (M, N, K, x, ldx, sx, fx, *weight, c, ldc, sc, batch, _at(rows), f, act, slope, _at(workspace), nbytes))
         return out
-    _u8("scale_a", scale_a, (*a.shape[:-1], NB))
-    codes = (a.data_ptr(), _rows_ld("a", a), sa, scale_a.data_ptr(), _rows_ld("scale_a", scale_a),
-             scale_a.stride(0) if ba > 1 else 0)
     if rows is None:
         _launch("gemm_mx4_strided_batched", stream, (a, b, out, scale_a, scale_b),
-                (M, N, K, *codes, *weight, *result, batch, f, act, slope))
+                (M, N, K, *codes, *weight, c, ldc, sc, batch, f, act, slope))
     else:
         _launch("gemm_mx4_grouped", stream, (a, b, out, scale_a, scale_b, rows),
-                (M, N, K, *codes, *weight, *result, _at(rows), batch, f, act, slope))
+                (M, N, K, *codes, *weight, c, ldc, sc, _at(rows), batch, f, act, slope))
     return out
 
 
