@@ -1,0 +1,266 @@
+// Products of microscaled 4-bit codes of few rows (decoding steps) for gfx950: bound
+// by reading the weights once.
+//
+// The streaming kernel of the int8 products (gemm_i8_skinny.hip): a workgroup owns a
+// block of C, its waves share out K in steps of 512 elements (256 bytes of a row),
+// each copies its steps into an LDS ring of its own and multiplies from there, and
+// their float32 sums meet in LDS, added in the order of the waves.  The workgroups
+// stay for all of the tiles and the copies run on across tile boundaries.
+//
+// A lane takes blocks 4g .. 4g + 3 of a step's sixteen (g = lane / 16) in its four
+// matrix instructions, so that its scales of a step are one word per 16 rows, loaded
+// straight into a register beside the copies.
+#include "lds_ring.hpp"
+#include "mx4_common.hpp"
+
+namespace tsm {
+namespace {
+
+constexpr int STEP = 256;  // bytes of codes per step and row
+constexpr int BLOCKS = STEP / 16;
+
+struct Place {
+  int64_t z, m0, n0, M;
+};
+
+constexpr int kMaxGroups = 512;  // groups of a launch, whose tiles before each are kept in LDS
+
+// Place of tile t: row tiles fastest, then columns, then problems.  first: of a grouped call, the tiles before each
+// group (in LDS, kMaxGroups of them, the ones past the launch's groups holding the total).
+template <int AR, int NB>
+__device__ __forceinline__ Place stream_tile(const Mx4Args &p, int t, const int *first, int lane) {
+  Place e;
+  int tm = p.tiles_m, g = 0;
+  if (p.rows) {
+    for (int i = 0; i < p.nz; i += 64) g += __popcll(__ballot(first[i + lane] <= t));
+    g = min(g, p.nz) - 1;
+    const int f = __builtin_amdgcn_readfirstlane(first[g]);
+    tm = (int)((valid_rows(p, p.z0 + g) + AR - 1) / AR);
+    t -= f;
+  } else {
+    g = t / (tm * p.tiles_n);
+    t -= g * (tm * p.tiles_n);
+  }
+  e.z = p.z0 + g;
+  e.M = valid_rows(p, e.z);
+  e.m0 = (int64_t)(t % tm) * AR;
+  e.n0 = (int64_t)(t / tm) * (16 * NB);
+  return e;
+}
+
+// The kernel's arguments, read again for each tile: held in scalar registers through the loop they would spill.
+__device__ __forceinline__ Mx4Args args_again() {
+  typedef const __attribute__((address_space(4))) Mx4Args *At;
+  At p = (At)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const Mx4Args *)p;
+}
+
+template <int AR, int NB, int W, int FMT>
+__device__ __forceinline__ void stream(const Mx4Args &p) {
+  constexpr int MB = AR / 16;
+  constexpr int LA = AR / 4, LB = 4 * NB, L = LA + LB;  // wave-loads (1 KiB: 4 rows) per step
+  constexpr int BYTES = L * 1024;
+  __shared__ __attribute__((aligned(1024))) char s0[W * BYTES], s1[W * BYTES];  // the ring's two stages
+  __shared__ int first[kMaxGroups];
+  static_assert(MB * NB <= L, "a wave's sums fit one stage");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tiles = p.tiles_m * p.tiles_n * p.nz;
+  if (p.rows) {
+    // every wave computes the sums, the first writes them
+    int sum = 0;
+    for (int g = 0; g < p.nz; g += 64) {
+      const int v = group_tiles<AR>(p, g + lane) * p.tiles_n;
+      const int s = wave_scan(v, lane);
+      if (wave == 0) first[g + lane] = sum + s - v;
+      sum += __builtin_amdgcn_readlane(s, 63);
+    }
+    tiles = sum;
+    __syncthreads();
+  }
+  int t = blockIdx.x;
+  if (t >= tiles) return;  // uniform
+  // wave-load g: rows 4 g + lane / 16; LDS position lane % 16 of a row holds chunk (lane % 16) ^ (row % 16)
+  auto row_of = [&](int g) { return 4 * (g < LA ? g : g - LA) + (lane >> 4); };
+  auto chunk_of = [&](int g) { return ((lane & 15) ^ (row_of(g) & 15)) * 16; };  // its first byte within the step
+  uint32_t off[L];
+#pragma unroll
+  for (int g = 0; g < L; ++g) off[g] = (uint32_t)(row_of(g) * (g < LA ? p.lda : p.ldb) + chunk_of(g));
+  // the scales' words: row lane % 16, word lane / 16 of a step's four
+  const uint32_t offa = (uint32_t)((lane & 15) * p.ldsa + (lane >> 4) * 4);
+  const uint32_t offb = (uint32_t)((lane & 15) * p.ldsb + (lane >> 4) * 4);
+  const int steps = (int)((p.kb + STEP - 1) / STEP);
+  const int turns = (steps + 2 * W - 1) / (2 * W);  // of the ring, per tile
+  // (kept out of the compiler's sight: every copy's LDS address held in a scalar register of its own would spill them)
+  int mine = wave * BYTES;
+  auto stage = [&](int d) -> char * {
+    asm volatile("" : "+s"(mine));
+    return (d == 0 ? s0 : s1) + mine;
+  };
+  // The copies run one step ahead of the products: step fq of tile ft, through resources over its valid rows
+  // (others lie past them, since leading dimensions are at least a row's bytes, and load as zeros).
+  __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
+  uint32_t wa[2][MB], wb[2][NB];
+  int ft = blockIdx.x, fq = 0;
+  auto open = [&](int t) {
+    const Mx4Args q = args_again();
+    const Place e = stream_tile<AR, NB>(q, t, first, lane);
+    const int64_t vm = e.M - e.m0 < AR ? e.M - e.m0 : AR, vn = q.N - e.n0 < 16 * NB ? q.N - e.n0 : 16 * NB;
+    ra = make_rsrc(q.A + e.z * q.strideA + e.m0 * q.lda, (uint32_t)((vm - 1) * q.lda + q.kb));
+    rb = make_rsrc(q.B + e.z * q.strideB + e.n0 * q.ldb, (uint32_t)((vn - 1) * q.ldb + q.kb));
+    rsa = make_rsrc(q.SA + e.z * q.strideSA + e.m0 * q.ldsa, (uint32_t)((vm - 1) * q.ldsa + q.nb));
+    rsb = make_rsrc(q.SB + e.z * q.strideSB + e.n0 * q.ldsb, (uint32_t)((vn - 1) * q.ldsb + q.nb));
+  };
+  // The next step's copies into stage d.  Chunks past K, and steps past the end, copy zeros without touching memory
+  // (their scales too: what lies behind a row may be a scale of NaN): the count of copies in flight stays the same.
+  auto fetch = [&](int d) {
+    const int s = fq * W + wave;
+    const int left = ft < tiles && s < steps ? (int)(p.kb - (int64_t)s * STEP) : 0;
+    char *const to = stage(d);
+#pragma unroll
+    for (int g = 0; g < L; ++g)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(g < LA ? ra : rb, (lds_void *)(to + g * 1024), 16,
+                                               chunk_of(g) < left ? off[g] : kOutside, left ? s * STEP : 0, 0, 0);
+    const bool in = (lane >> 4) * 64 < left;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+      wa[d][i] = __builtin_amdgcn_raw_buffer_load_b32(rsa, in ? offa + (uint32_t)(16 * i * p.ldsa) : kOutside,
+                                                      left ? s * BLOCKS : 0, 0);
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      wb[d][j] = __builtin_amdgcn_raw_buffer_load_b32(rsb, in ? offb + (uint32_t)(16 * j * p.ldsb) : kOutside,
+                                                      left ? s * BLOCKS : 0, 0);
+    if (++fq == turns * 2) {
+      fq = 0;
+      ft += gridDim.x;
+      if (ft < tiles) open(ft);
+    }
+  };
+  open(t);
+  fetch(0);
+  for (; t < tiles; t += gridDim.x) {
+    f32x4 acc[MB][NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{};
+    for (int q = 0; q < turns; ++q) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        // the stage read in the last turn is free (its reads are done): refill it
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        fetch(1 - d);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L + MB + NB) : "memory");
+        const char *a = stage(d), *b = a + LA * 1024;
+        unrolled<4>([&](auto u) {
+          const int r = lane & 15;
+          // offset of this lane's chunk; opaque, because a read that the compiler can tell apart from a stage's first
+          // copy makes it wait for every copy in flight
+          int at = r * STEP + ((4 * (lane >> 4) + u.value) ^ r) * 16;
+          asm("" : "+v"(at));
+          u32x4 fa[MB], fb[NB];
+#pragma unroll
+          for (int i = 0; i < MB; ++i) fa[i] = *reinterpret_cast<const u32x4 *>(a + at + 16 * i * STEP);
+#pragma unroll
+          for (int j = 0; j < NB; ++j) fb[j] = *reinterpret_cast<const u32x4 *>(b + at + 16 * j * STEP);
+#pragma unroll
+          for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+              acc[i][j] = mfma_mx4<u.value, u.value>(fb[j], wb[d][j], fa[i], wa[d][i], acc[i][j]);
+        });
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      // (the stage just read is refilled only in the next tile)
+      for (int j = 0; j < NB; ++j) *reinterpret_cast<f32x4 *>(stage(1) + ((i * NB + j) * 64 + lane) * 16) = acc[i][j];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const Mx4Args e = args_again();
+    const Place o = stream_tile<AR, NB>(e, t, first, lane);
+    const Epilogue ep{e.act, e.slope, false};
+    for (int k = threadIdx.x; k < MB * NB * 64; k += W * 64) {
+      const int blk = k >> 6, l = k & 63;
+      const int64_t m = o.m0 + 16 * (blk / NB) + (l & 15), n = o.n0 + 16 * (blk % NB) + 4 * (l >> 4);
+      if (m >= o.M || m >= o.m0 + AR || n >= e.N) continue;
+      f32x4 sum{};
+#pragma unroll
+      for (int w = 0; w < W; ++w) sum += *reinterpret_cast<const f32x4 *>(s1 + w * BYTES + k * 16);
+      store_mx4<FMT>(e, ep, (char *)e.C + (o.z * e.strideC + m * e.ldc) * fmt_bytes(FMT), n, sum);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();  // the sums are read: the next tile's may be written
+    asm volatile("" ::: "memory");
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the copies of zeros past the end
+}
+
+template <int AR, int NB, int W, int FMT>
+__global__ __launch_bounds__(W * 64) void gemm_mx4_stream_kernel(Mx4Args p) {
+  stream<AR, NB, W, FMT>(p);
+}
+
+template <int AR, int NB, int W>
+hipError_t stream_t(Mx4Args a, hipStream_t st) {
+  constexpr int LDS = 2 * W * (AR / 4 + 4 * NB) * 1024 + 4 * kMaxGroups + 64;
+  a.tiles_m = (int32_t)((a.M + AR - 1) / AR);
+  a.tiles_n = (int32_t)((a.N + 16 * NB - 1) / (16 * NB));
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  // what 256 CUs of 160 KiB hold at once; the rest of the tiles follow in the same workgroups
+  const int64_t resident = 256 * (163840 / LDS);
+  int64_t most = 0x3fffffff / tiles;  // problems per launch: tile numbers stay far below 2^31
+  if (a.rows && most > kMaxGroups) most = kMaxGroups;
+  for (int64_t z0 = 0; z0 < a.batch; z0 += most) {
+    a.z0 = z0;
+    a.nz = (int32_t)(a.batch - z0 < most ? a.batch - z0 : most);
+    const dim3 grid((unsigned)(tiles * a.nz < resident ? tiles * a.nz : resident));
+    if (a.fmt == FMT_F32)
+      hipLaunchKernelGGL((gemm_mx4_stream_kernel<AR, NB, W, FMT_F32>), grid, dim3(W * 64), 0, st, a);
+    else if (a.fmt == FMT_F16)
+      hipLaunchKernelGGL((gemm_mx4_stream_kernel<AR, NB, W, FMT_F16>), grid, dim3(W * 64), 0, st, a);
+    else
+      hipLaunchKernelGGL((gemm_mx4_stream_kernel<AR, NB, W, FMT_BF16>), grid, dim3(W * 64), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+Mx4Stream mx4_stream_plan(const Mx4Args &p) {
+  Mx4Stream s;
+  // (more columns than tile numbers hold go to the general kernel)
+  if (p.M > 64 || p.K == 0 || p.N > 0xffffffffLL / 256 * 16) return s;
+  const bool aligned = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && (((uintptr_t)p.SA | (uintptr_t)p.SB) & 3) == 0 &&
+                       p.K % 128 == 0 && ((p.lda | p.ldb | p.strideA | p.strideB) & 15) == 0 &&
+                       ((p.ldsa | p.ldsb | p.strideSA | p.strideSB) & 3) == 0;
+  // 32-bit offsets over a block's rows
+  const int64_t limit = (int64_t)1 << 30;
+  s.can = aligned && 32 * p.lda + p.kb < limit && 32 * p.ldb + p.kb < limit && 32 * p.ldsa + p.nb < limit &&
+          32 * p.ldsb + p.nb < limit;
+  const int64_t per = (p.N + 15) / 16;
+  const int64_t tiles = per > ((int64_t)1 << 40) / p.batch ? (int64_t)1 << 40 : per * p.batch;
+  if (p.M <= 16) {
+    s.rows = 16;
+    s.nb = 1;
+    s.waves = tiles >= 1024 && tiles >= p.K / 4 ? 1 : 4;
+  } else {
+    s.rows = 32;
+    s.nb = tiles >= (p.M > 32 ? 512 : 1536) ? 2 : 1;
+    s.waves = s.nb == 2 ? 1 : 2;
+  }
+  s.use = s.can && !(p.M > 32 && tiles >= 768 && !p.rows);
+  return s;
+}
+
+hipError_t launch_mx4_stream(const Mx4Args &p, hipStream_t st) {
+  const Mx4Stream s = mx4_stream_plan(p);
+  if (s.rows == 16) return s.waves == 1 ? stream_t<16, 1, 1>(p, st) : stream_t<16, 1, 4>(p, st);
+  return s.nb == 1 ? stream_t<32, 1, 2>(p, st) : stream_t<32, 2, 1>(p, st);
+}
+
+}  // namespace tsm

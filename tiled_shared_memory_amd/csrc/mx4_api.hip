@@ -21,6 +21,8 @@ const char *mx4_name(Mx4Kernel k) {
       return "mx4_block_64x64x256";
     case Mx4Kernel::Tile:
       return "mx4_tile_256x256x256";
+    case Mx4Kernel::Stream:
+      return "mx4_stream";
     default:
       return nullptr;
   }
@@ -148,16 +150,18 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
   const bool half = M <= 128 && tiles128 * batch <= 256;  // 256-tiles half empty, and a round of 128-tiles does it
   const int64_t tiles256 = ((M + 255) / 256) * ((N + 255) / 256) * batch;
   if (M > 64 && !half && tiles256 >= kFewTiles && mx4_tile_supports(p)) call->kernel = Mx4Kernel::Tile;
+  const Mx4Stream stream = mx4_stream_plan(p);
+  if (stream.use) call->kernel = Mx4Kernel::Stream;
   // TSM_GEMM_KERNEL=<name> forces a variant (tests and tuning); names of other
   // families are left alone, a variant that cannot run the problem is an error.
   const char *force = getenv("TSM_GEMM_KERNEL");
   if (force && strncmp(force, "mx4_", 4) == 0) {
     Mx4Kernel want = Mx4Kernel::None;
-    for (Mx4Kernel k : {Mx4Kernel::Block128, Mx4Kernel::Block64, Mx4Kernel::Tile})
+    for (Mx4Kernel k : {Mx4Kernel::Block128, Mx4Kernel::Block64, Mx4Kernel::Tile, Mx4Kernel::Stream})
       if (strcmp(force, mx4_name(k)) == 0) want = k;
     if (want == Mx4Kernel::None) return fail(TSM_ERROR_INVALID_VALUE, "TSM_GEMM_KERNEL=%s names no kernel", force);
     if ((want == Mx4Kernel::Block64 && tiles64 * 512 > 0xffffffffLL) ||
-        (want == Mx4Kernel::Tile && !mx4_tile_supports(p)))
+        (want == Mx4Kernel::Tile && !mx4_tile_supports(p)) || (want == Mx4Kernel::Stream && !stream.can))
       return fail(TSM_ERROR_NOT_SUPPORTED, "TSM_GEMM_KERNEL=%s cannot run this problem", force);
     call->kernel = want;
     call->forced = true;
@@ -179,6 +183,8 @@ int mx4_run(const Call &c, void *stream) {
       return launched(launch_mx4_block(c.p, 64, s));
     case Mx4Kernel::Tile:
       return launched(launch_mx4_tile(c.p, !c.forced, s));
+    case Mx4Kernel::Stream:
+      return launched(launch_mx4_stream(c.p, s));
     default:
       return TSM_SUCCESS;
   }

@@ -42,7 +42,14 @@ hipError_t launch_mx4_rest(const Mx4Args &a, hipStream_t stream);
 // CUs of the current device (gemm_api.hip).
 int device_cus();
 
-enum class Mx4Kernel { None, Block128, Block64, Tile };
+enum class Mx4Kernel { None, Block128, Block64, Tile, Stream };
+// Few rows (up to 64).
+struct Mx4Stream {
+  bool can = false, use = false;     // what the problem allows; the rule's choice
+  int rows = 0, nb = 0, waves = 0;   // rows by 16 nb columns per workgroup of `waves` waves
+};
+Mx4Stream mx4_stream_plan(const Mx4Args &p);
+hipError_t launch_mx4_stream(const Mx4Args &p, hipStream_t stream);
 hipError_t launch_mx4_block(const Mx4Args &p, int tile, hipStream_t stream);
 
 struct Mx4QuantArgs {

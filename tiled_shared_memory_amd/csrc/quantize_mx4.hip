@@ -91,8 +91,12 @@ __global__ __launch_bounds__(kThreads) void quantize_mx4_kernel(Mx4QuantArgs a) 
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
     const int64_t c = c0 + u * TPR;
-    if (c < whole) ch[u].load(x, c);
-    else ch[u].load_part(x, c, c == whole ? rest : 0);
+    if (c < whole) {
+      ch[u].load(x, c);
+    } else {
+      ch[u] = Chunk<FMT>{};
+      if (c == whole && rest) ch[u].load_part(x, c, rest);
+    }
   }
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
@@ -249,8 +253,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4QuantArgs a
 template <class F>
 hipError_t over_rows(const Mx4QuantArgs &base, F &&launch) {
   const int64_t chunks = (base.C + 7) / 8, rows = base.R * base.groups;
-  int tpr = 16;
-  while (tpr < kThreads && tpr * kPer < chunks) tpr *= 4;
+  const int tpr = chunks <= 16 * kPer ? 16 : 64;
   const int64_t segs = (chunks + tpr * kPer - 1) / (tpr * kPer), per = kThreads / tpr;
   const int64_t most = 0xffffffffLL / kThreads / segs * per;
   for (int64_t r0 = 0; r0 < rows; r0 += most) {
@@ -270,10 +273,8 @@ hipError_t quantize_rows(const Mx4QuantArgs &base, hipStream_t stream) {
   return over_rows(base, [&](const Mx4QuantArgs &a, int tpr, dim3 grid) {
     if (tpr == 16)
       hipLaunchKernelGGL((quantize_mx4_kernel<FMT, 16>), grid, dim3(kThreads), 0, stream, a);
-    else if (tpr == 64)
-      hipLaunchKernelGGL((quantize_mx4_kernel<FMT, 64>), grid, dim3(kThreads), 0, stream, a);
     else
-      hipLaunchKernelGGL((quantize_mx4_kernel<FMT, 256>), grid, dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((quantize_mx4_kernel<FMT, 64>), grid, dim3(kThreads), 0, stream, a);
   });
 }
 
@@ -299,10 +300,8 @@ hipError_t dequantize_rows(const Mx4QuantArgs &base, hipStream_t stream) {
   return over_rows(base, [&](const Mx4QuantArgs &a, int tpr, dim3 grid) {
     if (tpr == 16)
       hipLaunchKernelGGL((dequantize_mx4_kernel<FMT, 16>), grid, dim3(kThreads), 0, stream, a);
-    else if (tpr == 64)
-      hipLaunchKernelGGL((dequantize_mx4_kernel<FMT, 64>), grid, dim3(kThreads), 0, stream, a);
     else
-      hipLaunchKernelGGL((dequantize_mx4_kernel<FMT, 256>), grid, dim3(kThreads), 0, stream, a);
+      hipLaunchKernelGGL((dequantize_mx4_kernel<FMT, 64>), grid, dim3(kThreads), 0, stream, a);
   });
 }
 
