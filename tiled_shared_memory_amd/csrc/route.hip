@@ -7,12 +7,18 @@
 //   weight  factor * s_e, renormalised over the chosen: factor * s_e / sum of their s
 //
 // L lanes hold a token's row (16, or 32 above 256 experts), each the experts
-// l V .. l V + V - 1; a wave works on 64 / L tokens.  The chosen ones are found one
-// after another: the largest key of each lane, of the L lanes, the first lane that
-// holds it.
+// l V .. l V + V - 1; a wave works on 64 / L tokens.
+//
+// Up to 8 choices (route8_kernel): each lane sorts its keys, the lanes' lists of 8 are
+// merged pairwise (element i against the partner's 7 - i, then three exchanges), and
+// the k-th of the result is the smallest key that is chosen.  The lanes list the
+// experts that reach it, and up to 8 lanes order those and weigh them: about as much
+// work as two rounds of searching the largest key, which it replaces.  More choices,
+// and groups that lanes cannot share out evenly (route_kernel): one after another, the
+// largest key of each lane, of the L lanes, the first lane that holds it.
 //
 // A choice is made by the exact keys.  Keys computed in float32 are off by a
-// known bound (kScoreError); where two neighbours in the order, or two groups, lie
+// known bound (score_error); where two neighbours in the order, or two groups, lie
 // nearer than that, the token's wave decides again by keys in float64.  Which
 // experts are chosen is therefore the same whatever exp() rounds to.
 //
@@ -28,24 +34,67 @@ constexpr int kThreads = 256;
 constexpr float kInf = __builtin_inff();
 
 // How far a float32 score may be from the exact one (scores are at most 1).  exp of an argument d is off by
-// |d| 2^-23 + 2^-22 relative, which |d| exp(-|d|) < 0.37 keeps below 2^-22 of 1; a softmax's sum of up to 32 numbers
-// a lane and 5 steps over the lanes adds 37 * 2^-24, its division 2^-24: together below 2^-18, for a sigmoid below
-// 2^-21.
-__device__ __forceinline__ float score_error(bool sigmoid) { return sigmoid ? 0x1p-21f : 0x1p-18f; }
+// |d| 2^-23 + 2^-22 relative; |d| exp(-|d|) < 0.37, so by 2^-22 of 1 at most.  A sigmoid adds a sum (2^-24) and a
+// reciprocal (2^-23): below 2^-20 together.  A softmax's sum of up to 32 numbers a lane and 5 steps over the lanes adds
+// 37 * 2^-24, its reciprocal and product 2^-22: below 2^-18.
+__device__ __forceinline__ float score_error(bool sigmoid) { return sigmoid ? 0x1p-20f : 0x1p-18f; }
 
-template <int L, class T>
-__device__ __forceinline__ T row_max(T v) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) {
-    const T o = __shfl_xor(v, d, L);
-    v = o > v ? o : v;
+// ---- lanes of a token ----
+// The value of another lane: step 0 and 1 exchange within a quad, 2 and 3 mirror 8 and 16 lanes (which, after the
+// steps before, hold equal values by quads and by eights), 4 exchanges the rows of 32.
+template <int STEP>
+__device__ __forceinline__ int across(int v) {
+  if constexpr (STEP == 0) return __builtin_amdgcn_mov_dpp(v, 0xb1, 0xf, 0xf, true);
+  if constexpr (STEP == 1) return __builtin_amdgcn_mov_dpp(v, 0x4e, 0xf, 0xf, true);
+  if constexpr (STEP == 2) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true);
+  if constexpr (STEP == 3) return __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true);
+  return __shfl_xor(v, 16, 32);
+}
+template <int STEP>
+__device__ __forceinline__ float across(float v) {
+  return __builtin_bit_cast(float, across<STEP>(__builtin_bit_cast(int, v)));
+}
+template <int N>
+constexpr int log2_of() {
+  return N == 1 ? 0 : 1 + log2_of<N / 2>();
+}
+
+template <int N>
+struct Step {
+  static constexpr int value = N;
+};
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void steps(F &&f) {
+  if constexpr (I < N) {
+    f(Step<I>{});
+    steps<N, I + 1>(f);
   }
+}
+template <int L>
+__device__ __forceinline__ float row_max(float v) {
+  steps<log2_of<L>()>([&](auto s) {
+    const float o = across<s.value>(v);
+    v = o > v ? o : v;
+  });
   return v;
 }
 template <int L, class T>
 __device__ __forceinline__ T row_sum(T v) {
+  if constexpr (sizeof(T) == 4) {
+    steps<log2_of<L>()>([&](auto s) { v += across<s.value>(v); });
+  } else {
 #pragma unroll
-  for (int d = 1; d < L; d <<= 1) v += __shfl_xor(v, d, L);
+    for (int d = 1; d < L; d <<= 1) v += __shfl_xor(v, d, L);
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ double row_max(double v) {
+#pragma unroll
+  for (int d = 1; d < L; d <<= 1) {
+    const double o = __shfl_xor(v, d, L);
+    v = o > v ? o : v;
+  }
   return v;
 }
 // Which of a token's lanes say so.
@@ -111,9 +160,12 @@ __device__ __forceinline__ void soft_stats(const Row<V> &w, T &top, T &sum) {
   sum = row_sum<L>(sum);
 }
 
+__device__ __forceinline__ float one_over(float x) { return __builtin_amdgcn_rcpf(x); }
+__device__ __forceinline__ double one_over(double x) { return 1.0 / x; }
+// by: of a softmax, one over the sum.
 template <class T>
-__device__ __forceinline__ T score_of(bool sigmoid, T x, T top, T sum) {
-  return sigmoid ? T(1) / (T(1) + expo(-x)) : expo(x - top) / sum;
+__device__ __forceinline__ T score_of(bool sigmoid, T x, T top, T by) {
+  return sigmoid ? one_over(T(1) + expo(-x)) : expo(x - top) * by;
 }
 
 // Chooses a token's experts into chosen[0 .. topk) (-1: none left) and their logits; returns whether float32 keys left
@@ -128,7 +180,10 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const Row<V> &w, cons
   const bool scored = a.bias && !bad, sums = grouped && (a.bias || a.best > 1);
   bool open = false;
   T key[V], top = 0, sum = 1;
-  if ((scored || sums) && !a.sigmoid) soft_stats<T, L>(w, top, sum);
+  if ((scored || sums) && !a.sigmoid) {
+    soft_stats<T, L>(w, top, sum);
+    sum = one_over(sum);
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     key[i] = w.x[i] == w.x[i] ? (T)w.x[i] : none;
@@ -217,14 +272,329 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const Row<V> &w, cons
   return row_ballot<L>(open) != 0;
 }
 
+// The weights of a token's choices, which lie in chosen and logit (in LDS): lane l's are l, l + L, ...  P of them.
+template <int L, int V, int P>
+__device__ __forceinline__ void weigh(const RouteArgs &a, const Row<V> &w, bool bad, bool held, int64_t t,
+                                      const int *chosen, const float *logit) {
+  const int l = threadIdx.x % L;
+  float top = 0.f, sum = 1.f, x[P], s[P], part = 0.f;
+  int e[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int j = l + p * L;
+    e[p] = j < a.topk ? chosen[j] : -1;
+    x[p] = e[p] >= 0 ? logit[j] : -kInf;
+  }
+  if (a.renormalize) {
+    // the largest (softmax), or the largest below 0 (sigmoid): s = exp(min(x, 0)) / (1 + exp(-|x|))
+    float m = x[0];
+#pragma unroll
+    for (int p = 1; p < P; ++p) m = fmaxf(m, x[p]);
+    top = row_max<L>(m);
+    if (a.sigmoid && top > 0.f) top = 0.f;
+    if (top == -kInf) top = 0.f;
+  } else if (!a.sigmoid) {
+    soft_stats<float, L>(w, top, sum);
+  }
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    s[p] = 0.f;
+    if (e[p] >= 0) {
+      if (a.sigmoid)
+        s[p] = expf((a.renormalize ? fminf(x[p], 0.f) - top : fminf(x[p], 0.f))) / (1.f + expf(-fabsf(x[p])));
+      else
+        s[p] = expf(x[p] - top);
+      part += s[p];
+    }
+  }
+  if (a.renormalize) sum = row_sum<L>(part);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int j = l + p * L;
+    if (!held || j >= a.topk) continue;
+    float wt = e[p] < 0 ? 0.f : s[p] / sum * a.factor;
+    if (bad && e[p] >= 0) wt = __builtin_nanf("");
+    a.ids[t * a.topk + j] = e[p];
+    a.weights[t * a.topk + j] = wt;
+  }
+}
+
+// ---- up to 8 choices ----
+// Floats in the order of their values as whole numbers (-0 as 0), and back.
+__device__ __forceinline__ int ordered(float f) {
+  const int b = __builtin_bit_cast(int, f + 0.f);
+  return b ^ (b >> 31 & 0x7fffffff);
+}
+__device__ __forceinline__ float of_ordered(int i) { return __builtin_bit_cast(float, i ^ (i >> 31 & 0x7fffffff)); }
+constexpr int kNone = -0x7f800001;  // -inf
+
+__device__ __forceinline__ void exchange(int &a, int &b) {  // the larger to a
+  const int m = a > b ? a : b;
+  b = a > b ? b : a;
+  a = m;
+}
+// A list that rises and then falls (or the reverse), to falling.
+__device__ __forceinline__ void merge8(int (&v)[8]) {
+#pragma unroll
+  for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) exchange(v[i], v[i + d]);
+}
+// 8 numbers to falling order: Batcher's odd-even merge sort, 19 exchanges.
+__device__ __forceinline__ void sort8(int (&v)[8]) {
+#pragma unroll
+  for (int p = 1; p < 8; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < 8; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (j + i + k < 8 && (j + i) / (2 * p) == (j + i + k) / (2 * p)) exchange(v[j + i], v[j + i + k]);
+}
+// The larger 8 of two falling lists of 8, as a list for merge8.
+__device__ __forceinline__ void join8(int (&a)[8], const int (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = b[7 - i] > a[i] ? b[7 - i] : a[i];
+}
+
+template <int FMT, int L, int V>
+__global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs a) {
+  constexpr int kTokens = kThreads / L;
+  extern __shared__ double dynamic[];  // of the groups' keys: L * V float64 per token
+  struct Choice {
+    float key, x, bias;
+    int e;
+  };
+  __shared__ Choice list[kTokens][8];
+  __shared__ int chosen[kTokens][8];
+  __shared__ float logit[kTokens][8];
+  const int slot = threadIdx.x / L, l = threadIdx.x % L;
+  const int64_t t = a.t0 + (int64_t)blockIdx.x * kTokens + slot;
+  const bool held = t < a.tokens;
+  const int64_t row = held ? t : a.tokens - 1;
+  const bool grouped = a.top_groups < a.groups, scored = a.bias != nullptr;  // uniform
+  const bool sums = grouped && (scored || a.best > 1);
+  Row<V> w;
+  w.e0 = l * V;
+  load_row<FMT, L>(w, a, row);
+  float bias[V] = {};
+  if (scored) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (w.e0 + i < a.experts) bias[i] = a.bias[w.e0 + i];
+  }
+  // a NaN is above +inf or below -inf in this order
+  int key[V], hi, lo;
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = ordered(w.x[i]);
+  hi = lo = key[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) hi = key[i] > hi ? key[i] : hi, lo = key[i] < lo ? key[i] : lo;
+  const bool bad = row_ballot<L>(hi > (a.sigmoid ? 0x7f800000 : 0x7f7fffff) || lo < kNone) != 0;
+  bool open = bad;
+  const float error = score_error(a.sigmoid);
+  float top = 0.f, by = 1.f;
+  if (scored || sums) {
+    if (!a.sigmoid) {
+      soft_stats<float, L>(w, top, by);
+      by = one_over(by);
+    }
+    float g[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float s = score_of<float>(a.sigmoid, w.x[i], top, by) + bias[i];
+      g[i] = w.x[i] > -kInf && s == s ? s : -kInf;
+      if (scored) key[i] = ordered(g[i]);
+    }
+    if (sums) {
+      // the two largest of the lane's, then of its group's lanes
+      float b1 = g[0], b2 = -kInf;
+#pragma unroll
+      for (int i = 1; i < V; ++i) {
+        b2 = __builtin_amdgcn_fmed3f(b1, b2, g[i]);
+        b1 = g[i] > b1 ? g[i] : b1;
+      }
+      const int lanes = a.experts / a.groups / V;  // of a group: a power of two
+      steps<log2_of<L>()>([&](auto s) {
+        if ((1 << s.value) < lanes) {
+          const float o1 = across<s.value>(b1), o2 = across<s.value>(b2);
+          const float least = o1 < b1 ? o1 : b1, rest = o2 > b2 ? o2 : b2;
+          b1 = o1 > b1 ? o1 : b1;
+          b2 = least > rest ? least : rest;
+        }
+      });
+      if (a.best > 1 && b2 > -kInf) b1 += b2;
+      int before = 0;
+      for (int r = lanes; r < L; r += lanes) {  // the group r lanes before, around the row
+        const float o = __shfl(b1, (l - r) & (L - 1), L);
+        before += o > b1 || (o == b1 && l >= r);
+        open |= fabsf(o - b1) <= 8 * error + 0x1p-21f * fabsf(o);
+      }
+      const bool in = before < a.top_groups;
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = in ? key[i] : kNone;
+    }
+  }
+  if (grouped && !sums) {
+    int b1 = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) b1 = key[i] > b1 ? key[i] : b1;
+    const int lanes = a.experts / a.groups / V;
+    steps<log2_of<L>()>([&](auto s) {
+      if ((1 << s.value) < lanes) {
+        const int o = across<s.value>(b1);
+        b1 = o > b1 ? o : b1;
+      }
+    });
+    int before = 0;
+    for (int r = lanes; r < L; r += lanes) {
+      const int o = __shfl(b1, (l - r) & (L - 1), L);
+      before += o > b1 || (o == b1 && l >= r);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = before < a.top_groups ? key[i] : kNone;
+  }
+
+  // the 8 largest keys of the token, in every lane
+  int best[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) best[i] = i < V ? key[i % V] : kNone;
+  if constexpr (V > 1) sort8(best);
+  if constexpr (V > 8) {
+    int more[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) more[i] = key[(8 + i) % V];
+    sort8(more);
+    join8(best, more);
+    merge8(best);
+  }
+  steps<log2_of<L>()>([&](auto s) {
+    int other[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) other[i] = across<s.value>(best[i]);
+    join8(best, other);
+    merge8(best);
+  });
+  int least = best[0];  // the smallest chosen key
+#pragma unroll
+  for (int i = 1; i < 8; ++i)
+    if (i < a.topk) least = best[i];
+  const bool all = least <= kNone;  // fewer than topk are left
+  if (all) least = kNone + 1;
+
+  // who reaches it
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = V - 1; i >= 0; --i) mine = mine + mine + (key[i] >= least);
+  int count = __builtin_popcount(mine), upto = count, total;
+  steps<log2_of<L>()>([&](auto s) {
+    const int o = __shfl_up(upto, 1 << s.value, L);
+    if (l >= (1 << s.value)) upto += o;
+  });
+  total = __shfl(upto, L - 1, L);
+  const bool tied = total > a.topk;  // equal keys at the border: the lowest indices
+  if (__ballot(tied)) {
+    uint32_t equal = 0;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) equal = equal + equal + (key[i] == least);
+    int before = __builtin_popcount(equal);
+    const int own = before;
+    steps<log2_of<L>()>([&](auto s) {
+      const int o = __shfl_up(before, 1 << s.value, L);
+      if (l >= (1 << s.value)) before += o;
+    });
+    const int excess = total - a.topk, sum = __shfl(before, L - 1, L);
+    // of the token's `sum` equal ones the first sum - excess stay
+    int drop = before - (sum - excess);
+    drop = drop < 0 ? 0 : drop > own ? own : drop;
+    for (; drop > 0; --drop) {
+      const uint32_t last = 0x80000000u >> __builtin_clz(equal);
+      equal ^= last;
+      mine ^= last;
+      --count;
+    }
+    upto = count;
+    steps<log2_of<L>()>([&](auto s) {
+      const int o = __shfl_up(upto, 1 << s.value, L);
+      if (l >= (1 << s.value)) upto += o;
+    });
+  }
+  const uint32_t taken = mine;
+  for (int at = upto - count; mine; mine &= mine - 1) list[slot][at++].e = w.e0 + __builtin_ctz(mine);
+  wave_sync();
+  const int n = total < a.topk ? total : a.topk;
+
+  // lane j orders the j-th of the list
+  Choice c{-kInf, 0.f, 0.f, -1};
+  if (l < n) {
+    c.e = list[slot][l].e;
+    c.x = elem_f32<FMT>(elem_bits<FMT>((const char *)a.logits + row * a.ld * fmt_bytes(FMT), c.e));
+    c.key = c.x;
+    if (scored) {
+      c.bias = a.bias[c.e];
+      c.key = score_of<float>(a.sigmoid, c.x, top, by) + c.bias;
+    }
+    list[slot][l] = c;
+  }
+  if (l < 8) chosen[slot][l] = -1;
+  wave_sync();
+  int rank = 0;
+  bool close = false;
+  const float tolerance = 4 * error + 0x1p-22f * fabsf(c.key);
+  for (int j = 0; j < a.topk; ++j) {
+    const Choice o = list[slot][j];
+    const bool other = j < n && j != l;
+    rank += other && (o.key > c.key || (o.key == c.key && o.e < c.e));
+    // (equal logits and biases make equal keys, whatever they round to)
+    close |= other && fabsf(o.key - c.key) <= tolerance && (o.x != c.x || o.bias != c.bias);
+  }
+  if (l < n) {
+    chosen[slot][rank] = c.e;
+    logit[slot][rank] = c.x;
+    if (scored) open |= close;
+  }
+  if (scored) {
+    // those that are not chosen but as near to the last chosen one as keys may be off
+    const float f = of_ordered(least);
+    const int near = all ? least : ordered(f - (4 * error + 0x1p-22f * fabsf(f)));
+    int around = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) around += key[i] >= near;
+    if (__ballot(row_sum<L>(around) > n)) {
+      // (the last chosen one's logit and bias)
+      float lx = 0.f, lb = 0.f;
+      for (int j = 0; j < n; ++j)
+        if (ordered(list[slot][j].key) == least) lx = list[slot][j].x, lb = list[slot][j].bias;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        open |= key[i] >= near && !(taken >> i & 1) && (w.x[i] != lx || bias[i] != lb);
+    }
+  }
+  wave_sync();
+  if (__ballot(open)) {  // the whole wave, so that its lanes stay together; what was decided is decided again, equally
+    double *const keys = dynamic + slot * (grouped ? L * V : 0);
+    choose<double, L>(a, w, bias, bad, keys, chosen[slot], logit[slot]);
+  }
+  weigh<L, V, 1>(a, w, bad, held, t, chosen[slot], logit[slot]);
+}
+
+// Whether lanes of V experts share out the groups evenly, a power of two lanes each.
+inline bool even_groups(const RouteArgs &a, int V) {
+  if (a.top_groups == a.groups) return true;
+  const int size = a.experts / a.groups, lanes = size / V;
+  return size % V == 0 && (lanes & (lanes - 1)) == 0;
+}
+
 template <int FMT, int L, int V>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs first) {
   RouteArgs a = first;
-  constexpr int kLanes = L, kTokens = kThreads / L;
+  constexpr int kTokens = kThreads / L;
   extern __shared__ double dynamic[];  // of the groups' keys: L * V float64 per token
   __shared__ int chosen[kTokens][RouteInfo::kMaxTopk];
   __shared__ float logit[kTokens][RouteInfo::kMaxTopk];
-  const int slot = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+  const int slot = threadIdx.x / L, l = threadIdx.x % L;
   const int64_t t = a.t0 + (int64_t)blockIdx.x * kTokens + slot;
   const bool held = t < a.tokens;
   Row<V> w;
@@ -246,47 +616,8 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs first) {
   a = args_again();
   if (__ballot(open)) choose<double, L>(a, w, bias, bad, keys, chosen[slot], logit[slot]);
 
-  // the weights: lane l's choices l, l + L, ...
   a = args_again();
-  constexpr int P = RouteInfo::kMaxTopk / kLanes;
-  float top = 0.f, sum = 1.f;
-  if (a.renormalize) {
-    // the largest (softmax), or the largest below 0 (sigmoid): s = exp(min(x, 0)) / (1 + exp(-|x|))
-    float m = -kInf;
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-      if (l + p * kLanes < a.topk && chosen[slot][l + p * kLanes] >= 0) m = fmaxf(m, logit[slot][l + p * kLanes]);
-    top = row_max<L>(m);
-    if (a.sigmoid && top > 0.f) top = 0.f;
-    if (top == -kInf) top = 0.f;
-  } else if (!a.sigmoid) {
-    soft_stats<float, L>(w, top, sum);
-  }
-  float s[P], part = 0.f;
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int j = l + p * kLanes;
-    s[p] = 0.f;
-    if (j < a.topk && chosen[slot][j] >= 0) {
-      const float x = logit[slot][j];
-      if (a.sigmoid)
-        s[p] = expf((a.renormalize ? fminf(x, 0.f) - top : fminf(x, 0.f))) / (1.f + expf(-fabsf(x)));
-      else
-        s[p] = expf(x - top);
-      part += s[p];
-    }
-  }
-  if (a.renormalize) sum = row_sum<L>(part);
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    const int j = l + p * kLanes;
-    if (!held || j >= a.topk) continue;
-    const int e = chosen[slot][j];
-    float wt = e < 0 ? 0.f : s[p] / sum * a.factor;
-    if (bad && e >= 0) wt = __builtin_nanf("");
-    a.ids[t * a.topk + j] = e;
-    a.weights[t * a.topk + j] = wt;
-  }
+  weigh<L, V, RouteInfo::kMaxTopk / L>(a, w, bad, held, t, chosen[slot], logit[slot]);
 }
 
 // With g the gradients of the weights times the factor, q the chosen scores over their sum:
@@ -408,6 +739,8 @@ hipError_t route_v(const RouteArgs &base, bool backward, hipStream_t stream) {
     const size_t lds = a.top_groups < a.groups ? (size_t)kTokens * L * V * 8 : 0;
     if (backward)
       hipLaunchKernelGGL((route_backward_kernel<FMT, L, V>), grid, dim3(kThreads), 0, stream, a);
+    else if (a.topk <= 8 && even_groups(a, V))
+      hipLaunchKernelGGL((route8_kernel<FMT, L, V>), grid, dim3(kThreads), lds, stream, a);
     else
       hipLaunchKernelGGL((route_kernel<FMT, L, V>), grid, dim3(kThreads), lds, stream, a);
     const hipError_t e = hipGetLastError();
