@@ -34,11 +34,19 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kInf = __builtin_inff();
 
-// How far a float32 score may be from the exact one (scores are at most 1).  exp of an argument d is off by
-// |d| 2^-23 + 2^-22 relative; |d| exp(-|d|) < 0.37, so by 2^-22 of 1 at most.  A sigmoid adds a sum (2^-24) and a
-// reciprocal (2^-23): below 2^-20 together.  A softmax's sum of up to 32 numbers a lane and 5 steps over the lanes adds
-// 37 * 2^-24, its reciprocal and product 2^-22: below 2^-18.
-__device__ __forceinline__ float score_error(bool sigmoid) { return sigmoid ? 0x1p-20f : 0x1p-18f; }
+// How far a float32 score may be from the exact one.  exp of d is off by |d| 1.5 * 2^-24 (the product with log2 e) and
+// 2^-23, relative.
+//  * A sigmoid s = 1 / (1 + exp(-x)) takes s (1 - s) of that, at most 0.224 / |x| and 1/4 of it, and adds a sum (2^-24)
+//    and a reciprocal (2^-23): below 2^-21.
+//  * A softmax's score takes it whole, relative to itself, and |d| exp(-|d|) < 0.37; the sum's error is that of its
+//    terms in the mean (|d| is at most ln 512 in that mean, plus the logarithm of the largest score's share) and of 37
+//    additions, 32 in a lane and 5 over the lanes; with reciprocal and product below 2^-18 of the largest score.
+__device__ __forceinline__ float score_error(bool sigmoid, float largest) {
+  return sigmoid ? 0x1p-21f : 0x1p-18f * largest;
+}
+// Two keys, and two groups' sums, that may be in the other order.
+__device__ __forceinline__ float key_error(float error, float key) { return 2 * error + 0x1p-22f * fabsf(key); }
+__device__ __forceinline__ float group_error(float error, float sum) { return 4 * error + 0x1p-21f * fabsf(sum); }
 
 // ---- lanes of a token ----
 template <int N>
@@ -198,7 +206,7 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, T *keys, T e
       before += k > of[p] || (k == of[p] && o < g);
       if (error > 0 && g < a.groups && o != g) {
         const T d = k > of[p] ? k - of[p] : of[p] - k;
-        *open |= d <= 8 * error + T(0x1p-21) * (k > 0 ? k : -k);
+        *open |= d <= group_error((float)error, (float)k);
       }
     }
     kept |= row_ballot<L>(g < a.groups && before < a.top_groups && of[p] > none) << (p * L % 64);
@@ -213,7 +221,6 @@ template <int L, int V>
 __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V], int e0, const float (&bias)[V],
                                        float *keys, int *chosen, float *logit) {
   const int l = threadIdx.x % L;
-  const float error = score_error(a.sigmoid);
   const bool grouped = a.top_groups < a.groups, scored = a.bias != nullptr;
   const bool sums = grouped && (scored || a.best > 1);
   bool open = false;
@@ -222,6 +229,7 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V], 
     soft_stats<L>(x, top, by);
     by = one_over(by);
   }
+  const float error = score_error(a.sigmoid, by);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     key[i] = x[i];
@@ -248,7 +256,7 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V], 
     for (int i = 1; i < V; ++i) m = key[i] > m ? key[i] : m;
     const float best = row_max<L>(m);
     if (scored) {
-      if (j > 0 && best > -kInf) open |= last - best <= 4 * error + 0x1p-22f * fabsf(best);
+      if (j > 0 && best > -kInf) open |= last - best <= key_error(error, best);
       last = best;
       if (j == a.topk) break;
     }
@@ -330,6 +338,46 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs &a, const char *r
     }
     wave_sync();
   }
+}
+
+// The order by keys in float64 of a token's experts that may be among the chosen: bits `within` of each lane's, up to L
+// in the token, `before` of them in the lanes before.  All of a wave's lanes come here, also those of tokens that do not
+// ask for it.
+template <int FMT, int L>
+__device__ __forceinline__ void order_exactly(const RouteArgs &a, const char *row, const float *bias, bool asked,
+                                              uint32_t within, int before, int around, int e0, double *keys, int *ids,
+                                              int *chosen, float *logit) {
+  const int l = threadIdx.x % L;
+  double top = -(double)kInf, sum = 0;
+  if (!a.sigmoid) {
+    for (int e = l; e < a.experts; e += L) {
+      const double x = elem_f32<FMT>(elem_bits<FMT>(row, e));
+      top = x > top ? x : top;
+    }
+    top = row_max<L>(top);
+    if (top == -(double)kInf) top = 0;
+    for (int e = l; e < a.experts; e += L) sum += exp((double)elem_f32<FMT>(elem_bits<FMT>(row, e)) - top);
+    sum = row_sum<L>(sum);
+  }
+  if (asked)
+    for (; within; within &= within - 1) ids[before++] = e0 + __builtin_ctz(within);
+  wave_sync();
+  const bool held = asked && l < around;
+  const int e = held ? ids[l] : 0;
+  const float x = elem_f32<FMT>(elem_bits<FMT>(row, e));
+  const double d = exp(a.sigmoid ? -(double)x : x - top);
+  const double key = (a.sigmoid ? 1.0 / (1.0 + d) : d / sum) + (double)bias[e];
+  if (held) keys[l] = key;
+  wave_sync();
+  if (held) {
+    int rank = 0;
+    for (int j = 0; j < around; ++j) rank += keys[j] > key || (keys[j] == key && ids[j] < e);
+    if (rank < a.topk) {
+      chosen[rank] = e;
+      logit[rank] = x;
+    }
+  }
+  wave_sync();
 }
 
 // choose_exactly for each of a wave's tokens whose lanes say `again`; t0, slot: the first of them, and its place in
@@ -464,6 +512,8 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
   __shared__ double keys[4][L * V < 64 ? 64 : L * V];  // of the choice in float64: a wave's
   __shared__ float bias_of[L * V];         // -inf for NaN
   __shared__ Choice list[kTokens][8];
+  __shared__ double near_keys[kTokens][L];
+  __shared__ int near_ids[kTokens][L];
   __shared__ int chosen[kTokens][8];
   __shared__ float logit[kTokens][8];
   RouteArgs a = first;
@@ -482,8 +532,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
     const bool sums = grouped && (scored || a.best > 1);
     int key[V];
     bool open, bad;
-    float top = 0.f, sum = 1.f, by = 1.f;
-    const float error = score_error(a.sigmoid);
+    float top = 0.f, sum = 1.f, by = 1.f, error;
     {
       float x[V];
       load_row<FMT, L>(x, a, held ? t : a.tokens - 1, e0);
@@ -500,6 +549,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
         soft_stats<L>(x, top, sum);
         by = one_over(sum);
       }
+      error = score_error(a.sigmoid, by);
       if (scored || sums) {
         float g[V];
 #pragma unroll
@@ -527,10 +577,18 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
           });
           if (a.best > 1 && b2 > -kInf) b1 += b2;
           int before = 0;
+          bool close = false;
           for (int r = lanes; r < L; r += lanes) {  // the group r lanes before, around the row
             const float o = __shfl(b1, (l - r) & (L - 1), L);
             before += o > b1 || (o == b1 && l >= r);
-            open |= fabsf(o - b1) <= 8 * error + 0x1p-21f * fabsf(o);
+            close |= fabsf(o - b1) <= group_error(error, o);
+          }
+          if (__ballot(close)) {  // it matters between one that is kept and one that is not
+            for (int r = lanes; r < L; r += lanes) {
+              const float o = __shfl(b1, (l - r) & (L - 1), L);
+              const int ob = __shfl(before, (l - r) & (L - 1), L);
+              open |= fabsf(o - b1) <= group_error(error, o) && (ob < a.top_groups) != (before < a.top_groups);
+            }
           }
 #pragma unroll
           for (int i = 0; i < V; ++i) key[i] = before < a.top_groups ? key[i] : kNone;
@@ -622,7 +680,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
     wave_sync();
     int rank = 0;
     bool close = false;
-    const float tolerance = 4 * error + 0x1p-22f * fabsf(c.key);
+    const float tolerance = key_error(error, c.key);
     for (int j = 0; j < a.topk; ++j) {
       const Choice o = list[slot][j];
       const bool other = j < n && j != l;
@@ -633,25 +691,31 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
     if (l < n) {
       chosen[slot][rank] = c.e;
       logit[slot][rank] = c.x;
-      if (scored) open |= close;
     }
     if (scored) {
       // those that are not chosen but as near to the last chosen one as keys may be off
       const float f = of_ordered(least);
-      const int near = all ? least : ordered(f - (4 * error + 0x1p-22f * fabsf(f)));
-      int around = 0;
+      const int near = all ? least : ordered(f - key_error(error, f));
+      uint32_t within = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) around += key[i] >= near;
-      if (__ballot(row_sum<L>(around) > n)) {
+      for (int i = V - 1; i >= 0; --i) within = within + within + (key[i] >= near);
+      const int own = __builtin_popcount(within), around = row_sum<L>(own);
+      bool unclear = l < n && close;
+      if (__ballot(around > n)) {
         // (the last chosen one's logit and bias)
         float lx = 0.f, lb = 0.f;
         for (int j = 0; j < n; ++j)
           if (ordered(list[slot][j].key) == least) lx = list[slot][j].x, lb = list[slot][j].bias;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (key[i] >= near && !(taken >> i & 1))
-            open |= elem_f32<FMT>(elem_bits<FMT>(row, e0 + i)) != lx || bias_of[e0 + i] != lb;
+        for (uint32_t rest = within & ~taken; rest; rest &= rest - 1) {
+          const int e = e0 + __builtin_ctz(rest);
+          unclear |= elem_f32<FMT>(elem_bits<FMT>(row, e)) != lx || bias_of[e] != lb;
+        }
       }
+      unclear = row_ballot<L>(unclear) != 0;
+      open |= unclear && around > L;
+      if (__ballot(unclear && !open))
+        order_exactly<FMT, L>(a, row, bias_of, unclear && around <= L, within, row_scan<L>(own) - own, around, e0,
+                              near_keys[slot], near_ids[slot], chosen[slot], logit[slot]);
     }
     wave_sync();
     choose_again<FMT, L>(row_ballot<L>(open) != 0, bad, t - slot % (64 / L), slot - slot % (64 / L),
