@@ -80,6 +80,19 @@ template <int STEP>
 __device__ __forceinline__ double across(double v) {
   return __shfl_xor(v, 1 << STEP, 64);
 }
+// f(the value r lanes before, around the token's lanes, and r) for the multiples of `apart` (a power of two) below L.
+template <int L, class T, class F>
+__device__ __forceinline__ void around_row(T v, int apart, F &&f) {
+  if constexpr (L == 16) {
+    steps<15>([&](auto s) {
+      constexpr int R = s.value + 1;
+      if ((R & (apart - 1)) == 0)  // uniform
+        f(__builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x120 + R, 0xf, 0xf, true)), R);
+    });
+  } else {
+    for (int r = apart; r < L; r += apart) f(__shfl(v, ((threadIdx.x & (L - 1)) - r) & (L - 1), L), r);
+  }
+}
 template <int L, class T>
 __device__ __forceinline__ T row_max(T v) {
   steps<log2_of(L)>([&](auto s) {
@@ -578,11 +591,10 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
           if (a.best > 1 && b2 > -kInf) b1 += b2;
           int before = 0;
           bool close = false;
-          for (int r = lanes; r < L; r += lanes) {  // the group r lanes before, around the row
-            const float o = __shfl(b1, (l - r) & (L - 1), L);
+          around_row<L>(b1, lanes, [&](float o, int r) {  // the other groups'
             before += o > b1 || (o == b1 && l >= r);
             close |= fabsf(o - b1) <= group_error(error, o);
-          }
+          });
           if (__ballot(close)) {  // it matters between one that is kept and one that is not
             for (int r = lanes; r < L; r += lanes) {
               const float o = __shfl(b1, (l - r) & (L - 1), L);
@@ -606,10 +618,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
           }
         });
         int before = 0;
-        for (int r = lanes; r < L; r += lanes) {
-          const int o = __shfl(b1, (l - r) & (L - 1), L);
-          before += o > b1 || (o == b1 && l >= r);
-        }
+        around_row<L>(b1, lanes, [&](int o, int r) { before += o > b1 || (o == b1 && l >= r); });
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = before < a.top_groups ? key[i] : kNone;
       }
