@@ -341,6 +341,40 @@ def test_product_of_activations(M, N, K, fmt):
         assert (c[z, m:] == 55.0).all()
 
 
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("K,pad", [(128, 0), (640, 3), (4096, 0), (8192, 8), (8320, 0), (16384, 1), (16512, 0)])
+@pytest.mark.parametrize("M", [1, 2, 3])
+def test_activations_of_few_rows(M, K, pad, fmt):
+    """Activations in padded rows with NaN behind them, blocks of NaN, zeros and infinities among theirs; more columns
+    than the kernels hold at once, an odd number of them; counts that leave rows as they are."""
+    import torch
+
+    g = gen(M * 31 + K)
+    N = 16 * 512 * 2 + 37
+    say(f"[gpu] mx4 activations of few rows {M}x{N}x{K}+{pad} {fmt}")
+    x, _ = strided(M, K, K + pad, math.nan, dtypes()[fmt])
+    x.copy_(torch.randn((M, K), generator=g, device="cuda"))
+    x[:, 32:64] = 0
+    w, ws = tsm.quantize_mx4(torch.randn((N, K), generator=g, device="cuda"))
+    vw = ref.values(w, ws, K)
+    for rows in (None, *range(M + 1)):
+        if rows == M:
+            x[0, 96 + K // 256 * 7] = math.nan
+        if rows == 0 and M == 2:
+            x[1, 5] = math.inf
+        m = M if rows is None else rows
+        count = None if rows is None else torch.tensor([rows], dtype=torch.int32, device="cuda")
+        c = torch.full((1, M, N), 55.0, device="cuda", dtype=dtypes()[fmt])
+        tsm.matmul_mx4(x[None], None, w[None].transpose(1, 2), ws[None], rows=count, out=c)
+        assert (c[:, m:] == 55.0).all()
+        if m:
+            q, s = tsm.quantize_mx4(x[:m])
+            want, mag = ref.product(ref.values(q, s, K), vw)
+            nan = want.isnan()
+            assert torch.equal(c[0, :m].isnan(), nan)
+            check_product(c[0, :m].masked_fill(nan, 0), want.masked_fill(nan, 0), mag.masked_fill(nan, 0), K, fmt)
+
+
 def test_empty_sums_and_sizes():
     import torch
 

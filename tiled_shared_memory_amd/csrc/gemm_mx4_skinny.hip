@@ -1,16 +1,18 @@
 // Products of microscaled 4-bit codes of few rows (decoding steps) for gfx950: bound
 // by reading the weights once.
 //
-// The streaming kernel of the int8 products (gemm_i8_skinny.hip): a workgroup owns a
-// block of C, its waves share out K in steps of 512 elements (256 bytes of a row),
-// each copies its steps into an LDS ring of its own and multiplies from there, and
-// their float32 sums meet in LDS, added in the order of the waves.  The workgroups
-// stay for all of the tiles and the copies run on across tile boundaries.
+//  * stream: up to 64 rows.  The streaming kernel of the int8 products
+//    (gemm_i8_skinny.hip): waves copy A's rows and the weights through LDS rings of
+//    their own and multiply from there.
+//  * rows: activations of one or two rows, quantised within the launch.  Every workgroup
+//    keeps all of A in LDS, after quantising it by itself while its first copies of
+//    the weights are on their way; only the weights pass through the waves' rings.
 //
 // A lane takes blocks 4g .. 4g + 3 of a step's sixteen (g = lane / 16) in its four
-// matrix instructions, so that its scales of a step are one word per 16 rows, loaded
-// straight into a register beside the copies.
+// matrix instructions, so that its scales of a step are one word per 16 rows; those of
+// the weights are loaded straight into a register beside the copies.
 #include "lds_ring.hpp"
+#include "mx4_codes.hpp"
 #include "mx4_common.hpp"
 
 namespace tsm {
@@ -229,10 +231,178 @@ hipError_t stream_t(Mx4Args a, hipStream_t st) {
   return hipSuccess;
 }
 
+// ---- activations of one or two rows, kept in LDS ---------------------------------
+constexpr int kRowWaves = 4, kRowThreads = kRowWaves * 64, kRing = 4;
+constexpr int kRowWave = 4096 + 256;             // a wave's ring stage: 16 columns x 256 bytes, and their scales
+constexpr int kRowStage = kRowWaves * kRowWave;
+constexpr int kStepRow = STEP + BLOCKS;      // a row of a step of A: codes and scale bytes
+constexpr int kRowSteps = 2 * kRowWaves;     // rows times steps of A in each array
+// A wave's step q takes ring stage q % 4, and its part of A lies in the same array as that stage: a read of an array
+// waits for the copies into it (the compiler sees to it), and those into the other three stay in flight.
+constexpr int kRowArray = kRowStage + kRowSteps * kStepRow;
+
+// Byte offset in its array of step s of A (M rows); the arrays take wave after wave of a turn's steps.
+__device__ __forceinline__ int step_at(int s, int M) {
+  return kRowStage + (s / (kRing * kRowWaves) * kRowWaves + s % kRowWaves) * M * kStepRow;
+}
+
+// Writes to LDS that the compiler does not see: it would wait for every copy in flight before them.
+__device__ __forceinline__ uint32_t lds_at(const char *at) { return (uint32_t)(uintptr_t)(lds_void *)at; }
+
+// All of X in registers, a thread's chunks of 8 elements of each row kRowThreads apart (rows past the last one and chunks
+// past K load the first in their place).
+constexpr int kRowChunks = kRowSteps * kRing * (2 * STEP / 8) / kRowThreads;
+template <int XF>
+__device__ __forceinline__ void load_rows(const Mx4Args &p, int rows, int per, Chunk<XF> (&ch)[kRowChunks]) {
+#pragma unroll
+  for (int i = 0; i < kRowChunks; ++i) {
+    const int r = i / 4 * 4 / per, c = (i - r * per) * kRowThreads + threadIdx.x;  // a turn's 16 steps are 4 chunks a thread
+    ch[i].load((const char *)p.X + (r < rows ? r : 0) * p.ldx * fmt_bytes(XF), c * 8 < p.K ? c : 0);
+  }
+}
+
+// Their codes and scales to LDS, zeros past K: four lanes hold a block of 32.  Chunk c of a row of a step lies at c ^ row.
+template <int XF>
+__device__ __forceinline__ void keep_rows(const Mx4Args &p, const Chunk<XF> (&ch)[kRowChunks], int rows, int per,
+                                          const uint32_t (&array)[kRing]) {
+#pragma unroll
+  for (int i = 0; i < kRowChunks; ++i) {
+    const int r = i / 4 * 4 / per, c = (i - r * per) * kRowThreads + threadIdx.x;
+    if (r >= rows) break;  // uniform
+    const uint32_t e = c * 8 < p.K ? scale_byte(quad_max(ch[i].top())) : 0u;
+    const uint32_t codes = e == 255u || c * 8 >= p.K ? 0u : codes_of<XF>(ch[i], scale_of(e));
+    const int s = c / (2 * STEP / 8), in = c % (2 * STEP / 8);
+    // a thread's chunk i is of step 4 i + threadIdx.x / 64 of its row, and so of array i % 4
+    static_assert(kRowThreads == kRowWaves * (2 * STEP / 8) && kRing == 4);
+    const uint32_t to = array[i % 4] + step_at(s, (int)p.M) + r * kStepRow;
+    asm volatile("ds_write_b32 %0, %1" ::"v"(to + (((in >> 2) ^ r) * 16) + (in & 3) * 4), "v"(codes) : "memory");
+    if ((in & 3) == 0) asm volatile("ds_write_b8 %0, %1" ::"v"(to + STEP + (in >> 2)), "v"(e) : "memory");
+  }
+}
+
+template <int XF>
+__device__ __forceinline__ void rows_product(const Mx4Args &p) {
+  __shared__ __attribute__((aligned(1024))) char s0[kRowArray], s1[kRowArray], s2[kRowArray], s3[kRowArray];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tiles = p.tiles_n;
+  const int steps = (int)((p.kb + STEP - 1) / STEP);
+  const int turns = (steps + kRing * kRowWaves - 1) / (kRing * kRowWaves);
+  const int M = (int)p.M;
+  const int rows = (int)valid_rows(p, 0);
+  if (rows == 0) return;
+  // wave-load g: rows 4 g + lane / 16 of the weights; position lane % 16 of a row holds chunk (lane % 16) ^ (row % 16)
+  auto row_of = [&](int g) { return 4 * g + (lane >> 4); };
+  auto chunk_of = [&](int g) { return ((lane & 15) ^ (row_of(g) & 15)) * 16; };
+  uint32_t off[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) off[g] = (uint32_t)(row_of(g) * p.ldb + chunk_of(g));
+  const uint32_t offb = (uint32_t)((lane & 15) * p.ldsb + (lane >> 4) * 4);
+  int mine = wave * kRowWave;
+  auto array = [&](int d) -> char * { return d == 0 ? s0 : d == 1 ? s1 : d == 2 ? s2 : s3; };
+  auto stage = [&](int d) -> char * {
+    asm volatile("" : "+s"(mine));  // (as in the streaming kernel)
+    return array(d) + mine;
+  };
+  __amdgpu_buffer_rsrc_t rb, rsb;
+  int ft = blockIdx.x, fq = 0;
+  auto open = [&](int t) {
+    const Mx4Args q = args_again();
+    const int64_t n0 = (int64_t)t * 16, vn = q.N - n0 < 16 ? q.N - n0 : 16;
+    rb = make_rsrc(q.B + n0 * q.ldb, (uint32_t)((vn - 1) * q.ldb + q.kb));
+    rsb = make_rsrc(q.SB + n0 * q.ldsb, (uint32_t)((vn - 1) * q.ldsb + q.nb));
+  };
+  // The next step's copies into stage d; chunks past K and steps past the end copy zeros without touching memory, their
+  // scales too.
+  auto fetch = [&](int d) {
+    const int s = fq * kRowWaves + wave;
+    const int left = ft < tiles && s < steps ? (int)(p.kb - (int64_t)s * STEP) : 0;
+    char *const to = stage(d);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(to + g * 1024), 16, chunk_of(g) < left ? off[g] : kOutside,
+                                               left ? s * STEP : 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(to + 4096), 4, (lane >> 4) * 64 < left ? offb : kOutside,
+                                             left ? s * BLOCKS : 0, 0, 0);
+    if (++fq == turns * kRing) {
+      fq = 0;
+      ft += gridDim.x;
+      if (ft < tiles) open(ft);
+    }
+  };
+  {
+    // the activations first: what is loaded after the copies would arrive after them
+    Chunk<XF> ch[kRowChunks];
+    load_rows<XF>(p, rows, 4 * turns, ch);
+    open(ft);
+    unrolled<kRing - 1>([&](auto d) { fetch(d.value); });
+    const uint32_t at[kRing] = {lds_at(s0), lds_at(s1), lds_at(s2), lds_at(s3)};
+    keep_rows<XF>(p, ch, rows, 4 * turns, at);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+  // rows past the last one multiply row 0: their results are not stored
+  const int r = lane & 15, ra = r < rows ? r : 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    f32x4 acc{};
+    for (int q = 0; q < turns; ++q) {
+      unrolled<kRing>([&](auto d) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        fetch((d.value + kRing - 1) % kRing);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(5 * (kRing - 1)) : "memory");
+        const char *const b = stage(d.value), *const base = array(d.value);
+        int at_a = step_at((kRing * q + d.value) * kRowWaves + wave, M) + ra * kStepRow;
+        asm("" : "+v"(at_a));
+        const uint32_t wa = *reinterpret_cast<const uint32_t *>(base + at_a + STEP + (lane >> 4) * 4);
+        int at_s = 4096 + lane * 4;
+        asm("" : "+v"(at_s));
+        const uint32_t wb = *reinterpret_cast<const uint32_t *>(b + at_s);
+        unrolled<4>([&](auto u) {
+          int at = r * STEP + ((4 * (lane >> 4) + u.value) ^ r) * 16;
+          asm("" : "+v"(at));
+          const u32x4 fa = *reinterpret_cast<const u32x4 *>(base + at_a + ((4 * (lane >> 4) + u.value) ^ ra) * 16);
+          const u32x4 fb = *reinterpret_cast<const u32x4 *>(b + at);
+          acc = mfma_mx4<u.value, u.value>(fb, wb, fa, wa, acc);
+        });
+      });
+    }
+    // the waves' sums meet in the stage just read, which the next tile's first step refills
+    asm volatile("s_nop 15\n\ts_nop 15\n\tds_write_b128 %0, %1" ::"v"(lds_at(stage(kRing - 1)) + lane * 16), "v"(acc)
+                 : "memory");
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (wave == 0) {
+      const Mx4Args e = args_again();
+      const int64_t n = (int64_t)t * 16 + 4 * (lane >> 4);
+      if (r < rows && n < e.N) {
+        f32x4 sum{};
+#pragma unroll
+        for (int w = 0; w < kRowWaves; ++w)
+          sum += *reinterpret_cast<const f32x4 *>(array(kRing - 1) + w * kRowWave + lane * 16);
+        const Epilogue ep{e.act, e.slope, false};
+        char *const row = (char *)e.C + r * e.ldc * (e.fmt == FMT_F32 ? 4 : 2);
+        if (e.fmt == FMT_F32) store_mx4<FMT_F32>(e, ep, row, n, sum);
+        else if (e.fmt == FMT_F16) store_mx4<FMT_F16>(e, ep, row, n, sum);
+        else store_mx4<FMT_BF16>(e, ep, row, n, sum);
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();  // the sums are read
+    asm volatile("" ::: "memory");
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the copies of zeros past the end
+}
+
+template <int XF>
+__global__ __launch_bounds__(kRowThreads, 2) void gemm_mx4_rows_kernel(Mx4Args p) {
+  rows_product<XF>(p);
+}
+
 }  // namespace
 
-Mx4Stream mx4_stream_plan(const Mx4Args &p) {
-  Mx4Stream s;
+Mx4Few mx4_few_plan(const Mx4Args &p) {
+  Mx4Few s;
   // (more columns than tile numbers hold go to the general kernel)
   if (p.M > 64 || p.K == 0 || p.N > 0xffffffffLL / 256 * 16) return s;
   const bool aligned = (((uintptr_t)p.A | (uintptr_t)p.B) & 15) == 0 && (((uintptr_t)p.SA | (uintptr_t)p.SB) & 3) == 0 &&
@@ -240,8 +410,8 @@ Mx4Stream mx4_stream_plan(const Mx4Args &p) {
                        ((p.ldsa | p.ldsb | p.strideSA | p.strideSB) & 3) == 0;
   // 32-bit offsets over a block's rows
   const int64_t limit = (int64_t)1 << 30;
-  s.can = aligned && 32 * p.lda + p.kb < limit && 32 * p.ldb + p.kb < limit && 32 * p.ldsa + p.nb < limit &&
-          32 * p.ldsb + p.nb < limit;
+  s.can_stream = aligned && 32 * p.lda + p.kb < limit && 32 * p.ldb + p.kb < limit && 32 * p.ldsa + p.nb < limit &&
+                 32 * p.ldsb + p.nb < limit;
   const int64_t per = (p.N + 15) / 16;
   const int64_t tiles = per > ((int64_t)1 << 40) / p.batch ? (int64_t)1 << 40 : per * p.batch;
   if (p.M <= 16) {
@@ -253,14 +423,34 @@ Mx4Stream mx4_stream_plan(const Mx4Args &p) {
     s.nb = tiles >= (p.M > 32 ? 512 : 1536) ? 2 : 1;
     s.waves = s.nb == 2 ? 1 : 2;
   }
-  s.use = s.can && !(p.M > 32 && tiles >= 768 && !p.rows);
+  s.use_stream = s.can_stream && !(p.M > 32 && tiles >= 768 && !p.rows);
   return s;
 }
 
 hipError_t launch_mx4_stream(const Mx4Args &p, hipStream_t st) {
-  const Mx4Stream s = mx4_stream_plan(p);
+  const Mx4Few s = mx4_few_plan(p);
   if (s.rows == 16) return s.waves == 1 ? stream_t<16, 1, 1>(p, st) : stream_t<16, 1, 4>(p, st);
   return s.nb == 1 ? stream_t<32, 1, 2>(p, st) : stream_t<32, 2, 1>(p, st);
+}
+
+bool mx4_rows_supports(const Mx4Args &p) {
+  const int64_t turns = (p.kb + kRing * kRowWaves * STEP - 1) / (kRing * kRowWaves * STEP);
+  return p.batch == 1 && p.K > 0 && turns * kRowWaves * p.M <= kRowSteps && p.N <= 0x3fffffff && p.K % 128 == 0 &&
+         ((uintptr_t)p.B & 15) == 0 && (p.ldb & 15) == 0 && (((uintptr_t)p.SB | p.ldsb) & 3) == 0 &&
+         16 * p.ldb + p.kb < ((int64_t)1 << 30) && 16 * p.ldsb + p.nb < ((int64_t)1 << 30);
+}
+
+hipError_t launch_mx4_rows(const Mx4Args &p, int xfmt, hipStream_t st) {
+  Mx4Args a = p;
+  a.tiles_n = (int32_t)((a.N + 15) / 16);
+  const dim3 grid((unsigned)(a.tiles_n < 512 ? a.tiles_n : 512)), block(kRowThreads);  // two per CU
+  if (xfmt == FMT_F32)
+    hipLaunchKernelGGL((gemm_mx4_rows_kernel<FMT_F32>), grid, block, 0, st, a);
+  else if (xfmt == FMT_F16)
+    hipLaunchKernelGGL((gemm_mx4_rows_kernel<FMT_F16>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((gemm_mx4_rows_kernel<FMT_BF16>), grid, block, 0, st, a);
+  return hipGetLastError();
 }
 
 }  // namespace tsm

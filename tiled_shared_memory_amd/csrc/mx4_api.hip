@@ -150,8 +150,8 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
   const bool half = M <= 128 && tiles128 * batch <= 256;  // 256-tiles half empty, and a round of 128-tiles does it
   const int64_t tiles256 = ((M + 255) / 256) * ((N + 255) / 256) * batch;
   if (M > 64 && !half && tiles256 >= kFewTiles && mx4_tile_supports(p)) call->kernel = Mx4Kernel::Tile;
-  const Mx4Stream stream = mx4_stream_plan(p);
-  if (stream.use) call->kernel = Mx4Kernel::Stream;
+  const Mx4Few few = mx4_few_plan(p);
+  if (few.use_stream) call->kernel = Mx4Kernel::Stream;
   // TSM_GEMM_KERNEL=<name> forces a variant (tests and tuning); names of other
   // families are left alone, a variant that cannot run the problem is an error.
   const char *force = getenv("TSM_GEMM_KERNEL");
@@ -161,7 +161,7 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
       if (strcmp(force, mx4_name(k)) == 0) want = k;
     if (want == Mx4Kernel::None) return fail(TSM_ERROR_INVALID_VALUE, "TSM_GEMM_KERNEL=%s names no kernel", force);
     if ((want == Mx4Kernel::Block64 && tiles64 * 512 > 0xffffffffLL) ||
-        (want == Mx4Kernel::Tile && !mx4_tile_supports(p)) || (want == Mx4Kernel::Stream && !stream.can))
+        (want == Mx4Kernel::Tile && !mx4_tile_supports(p)) || (want == Mx4Kernel::Stream && !few.can_stream))
       return fail(TSM_ERROR_NOT_SUPPORTED, "TSM_GEMM_KERNEL=%s cannot run this problem", force);
     call->kernel = want;
     call->forced = true;
@@ -356,6 +356,12 @@ int gemm_mx4_float_a(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx
                 B, ldb, strideB, scale_b, ld_sb, stride_sb, C, ldc, strideC, batch, rows, false, out_dtype, activation,
                 slope, &c);
   if (st != TSM_SUCCESS) return st;
+  if (c.kernel == Mx4Kernel::Stream && !c.forced && mx4_rows_supports(c.p)) {
+    c.p.X = X;
+    c.p.ldx = ldx;
+    c.p.strideX = strideX;
+    return launched(launch_mx4_rows(c.p, xdtype, (hipStream_t)stream));
+  }
   if (K > 0) {
     const Mx4QuantArgs q{X, (uint8_t *)codes, (uint8_t *)scales, M, K, ldx, room.ld, room.lds, strideX, M * room.ld,
                          M * room.lds, groups, groups > 1 || batch == 1 ? rows : nullptr, xdtype, 0, 0};

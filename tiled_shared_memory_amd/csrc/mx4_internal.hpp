@@ -16,6 +16,8 @@ struct Mx4Args {
   const int8_t *A, *B;      // codes
   const uint8_t *SA, *SB;   // scale bytes
   void *C;
+  const void *X;            // few rows: activations to quantise, in A's place
+  int64_t ldx, strideX;
   int64_t M, N, K;          // K in elements
   int64_t kb, nb;           // bytes of codes and of scales per row
   int64_t lda, ldb, ldsa, ldsb, ldc;  // bytes; of C elements
@@ -43,13 +45,16 @@ hipError_t launch_mx4_rest(const Mx4Args &a, hipStream_t stream);
 int device_cus();
 
 enum class Mx4Kernel { None, Block128, Block64, Tile, Stream };
-// Few rows (up to 64).
-struct Mx4Stream {
-  bool can = false, use = false;     // what the problem allows; the rule's choice
-  int rows = 0, nb = 0, waves = 0;   // rows by 16 nb columns per workgroup of `waves` waves
+// Few rows (up to 64): what the problem allows, and the rule's choice.
+struct Mx4Few {
+  bool can_stream = false, use_stream = false;
+  int rows = 0, nb = 0, waves = 0;  // streaming: rows by 16 nb columns per workgroup of `waves` waves
 };
-Mx4Stream mx4_stream_plan(const Mx4Args &p);
+Mx4Few mx4_few_plan(const Mx4Args &p);
 hipError_t launch_mx4_stream(const Mx4Args &p, hipStream_t stream);
+// Activations X of format xfmt in A's place, quantised within the launch.
+bool mx4_rows_supports(const Mx4Args &p);
+hipError_t launch_mx4_rows(const Mx4Args &p, int xfmt, hipStream_t stream);
 hipError_t launch_mx4_block(const Mx4Args &p, int tile, hipStream_t stream);
 
 struct Mx4QuantArgs {
