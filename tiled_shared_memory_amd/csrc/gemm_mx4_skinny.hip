@@ -1,16 +1,30 @@
 // Products of microscaled 4-bit codes of few rows (decoding steps) for gfx950: bound
 // by reading the weights once.
 //
-//  * stream: up to 64 rows.  The streaming kernel of the int8 products
-//    (gemm_i8_skinny.hip): waves copy A's rows and the weights through LDS rings of
-//    their own and multiply from there.
+//  * stream: up to 64 rows.  Persistent workgroups of one or two waves, each tile all
+//    rows by 32 or 64 columns of a problem.  The waves of a workgroup share out K in
+//    steps of 512 elements (256 bytes of a row); each copies its steps' codes and
+//    scales of both operands into an LDS ring of its own with direct loads, without a
+//    barrier, and multiplies from there; their float32 sums meet in LDS and are added
+//    in the order of the waves.  The copies run on across tile boundaries.  The
+//    weights, which no other tile reads, are loaded non-temporally.
 //  * rows: activations of one or two rows, quantised within the launch.  Every workgroup
 //    keeps all of A in LDS, after quantising it by itself while its first copies of
 //    the weights are on their way; only the weights pass through the waves' rings.
 //
 // A lane takes blocks 4g .. 4g + 3 of a step's sixteen (g = lane / 16) in its four
-// matrix instructions, so that its scales of a step are one word per 16 rows; those of
-// the weights are loaded straight into a register beside the copies.
+// matrix instructions, so that its scales of a step are one word per 16 rows.  What
+// decides is that the copies never stop, and the compiler's waits stand in the way of
+// that: an array of LDS for each stage, scales that come through LDS too, counts by
+// scalar loads and writes that it does not see keep the loop free of waits for
+// everything in flight.
+//
+// Measured, bf16 out, weights from memory (a copy reaches 5.1 TB/s on the same card):
+//   16 x 16384 x 8192   17.0 us a call, 4.2 TB/s  (scales in registers, whose copies at
+//                       the loop's end waited: 21.5; then weights through all caches: 18.3)
+//   8 x 28672 x 8192    26.5 us, 4.7 TB/s     8 x 8192 x 28672   23.0 us, 5.4 TB/s
+//   64 groups of 4 x 2048 x 4096   48.5 us, 5.9 TB/s (part of it from the cache)
+//   1 x 8192 x 8192 from bf16   9.5 us, in two launches 15 (rings of 2 stages: 13.5)
 #include "lds_ring.hpp"
 #include "mx4_codes.hpp"
 #include "mx4_common.hpp"
@@ -21,32 +35,39 @@ namespace {
 constexpr int STEP = 256;  // bytes of codes per step and row
 constexpr int BLOCKS = STEP / 16;
 
+constexpr int kOnce = 2;  // (cache policy: non-temporal) of the weights, which are read once
+
 struct Place {
-  int64_t z, m0, n0, M;
+  int64_t z, n0, M;
 };
+
+// Valid rows of problem z, by a scalar load: the vector load that the compiler would choose waits, in its turn, for the
+// copies in flight.
+__device__ __forceinline__ int64_t rows_of(const Mx4Args &p, int64_t z) {
+  if (!p.rows) return p.M;
+  const int64_t r = ((const __attribute__((address_space(4))) int32_t *)p.rows)[z];
+  return r < 0 ? 0 : (r > p.M ? p.M : r);
+}
 
 constexpr int kMaxGroups = 512;  // groups of a launch, whose tiles before each are kept in LDS
 
-// Place of tile t: row tiles fastest, then columns, then problems.  first: of a grouped call, the tiles before each
-// group (in LDS, kMaxGroups of them, the ones past the launch's groups holding the total).
-template <int AR, int NB>
+// Place of tile t: columns, then problems.  first: of a grouped call, the tiles before each group, those of empty groups
+// left out (in LDS, kMaxGroups of them, the ones past the launch's groups holding the total).
+template <int NB>
 __device__ __forceinline__ Place stream_tile(const Mx4Args &p, int t, const int *first, int lane) {
   Place e;
-  int tm = p.tiles_m, g = 0;
+  int g = 0;
   if (p.rows) {
     for (int i = 0; i < p.nz; i += 64) g += __popcll(__ballot(first[i + lane] <= t));
     g = min(g, p.nz) - 1;
-    const int f = __builtin_amdgcn_readfirstlane(first[g]);
-    tm = (int)((valid_rows(p, p.z0 + g) + AR - 1) / AR);
-    t -= f;
+    t -= __builtin_amdgcn_readfirstlane(first[g]);
   } else {
-    g = t / (tm * p.tiles_n);
-    t -= g * (tm * p.tiles_n);
+    g = t / p.tiles_n;
+    t -= g * p.tiles_n;
   }
   e.z = p.z0 + g;
-  e.M = valid_rows(p, e.z);
-  e.m0 = (int64_t)(t % tm) * AR;
-  e.n0 = (int64_t)(t / tm) * (16 * NB);
+  e.M = rows_of(p, e.z);
+  e.n0 = (int64_t)t * (16 * NB);
   return e;
 }
 
@@ -58,16 +79,33 @@ __device__ __forceinline__ Mx4Args args_again() {
   return *(const Mx4Args *)p;
 }
 
+__device__ __forceinline__ uint32_t lds_at(const char *at) { return (uint32_t)(uintptr_t)(lds_void *)at; }
+
+// Writes to LDS that the compiler does not see: it would wait for every copy in flight before them.
+__device__ __forceinline__ void lds_write4(uint32_t at, uint32_t v) {
+  asm volatile("ds_write_b32 %0, %1" ::"v"(at), "v"(v) : "memory");
+}
+__device__ __forceinline__ void lds_write1(uint32_t at, uint32_t v) {
+  asm volatile("ds_write_b8 %0, %1" ::"v"(at), "v"(v) : "memory");
+}
+// (with the wait that a matrix instruction's result needs)
+__device__ __forceinline__ void lds_write_sums(uint32_t at, f32x4 v) {
+  asm volatile("s_nop 15\n\ts_nop 15\n\tds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
+}
+
 template <int AR, int NB, int W, int FMT>
 __device__ __forceinline__ void stream(const Mx4Args &p) {
   constexpr int MB = AR / 16;
   constexpr int LA = AR / 4, LB = 4 * NB, L = LA + LB;  // wave-loads (1 KiB: 4 rows) per step
-  constexpr int BYTES = L * 1024;
-  __shared__ __attribute__((aligned(1024))) char s0[W * BYTES], s1[W * BYTES];  // the ring's two stages
+  constexpr int N = L + MB + NB;                  // with those of the scales, 256 bytes each
+  constexpr int BYTES = L * 1024 + (MB + NB) * 256;
+  // the ring's two stages (deeper ones were no faster), an array each: a read waits for the copies into its array, as
+  // the compiler sees to it
+  __shared__ __attribute__((aligned(1024))) char s0[W * BYTES], s1[W * BYTES];
   __shared__ int first[kMaxGroups];
   static_assert(MB * NB <= L, "a wave's sums fit one stage");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int tiles = p.tiles_m * p.tiles_n * p.nz;
+  int tiles = p.tiles_n * p.nz;
   if (p.rows) {
     // every wave computes the sums, the first writes them
     int sum = 0;
@@ -102,15 +140,14 @@ __device__ __forceinline__ void stream(const Mx4Args &p) {
   // The copies run one step ahead of the products: step fq of tile ft, through resources over its valid rows
   // (others lie past them, since leading dimensions are at least a row's bytes, and load as zeros).
   __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
-  uint32_t wa[2][MB], wb[2][NB];
   int ft = blockIdx.x, fq = 0;
   auto open = [&](int t) {
     const Mx4Args q = args_again();
-    const Place e = stream_tile<AR, NB>(q, t, first, lane);
-    const int64_t vm = e.M - e.m0 < AR ? e.M - e.m0 : AR, vn = q.N - e.n0 < 16 * NB ? q.N - e.n0 : 16 * NB;
-    ra = make_rsrc(q.A + e.z * q.strideA + e.m0 * q.lda, (uint32_t)((vm - 1) * q.lda + q.kb));
+    const Place e = stream_tile<NB>(q, t, first, lane);
+    const int64_t vn = q.N - e.n0 < 16 * NB ? q.N - e.n0 : 16 * NB;
+    ra = make_rsrc(q.A + e.z * q.strideA, (uint32_t)((e.M - 1) * q.lda + q.kb));
     rb = make_rsrc(q.B + e.z * q.strideB + e.n0 * q.ldb, (uint32_t)((vn - 1) * q.ldb + q.kb));
-    rsa = make_rsrc(q.SA + e.z * q.strideSA + e.m0 * q.ldsa, (uint32_t)((vm - 1) * q.ldsa + q.nb));
+    rsa = make_rsrc(q.SA + e.z * q.strideSA, (uint32_t)((e.M - 1) * q.ldsa + q.nb));
     rsb = make_rsrc(q.SB + e.z * q.strideSB + e.n0 * q.ldsb, (uint32_t)((vn - 1) * q.ldsb + q.nb));
   };
   // The next step's copies into stage d.  Chunks past K, and steps past the end, copy zeros without touching memory
@@ -119,19 +156,20 @@ __device__ __forceinline__ void stream(const Mx4Args &p) {
     const int s = fq * W + wave;
     const int left = ft < tiles && s < steps ? (int)(p.kb - (int64_t)s * STEP) : 0;
     char *const to = stage(d);
-#pragma unroll
-    for (int g = 0; g < L; ++g)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(g < LA ? ra : rb, (lds_void *)(to + g * 1024), 16,
-                                               chunk_of(g) < left ? off[g] : kOutside, left ? s * STEP : 0, 0, 0);
+    unrolled<L>([&](auto g) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(g.value < LA ? ra : rb, (lds_void *)(to + g.value * 1024), 16,
+                                               chunk_of(g.value) < left ? off[g.value] : kOutside, left ? s * STEP : 0, 0,
+                                               g.value < LA ? 0 : kOnce);
+    });
     const bool in = (lane >> 4) * 64 < left;
 #pragma unroll
     for (int i = 0; i < MB; ++i)
-      wa[d][i] = __builtin_amdgcn_raw_buffer_load_b32(rsa, in ? offa + (uint32_t)(16 * i * p.ldsa) : kOutside,
-                                                      left ? s * BLOCKS : 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_void *)(to + L * 1024 + i * 256), 4,
+                                               in ? offa + (uint32_t)(16 * i * p.ldsa) : kOutside, left ? s * BLOCKS : 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < NB; ++j)
-      wb[d][j] = __builtin_amdgcn_raw_buffer_load_b32(rsb, in ? offb + (uint32_t)(16 * j * p.ldsb) : kOutside,
-                                                      left ? s * BLOCKS : 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(to + L * 1024 + (MB + j) * 256), 4,
+                                               in ? offb + (uint32_t)(16 * j * p.ldsb) : kOutside, left ? s * BLOCKS : 0, 0, 0);
     if (++fq == turns * 2) {
       fq = 0;
       ft += gridDim.x;
@@ -147,13 +185,19 @@ __device__ __forceinline__ void stream(const Mx4Args &p) {
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{};
     for (int q = 0; q < turns; ++q) {
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        // the stage read in the last turn is free (its reads are done): refill it
+      unrolled<2>([&](auto d) {
+        // the stage read in the last step is free (its reads are done): refill it
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        fetch(1 - d);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(L + MB + NB) : "memory");
-        const char *a = stage(d), *b = a + LA * 1024;
+        fetch(1 - d.value);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+        const char *a = stage(d.value), *b = a + LA * 1024;
+        int at_s = L * 1024 + lane * 4;
+        asm("" : "+v"(at_s));
+        uint32_t wa[MB], wb[NB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) wa[i] = *reinterpret_cast<const uint32_t *>(a + at_s + i * 256);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) wb[j] = *reinterpret_cast<const uint32_t *>(a + at_s + (MB + j) * 256);
         unrolled<4>([&](auto u) {
           const int r = lane & 15;
           // offset of this lane's chunk; opaque, because a read that the compiler can tell apart from a stage's first
@@ -169,25 +213,25 @@ __device__ __forceinline__ void stream(const Mx4Args &p) {
           for (int i = 0; i < MB; ++i)
 #pragma unroll
             for (int j = 0; j < NB; ++j)
-              acc[i][j] = mfma_mx4<u.value, u.value>(fb[j], wb[d][j], fa[i], wa[d][i], acc[i][j]);
+              acc[i][j] = mfma_mx4<u.value, u.value>(fb[j], wb[j], fa[i], wa[i], acc[i][j]);
         });
-      }
+      });
     }
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
       // (the stage just read is refilled only in the next tile)
-      for (int j = 0; j < NB; ++j) *reinterpret_cast<f32x4 *>(stage(1) + ((i * NB + j) * 64 + lane) * 16) = acc[i][j];
+      for (int j = 0; j < NB; ++j) lds_write_sums(lds_at(stage(1)) + ((i * NB + j) * 64 + lane) * 16, acc[i][j]);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     const Mx4Args e = args_again();
-    const Place o = stream_tile<AR, NB>(e, t, first, lane);
+    const Place o = stream_tile<NB>(e, t, first, lane);
     const Epilogue ep{e.act, e.slope, false};
     for (int k = threadIdx.x; k < MB * NB * 64; k += W * 64) {
       const int blk = k >> 6, l = k & 63;
-      const int64_t m = o.m0 + 16 * (blk / NB) + (l & 15), n = o.n0 + 16 * (blk % NB) + 4 * (l >> 4);
-      if (m >= o.M || m >= o.m0 + AR || n >= e.N) continue;
+      const int64_t m = 16 * (blk / NB) + (l & 15), n = o.n0 + 16 * (blk % NB) + 4 * (l >> 4);
+      if (m >= o.M || n >= e.N) continue;
       f32x4 sum{};
 #pragma unroll
       for (int w = 0; w < W; ++w) sum += *reinterpret_cast<const f32x4 *>(s1 + w * BYTES + k * 16);
@@ -207,10 +251,10 @@ __global__ __launch_bounds__(W * 64) void gemm_mx4_stream_kernel(Mx4Args p) {
 
 template <int AR, int NB, int W>
 hipError_t stream_t(Mx4Args a, hipStream_t st) {
-  constexpr int LDS = 2 * W * (AR / 4 + 4 * NB) * 1024 + 4 * kMaxGroups + 64;
-  a.tiles_m = (int32_t)((a.M + AR - 1) / AR);
+  constexpr int LDS = 2 * W * ((AR / 4 + 4 * NB) * 1024 + (AR / 16 + NB) * 256) + 4 * kMaxGroups;
+  a.tiles_m = 1;
   a.tiles_n = (int32_t)((a.N + 16 * NB - 1) / (16 * NB));
-  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  const int64_t tiles = a.tiles_n;
   // what 256 CUs of 160 KiB hold at once; the rest of the tiles follow in the same workgroups
   const int64_t resident = 256 * (163840 / LDS);
   int64_t most = 0x3fffffff / tiles;  // problems per launch: tile numbers stay far below 2^31
@@ -235,8 +279,8 @@ hipError_t stream_t(Mx4Args a, hipStream_t st) {
 constexpr int kRowWaves = 4, kRowThreads = kRowWaves * 64, kRing = 4;
 constexpr int kRowWave = 4096 + 256;             // a wave's ring stage: 16 columns x 256 bytes, and their scales
 constexpr int kRowStage = kRowWaves * kRowWave;
-constexpr int kStepRow = STEP + BLOCKS;      // a row of a step of A: codes and scale bytes
-constexpr int kRowSteps = 2 * kRowWaves;     // rows times steps of A in each array
+constexpr int kStepRow = STEP + BLOCKS;          // a row of a step of A: codes and scale bytes
+constexpr int kRowSteps = 2 * kRowWaves;         // rows times steps of A in each array
 // A wave's step q takes ring stage q % 4, and its part of A lies in the same array as that stage: a read of an array
 // waits for the copies into it (the compiler sees to it), and those into the other three stay in flight.
 constexpr int kRowArray = kRowStage + kRowSteps * kStepRow;
@@ -245,9 +289,6 @@ constexpr int kRowArray = kRowStage + kRowSteps * kStepRow;
 __device__ __forceinline__ int step_at(int s, int M) {
   return kRowStage + (s / (kRing * kRowWaves) * kRowWaves + s % kRowWaves) * M * kStepRow;
 }
-
-// Writes to LDS that the compiler does not see: it would wait for every copy in flight before them.
-__device__ __forceinline__ uint32_t lds_at(const char *at) { return (uint32_t)(uintptr_t)(lds_void *)at; }
 
 // All of X in registers, a thread's chunks of 8 elements of each row kRowThreads apart (rows past the last one and chunks
 // past K load the first in their place).
@@ -275,8 +316,8 @@ __device__ __forceinline__ void keep_rows(const Mx4Args &p, const Chunk<XF> (&ch
     // a thread's chunk i is of step 4 i + threadIdx.x / 64 of its row, and so of array i % 4
     static_assert(kRowThreads == kRowWaves * (2 * STEP / 8) && kRing == 4);
     const uint32_t to = array[i % 4] + step_at(s, (int)p.M) + r * kStepRow;
-    asm volatile("ds_write_b32 %0, %1" ::"v"(to + (((in >> 2) ^ r) * 16) + (in & 3) * 4), "v"(codes) : "memory");
-    if ((in & 3) == 0) asm volatile("ds_write_b8 %0, %1" ::"v"(to + STEP + (in >> 2)), "v"(e) : "memory");
+    lds_write4(to + (((in >> 2) ^ r) * 16) + (in & 3) * 4, codes);
+    if ((in & 3) == 0) lds_write1(to + STEP + (in >> 2), e);
   }
 }
 
@@ -288,7 +329,7 @@ __device__ __forceinline__ void rows_product(const Mx4Args &p) {
   const int steps = (int)((p.kb + STEP - 1) / STEP);
   const int turns = (steps + kRing * kRowWaves - 1) / (kRing * kRowWaves);
   const int M = (int)p.M;
-  const int rows = (int)valid_rows(p, 0);
+  const int rows = (int)rows_of(p, 0);
   if (rows == 0) return;
   // wave-load g: rows 4 g + lane / 16 of the weights; position lane % 16 of a row holds chunk (lane % 16) ^ (row % 16)
   auto row_of = [&](int g) { return 4 * g + (lane >> 4); };
@@ -320,7 +361,7 @@ __device__ __forceinline__ void rows_product(const Mx4Args &p) {
 #pragma unroll
     for (int g = 0; g < 4; ++g)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(to + g * 1024), 16, chunk_of(g) < left ? off[g] : kOutside,
-                                               left ? s * STEP : 0, 0, 0);
+                                               left ? s * STEP : 0, 0, kOnce);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_void *)(to + 4096), 4, (lane >> 4) * 64 < left ? offb : kOutside,
                                              left ? s * BLOCKS : 0, 0, 0);
     if (++fq == turns * kRing) {
@@ -367,8 +408,7 @@ __device__ __forceinline__ void rows_product(const Mx4Args &p) {
       });
     }
     // the waves' sums meet in the stage just read, which the next tile's first step refills
-    asm volatile("s_nop 15\n\ts_nop 15\n\tds_write_b128 %0, %1" ::"v"(lds_at(stage(kRing - 1)) + lane * 16), "v"(acc)
-                 : "memory");
+    lds_write_sums(lds_at(stage(kRing - 1)) + lane * 16, acc);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -410,27 +450,35 @@ Mx4Few mx4_few_plan(const Mx4Args &p) {
                        ((p.ldsa | p.ldsb | p.strideSA | p.strideSB) & 3) == 0;
   // 32-bit offsets over a block's rows
   const int64_t limit = (int64_t)1 << 30;
-  s.can_stream = aligned && 32 * p.lda + p.kb < limit && 32 * p.ldb + p.kb < limit && 32 * p.ldsa + p.nb < limit &&
-                 32 * p.ldsb + p.nb < limit;
-  const int64_t per = (p.N + 15) / 16;
-  const int64_t tiles = per > ((int64_t)1 << 40) / p.batch ? (int64_t)1 << 40 : per * p.batch;
-  if (p.M <= 16) {
-    s.rows = 16;
-    s.nb = 1;
-    s.waves = tiles >= 1024 && tiles >= p.K / 4 ? 1 : 4;
-  } else {
-    s.rows = 32;
-    s.nb = tiles >= (p.M > 32 ? 512 : 1536) ? 2 : 1;
-    s.waves = s.nb == 2 ? 1 : 2;
-  }
-  s.use_stream = s.can_stream && !(p.M > 32 && tiles >= 768 && !p.rows);
+  s.can_stream = aligned && 64 * p.lda + p.kb < limit && 64 * p.ldb + p.kb < limit && 64 * p.ldsa + p.nb < limit &&
+                 64 * p.ldsb + p.nb < limit;
+  const int64_t per = (p.N + 63) / 64;
+  const int64_t tiles = per > ((int64_t)1 << 40) / p.batch ? (int64_t)1 << 40 : per * p.batch;  // of 64 columns
+  // Two waves share K, one where it has no two full turns of the ring for them (us, one | two waves):
+  //   256 groups of 16 x 512 x 512   14.3 | 25.6     16 x 8192 x 8192   13.3 | 11.2     16 x 8192 x 28672   34 | 23
+  // 64 columns (up to 16 rows) halve the reads of A where they still give every CU a tile (32 | 64 columns):
+  //   16 x 16384 x 8192   17.4 | 17.0     8 x 28672 x 8192   27.7 | 26.5     16 x 128000 x 4096   60 | 52
+  //   16 x 8192 x 8192    11.2 | 12.7
+  // Rows past 32 stream while one round of workgroups holds all tiles (streaming | the general kernel's 64 x 64 tiles):
+  //   64 x 8192 x 8192    16.3 | 23.1     64 x 8192 x 28672   40.7 | 68.6     64 x 10240 x 8192   25.6 | 23.7
+  // and up to 32 rows always:
+  //   16 x 16384 x 8192   17.0 | 22.8     32 x 16384 x 8192   20.2 | 23.3     32 x 128000 x 4096   63.8 | 74.2
+  //   256 groups of 32 x 512 x 512   18.4 | 19.3     32 x 32000 x 1024   9.2 | 8.7
+  s.rows = p.M <= 16 ? 16 : p.M <= 32 ? 32 : 64;
+  s.waves = p.K <= 1024 && p.M <= 32 ? 1 : 2;
+  s.nb = p.M <= 16 && s.waves == 2 && tiles >= 256 ? 4 : 2;
+  s.use_stream = s.can_stream && (p.M <= 32 || tiles <= 128);
   return s;
 }
 
 hipError_t launch_mx4_stream(const Mx4Args &p, hipStream_t st) {
   const Mx4Few s = mx4_few_plan(p);
-  if (s.rows == 16) return s.waves == 1 ? stream_t<16, 1, 1>(p, st) : stream_t<16, 1, 4>(p, st);
-  return s.nb == 1 ? stream_t<32, 1, 2>(p, st) : stream_t<32, 2, 1>(p, st);
+  if (s.rows == 16) {
+    if (s.waves == 1) return stream_t<16, 2, 1>(p, st);
+    return s.nb == 2 ? stream_t<16, 2, 2>(p, st) : stream_t<16, 4, 2>(p, st);
+  }
+  if (s.rows == 32) return s.waves == 1 ? stream_t<32, 2, 1>(p, st) : stream_t<32, 2, 2>(p, st);
+  return stream_t<64, 2, 2>(p, st);
 }
 
 bool mx4_rows_supports(const Mx4Args &p) {
