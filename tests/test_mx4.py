@@ -222,6 +222,28 @@ def test_large_tiles(monkeypatch, M, N, K, pad, out):
         assert torch.equal(c[z, :m], plain[z, :m]) and (c[z, m:] == 55.0).all()
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,pad", [(300, 520, 128 * n, 0) for n in range(1, 29)]
+                         + [(257, 513, 640, 0), (513, 257, 1152, 1), (256, 1001, 128, 3), (700, 262, 4224, 2),
+                            (255, 255, 256, 1), (511, 300, 384, 4)])
+def test_large_tiles_of_half_slabs_and_odd_columns(monkeypatch, M, N, K, pad, out):
+    """A last slab of half its elements; results whose rows, or their first element, are not at 16 bytes; scales of NaN
+    and codes behind the operands' rows."""
+    import torch
+
+    monkeypatch.setenv("TSM_GEMM_KERNEL", "mx4_tile_256x256x256")
+    g = gen(M + N * 3 + K + pad)
+    say(f"[gpu] mx4 large tiles {M}x{N}x{K}+{pad} {out}")
+    a, sa, va = operand(M, K, 16 * (pad % 2), 4 * (pad % 2), g)
+    b, sb, vb = operand(N, K, 32 * (pad % 2), 8 * (pad % 2), g, 112, 124)
+    buf = torch.full(((M + 1) * (N + pad) + 1,), 77.0, dtype=dtypes()[out], device="cuda")
+    c = buf[pad % 2:].as_strided((M, N), (N + pad, 1))
+    tsm.matmul_mx4(a, sa, b.t(), sb, columns=K, out=c)
+    check_product(c, *ref.product(va, vb), K, out)
+    c.fill_(77.0)
+    assert (buf == 77.0).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(4352, 4096, 256), (4100, 4360, 512), (2200, 2304, 768)])
 def test_tiles_past_whole_rounds(M, N, K):
     """A few 256-tiles more than one per CU (272, 306), or fewer than a round: the two launches together write every

@@ -1,7 +1,7 @@
 // Large-tile products of microscaled 4-bit codes for gfx950: 256 x 256 tiles of C,
-// for K a multiple of 256, N of 8, 16-byte aligned rows of codes and 4-byte aligned
-// rows of scales, on problems whose tiles fill most of the chip.  (gemm_mx4.hip
-// covers everything else.)
+// for K a multiple of 128, 16-byte aligned rows of codes and 4-byte aligned rows of
+// scales, on problems whose tiles fill most of the chip.  (gemm_mx4.hip covers
+// everything else.)
 //
 // The blocking is that of the large-tile int8 kernel (gemm_i8_tile.hip), with
 // v_mfma_scale_f32_32x32x64_f8f6f4: a 256-thread workgroup, one wave per 128 x 128
@@ -20,6 +20,9 @@
 // slab, blocks 4h .. 4h + 3 of the slab's eight.  Those are the blocks that it takes
 // in the four sub-slices, in both operands, and the matrix instruction picks the
 // byte.
+//
+// K's last slab, which may hold half of its elements, comes first, so that its zeros
+// and its scales are the prologue's business and the loop has no branch for them.
 #include "lds_ring.hpp"
 #include "mx4_common.hpp"
 
@@ -38,7 +41,7 @@ __device__ __forceinline__ char *stage_b(int s) { return s == 0 ? s_b0 : s_b1; }
 struct Ctx {
   __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
   uint32_t offA[LOADS], offB[LOADS], offSA[4], offSB[4];
-  int nk, wave, wm, wn, lane;
+  int nk, wave, wm, wn, lane;  // nk: slabs
 };
 struct Frags {
   u32x4 a[4], b[4];
@@ -63,7 +66,7 @@ __device__ __forceinline__ void read_frags(const char *sa, const char *sb, Frags
     f.b[j] = *reinterpret_cast<const u32x4 *>(sb + (c.wn * 128 + j * 32 + row) * BK + chunk);
 }
 
-// The scales of slabs 4 quad .. 4 quad + 3.  (A lane's 16 bytes may lie partly or wholly past a row's end: past the
+// The scales of K's slabs 4 quad .. 4 quad + 3.  (A lane's 16 bytes may lie partly or wholly past a row's end: past the
 // resource they load as zeros, before its end they are another row's; no slab uses them.)
 __device__ __forceinline__ void load_scales(const Ctx &c, int quad, Scales &s) {
 #pragma unroll
@@ -95,11 +98,11 @@ __device__ __forceinline__ void mma(const Frags &f, const Scales &s, Acc &acc) {
       acc.v[i][j] = mfma_mx4_32<U>(f.b[j], s.b[j][W], f.a[i], s.a[i][W], FIRST ? f32x16{} : acc.v[i][j]);
 }
 
-// Sub-slice U of slab j = J (mod 12): A in stage J % 3, B in stage J % 2, scales J % 4.  U = 0 waits for slab j (only
-// A's copies of slab j + 1 may still be in flight), passes the barrier and refills the B stage that slab j - 1 freed;
-// U = 2 refills the A stage that it freed, two slabs ahead.  At the first slab of four, U = 1 takes over the scales
-// (the last slab's were used until then) and requests the next.  MODE 1: the tile's first sub-slice (nothing to
-// multiply yet); MODE 2: the second (starts the sums).
+// Sub-slice U of slab j = J (mod 12), which is K's slab j - 1 (the first: K's last): A in stage J % 3, B in stage J % 2,
+// scales (J + 3) % 4.  U = 0 waits for slab j (only A's copies of slab j + 1 may still be in flight), passes the barrier
+// and refills the B stage that slab j - 1 freed; U = 2 refills the A stage that it freed, two slabs ahead.  At the first
+// slab of four, U = 1 takes over the scales (the last slab's were used until then) and requests the next.  MODE 1: the
+// tile's first sub-slice (nothing to multiply yet); MODE 2: the second (starts the sums).
 template <int J, int U, int MODE = 0>
 __device__ __forceinline__ void substep(Ctx &c, int j, Frags (&fr)[2], Scales &sc, Scales &next, Acc &acc) {
   constexpr int SA = J % 3, SB = J % 2, V = (U + 3) % 4;  // V: the sub-slice that is multiplied
@@ -109,16 +112,16 @@ __device__ __forceinline__ void substep(Ctx &c, int j, Frags (&fr)[2], Scales &s
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   }
-  if constexpr (U == 1 && J % 4 == 0) {
+  if constexpr (U == 1 && J % 4 == 1) {
     arrange(sc, next);
     load_scales(c, (j >> 2) + 1, next);
   }
   read_frags<U>(stage_a(SA), stage_b(SB), fr[U & 1], c);
-  // past the end the last slab again: the count of copies in flight stays the same
-  if constexpr (U == 0) issue<LOADS>(c.rb, c.offB, (uint32_t)min(j + 1, c.nk - 1) * BK, stage_b(SB ^ 1), c.wave);
-  if constexpr (U == 2) issue<LOADS>(c.ra, c.offA, (uint32_t)min(j + 2, c.nk - 1) * BK, stage_a((SA + 2) % 3), c.wave);
-  if constexpr (MODE == 0) mma<V, (U ? J : J + 3) % 4>(fr[V & 1], sc, acc);
-  if constexpr (MODE == 2) mma<V, J % 4, true>(fr[V & 1], sc, acc);
+  // past the end the last one again: the count of copies in flight stays the same
+  if constexpr (U == 0) issue<LOADS>(c.rb, c.offB, (uint32_t)max(min(j, c.nk - 2), 0) * BK, stage_b(SB ^ 1), c.wave);
+  if constexpr (U == 2) issue<LOADS>(c.ra, c.offA, (uint32_t)max(min(j + 1, c.nk - 2), 0) * BK, stage_a((SA + 2) % 3), c.wave);
+  if constexpr (MODE == 0) mma<V, (U ? J + 3 : J + 2) % 4>(fr[V & 1], sc, acc);
+  if constexpr (MODE == 2) mma<V, (J + 3) % 4, true>(fr[V & 1], sc, acc);
 #pragma unroll
   for (int t = 0; t < 8; ++t) {
     __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 0);
@@ -134,6 +137,20 @@ __device__ __forceinline__ void slab(Ctx &c, int j, Frags (&fr)[2], Scales &sc, 
   substep<J, 1>(c, j, fr, sc, next, acc);
   substep<J, 2>(c, j, fr, sc, next, acc);
   substep<J, 3>(c, j, fr, sc, next, acc);
+}
+
+// Eight 16-bit results, of which the first n are stored, anywhere.
+__device__ __forceinline__ void store_any(char *at, u32x4 d, int n) {
+  struct __attribute__((packed, aligned(2))) Any {
+    u32x4 v;
+  };
+  if (n >= 8) {
+    reinterpret_cast<Any *>(at)->v = d;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < n) reinterpret_cast<uint16_t *>(at)[e] = (uint16_t)(d[e / 2] >> (e % 2 * 16));
 }
 
 constexpr int kNonTemporal = 2;  // buffer-store cache policy: C is written once and not read again
@@ -165,16 +182,35 @@ __global__ __launch_bounds__(256, 1) void gemm_mx4_tile_kernel(Mx4Args p) {
     c.offSA[i] = (uint32_t)((wm * 128 + i * 32 + (lane & 31)) * p.ldsa + (lane >> 5) * 16);
     c.offSB[i] = (uint32_t)((wn * 128 + i * 32 + (lane & 31)) * p.ldsb + (lane >> 5) * 16);
   }
-  c.nk = (int)(p.K / (2 * BK));
+  c.nk = (int)((p.K + 2 * BK - 1) / (2 * BK));
 
   Acc acc;  // started by the second sub-slice
   Scales sc, next;
   Frags fr[2];
   // copies in the order the waits count on: scales, A(0), B(0), A(1), then per slab j: B(j+1), A(j+2)
+  const int last = c.nk - 1, tail = (int)(p.kb - (int64_t)last * BK);  // K's last slab, its bytes of a row: 64 or 128
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // this lane's word of it, no scales where it has no elements
+    const bool in = (lane >> 5) * 64 < tail;
+    const uint32_t back = (uint32_t)(lane >> 5) * 12;  // offSA, offSB: of 16 bytes for each half of the lanes
+    sc.a[i][3] = __builtin_amdgcn_raw_buffer_load_b32(c.rsa, in ? c.offSA[i] - back : kOutside, last * 8, 0);
+    sc.b[i][3] = __builtin_amdgcn_raw_buffer_load_b32(c.rsb, in ? c.offSB[i] - back : kOutside, last * 8, 0);
+  }
   load_scales(c, 0, next);
-  issue<LOADS>(c.ra, c.offA, 0, s_a0, c.wave);
-  issue<LOADS>(c.rb, c.offB, 0, s_b0, c.wave);
-  issue<LOADS>(c.ra, c.offA, (uint32_t)min(1, c.nk - 1) * BK, s_a1, c.wave);
+  {
+    uint32_t first[LOADS];
+    auto masked = [&](const uint32_t(&off)[LOADS]) {
+#pragma unroll
+      for (int g = 0; g < LOADS; ++g)
+        first[g] = swz<2>((c.wave * LOADS + g) * 8 + (lane >> 3), lane & 7) * 16 < tail ? off[g] : kOutside;
+    };
+    masked(c.offA);
+    issue<LOADS>(c.ra, first, (uint32_t)last * BK, s_a0, c.wave);
+    masked(c.offB);
+    issue<LOADS>(c.rb, first, (uint32_t)last * BK, s_b0, c.wave);
+  }
+  issue<LOADS>(c.ra, c.offA, 0, s_a1, c.wave);
   substep<0, 0, 1>(c, 0, fr, sc, next, acc);
   substep<0, 1, 2>(c, 0, fr, sc, next, acc);
   substep<0, 2>(c, 0, fr, sc, next, acc);
@@ -229,7 +265,7 @@ __global__ __launch_bounds__(256, 1) void gemm_mx4_tile_kernel(Mx4Args p) {
     }
   }
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  const int w = (c.nk - 1) & 3;  // the last slab's word of the scales
+  const int w = (c.nk + 2) & 3;  // the last slab's word of the scales
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     sc.a[i][0] = w == 0 ? sc.a[i][0] : w == 1 ? sc.a[i][1] : w == 2 ? sc.a[i][2] : sc.a[i][3];
@@ -251,7 +287,8 @@ __global__ __launch_bounds__(256, 1) void gemm_mx4_tile_kernel(Mx4Args p) {
     // this wave's quadrant through LDS, 32 rows of 256 bytes at a time, chunk c of row r at c ^ (r % 16)
     char *const q = c.wave == 0 ? s_a0 : c.wave == 1 ? s_a1 : c.wave == 2 ? s_b0 : s_b1;
     const int col = wn * 128 + 8 * t;
-    const uint32_t coff = col < vc ? (uint32_t)(col * 2) : kOutside;
+    const bool whole = p.vec_store && col + 8 <= vc;
+    const uint32_t coff = whole ? (uint32_t)(col * 2) : kOutside;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       char *const at = q + i * 8192;
@@ -273,6 +310,8 @@ __global__ __launch_bounds__(256, 1) void gemm_mx4_tile_kernel(Mx4Args p) {
         const u32x4 d = *reinterpret_cast<const u32x4 *>(at + row * 256 + (t ^ (row & 15)) * 16);
         __builtin_amdgcn_raw_buffer_store_b128(d, rc, coff + (uint32_t)((wm * 128 + i * 32 + row) * ldc * 2), 0,
                                                kNonTemporal);
+        if (!whole && wm * 128 + i * 32 + row < vr)
+          store_any((char *)p.C + (z * p.strideC + (m0 + wm * 128 + i * 32 + row) * ldc + n0 + col) * 2, d, vc - col);
       }
     }
   } else {
@@ -281,13 +320,19 @@ __global__ __launch_bounds__(256, 1) void gemm_mx4_tile_kernel(Mx4Args p) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int col = wn * 128 + 32 * j2 + 8 * k + 4 * h;
-        const uint32_t off = col < vc ? (uint32_t)(((wm * 128 + r32) * ldc + col) * 4) : kOutside;
+        const uint32_t off = (uint32_t)(((wm * 128 + r32) * ldc + col) * 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           f32x4 v;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = act_codes(ep, acc.v[i][j2][4 * k + e]);
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rc, off + (uint32_t)(32 * i * ldc * 4), 0, 0);
+          const uint32_t at = off + (uint32_t)(32 * i * ldc * 4);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rc, col + 4 <= vc ? at : kOutside, 0, 0);
+          if (col < vc && col + 4 > vc) {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), rc, col + e < vc ? at + 4 * e : kOutside, 0, 0);
+          }
         }
       }
     }
@@ -297,21 +342,23 @@ __global__ __launch_bounds__(256, 1) void gemm_mx4_tile_kernel(Mx4Args p) {
 }  // namespace
 
 bool mx4_tile_supports(const Mx4Args &p) {
-  if (p.N % 8 || p.K % (2 * BK) || p.K == 0) return false;
+  if (p.K % BK || p.K == 0) return false;
   if (255 * p.lda + p.kb >= (int64_t)1 << 30 || 255 * p.ldb + p.kb >= (int64_t)1 << 30) return false;
   if (255 * p.ldsa + p.nb >= (int64_t)1 << 30 || 255 * p.ldsb + p.nb >= (int64_t)1 << 30) return false;
-  if (((uintptr_t)p.A | (uintptr_t)p.B | (uintptr_t)p.C) & 15) return false;
+  if (((uintptr_t)p.A | (uintptr_t)p.B) & 15) return false;
   if (((uintptr_t)p.SA | (uintptr_t)p.SB) & 3) return false;
   if (p.lda % 16 || p.ldb % 16 || p.strideA % 16 || p.strideB % 16) return false;
   if (p.ldsa % 4 || p.ldsb % 4 || p.strideSA % 4 || p.strideSB % 4) return false;
   const int es = fmt_bytes(p.fmt);
-  if (p.ldc * es % 16 || p.strideC * es % 16) return false;
   return 256 * p.ldc * es < (int64_t)1 << 31;  // 32-bit store offsets
 }
 
 hipError_t launch_mx4_tile(const Mx4Args &p, bool whole_only, hipStream_t stream) {
   Mx4Args q = p;
   q.cus = whole_only ? device_cus() : 0;
+  // whether rows start at 4 bytes, which vector stores through a resource want
+  const int64_t es = fmt_bytes(p.fmt);
+  q.vec_store = (uintptr_t)p.C % 4 == 0 && p.ldc * es % 4 == 0 && p.strideC * es % 4 == 0;
   return over_tiles(q, BM, BN, 256, [&](const Mx4Args &a, dim3 grid) {
     // without counts the host knows the tiles of whole rounds
     const int64_t whole = a.rows ? (int64_t)grid.x : whole_rounds(grid.x, a.cus);
@@ -326,7 +373,9 @@ hipError_t launch_mx4_tile(const Mx4Args &p, bool whole_only, hipStream_t stream
       if (hipPeekAtLastError() != hipSuccess) return;
     }
     if (whole_only && (a.rows || whole < (int64_t)grid.x)) {
-      const hipError_t e = launch_mx4_rest(a, stream);
+      Mx4Args b = a;
+      b.vec_store = p.vec_store;  // (of 4 elements there)
+      const hipError_t e = launch_mx4_rest(b, stream);
       (void)e;  // the launch's error is the last one
     }
   });
