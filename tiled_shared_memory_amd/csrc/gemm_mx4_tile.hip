@@ -139,18 +139,20 @@ __device__ __forceinline__ void slab(Ctx &c, int j, Frags (&fr)[2], Scales &sc, 
   substep<J, 3>(c, j, fr, sc, next, acc);
 }
 
-// Eight 16-bit results, of which the first n are stored, anywhere.
+// Sixteen bytes of results, of which the first n are stored, anywhere.
+template <int FMT>
 __device__ __forceinline__ void store_any(char *at, u32x4 d, int n) {
+  constexpr int PER = 16 / fmt_bytes(FMT);
   struct __attribute__((packed, aligned(2))) Any {
     u32x4 v;
   };
-  if (n >= 8) {
+  if (n >= PER) {
     reinterpret_cast<Any *>(at)->v = d;
     return;
   }
 #pragma unroll
-  for (int e = 0; e < 7; ++e)
-    if (e < n) reinterpret_cast<uint16_t *>(at)[e] = (uint16_t)(d[e / 2] >> (e % 2 * 16));
+  for (int e = 0; e < PER - 1; ++e)
+    if (e < n) put_bits<FMT>(at, e, FMT == FMT_F32 ? d[e] : d[e / 2] >> (e % 2 * 16) & 0xffff);
 }
 
 constexpr int kNonTemporal = 2;  // buffer-store cache policy: C is written once and not read again
@@ -276,65 +278,45 @@ __global__ __launch_bounds__(256, 1) void gemm_mx4_tile_kernel(Mx4Args p) {
 
   // ---- epilogue: acc.v[i][j], elements 4 q .. 4 q + 3, holds C[32 i + lane % 32][32 j + 8 q + 4 (lane / 32) + 0..3] of
   // the quadrant
-  const int r32 = lane & 31, h = lane >> 5, t = lane & 15, g = lane >> 4;
-  constexpr int ES = fmt_bytes(FMT);
+  const int r32 = lane & 31, h = lane >> 5;
+  constexpr int ES = fmt_bytes(FMT), PER = 16 / ES, CHUNKS = 128 / PER;  // results per chunk of 16 bytes, chunks per row
   const int64_t ldc = p.ldc;
   const __amdgpu_buffer_rsrc_t rc = make_rsrc((char *)p.C + (z * p.strideC + m0 * ldc + n0) * ES,
                                               (uint32_t)(((vr - 1) * ldc + vc) * ES));
   const Epilogue ep{p.act, p.slope, false};
-  if constexpr (FMT != FMT_F32) {
-    __syncthreads();  // every wave is past its last fragment read and copy
-    // this wave's quadrant through LDS, 32 rows of 256 bytes at a time, chunk c of row r at c ^ (r % 16)
-    char *const q = c.wave == 0 ? s_a0 : c.wave == 1 ? s_a1 : c.wave == 2 ? s_b0 : s_b1;
-    const int col = wn * 128 + 8 * t;
-    const bool whole = p.vec_store && col + 8 <= vc;
-    const uint32_t coff = whole ? (uint32_t)(col * 2) : kOutside;
+  __syncthreads();  // every wave is past its last fragment read and copy
+  // this wave's quadrant through LDS, 32 rows at a time, chunk c of row r at c ^ (r % CHUNKS); then whole rows are stored
+  char *const q = c.wave == 0 ? s_a0 : c.wave == 1 ? s_a1 : c.wave == 2 ? s_b0 : s_b1;
+  const int t = lane % CHUNKS, g = lane / CHUNKS, col = wn * 128 + PER * t;
+  const bool whole = p.vec_store && col + PER <= vc;
+  const uint32_t coff = whole ? (uint32_t)(col * ES) : kOutside;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      char *const at = q + i * 8192;
-#pragma unroll
-      for (int j2 = 0; j2 < 4; ++j2) {
-        f32x16 v = acc.v[i][j2];
-        if (p.act) {  // uniform
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = act_codes(ep, v[e]);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<u32x2 *>(at + r32 * 256 + ((64 * j2 + 16 * k + 8 * h) ^ (16 * t))) =
-              u32x2{pack2<FMT>(v[4 * k], v[4 * k + 1]), pack2<FMT>(v[4 * k + 2], v[4 * k + 3])};
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int row = 4 * k + g;
-        const u32x4 d = *reinterpret_cast<const u32x4 *>(at + row * 256 + (t ^ (row & 15)) * 16);
-        __builtin_amdgcn_raw_buffer_store_b128(d, rc, coff + (uint32_t)((wm * 128 + i * 32 + row) * ldc * 2), 0,
-                                               kNonTemporal);
-        if (!whole && wm * 128 + i * 32 + row < vr)
-          store_any((char *)p.C + (z * p.strideC + (m0 + wm * 128 + i * 32 + row) * ldc + n0 + col) * 2, d, vc - col);
-      }
-    }
-  } else {
+  for (int i = 0; i < 4; ++i) {
+    char *const at = q + (i * 32 * 128 * ES) % STAGE_BYTES;
 #pragma unroll
     for (int j2 = 0; j2 < 4; ++j2) {
+      f32x16 v = acc.v[i][j2];
+      if (p.act) {  // uniform
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = act_codes(ep, v[e]);
+      }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int col = wn * 128 + 32 * j2 + 8 * k + 4 * h;
-        const uint32_t off = (uint32_t)(((wm * 128 + r32) * ldc + col) * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f32x4 v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = act_codes(ep, acc.v[i][j2][4 * k + e]);
-          const uint32_t at = off + (uint32_t)(32 * i * ldc * 4);
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rc, col + 4 <= vc ? at : kOutside, 0, 0);
-          if (col < vc && col + 4 > vc) {
-#pragma unroll
-            for (int e = 0; e < 3; ++e)
-              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[e]), rc, col + e < vc ? at + 4 * e : kOutside, 0, 0);
-          }
-        }
+        char *const to = at + r32 * 128 * ES;
+        if constexpr (FMT == FMT_F32)
+          *reinterpret_cast<f32x4 *>(to + ((8 * j2 + 2 * k + h) ^ r32) * 16) =
+              f32x4{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
+        else
+          *reinterpret_cast<u32x2 *>(to + ((64 * j2 + 16 * k + 8 * h) ^ (16 * (r32 & 15)))) =
+              u32x2{pack2<FMT>(v[4 * k], v[4 * k + 1]), pack2<FMT>(v[4 * k + 2], v[4 * k + 3])};
       }
+    }
+#pragma unroll
+    for (int k = 0; k < CHUNKS / 2; ++k) {
+      const int row = 64 / CHUNKS * k + g, m = wm * 128 + i * 32 + row;
+      const u32x4 d = *reinterpret_cast<const u32x4 *>(at + row * 128 * ES + (t ^ (row % CHUNKS)) * 16);
+      __builtin_amdgcn_raw_buffer_store_b128(d, rc, coff + (uint32_t)(m * ldc * ES), 0, kNonTemporal);
+      if (!whole && m < vr) store_any<FMT>((char *)p.C + (z * p.strideC + (m0 + m) * ldc + n0 + col) * ES, d, vc - col);
     }
   }
 }
