@@ -71,14 +71,6 @@ __device__ __forceinline__ Place stream_tile(const Mx4Args &p, int t, const int 
   return e;
 }
 
-// The kernel's arguments, read again for each tile: held in scalar registers through the loop they would spill.
-__device__ __forceinline__ Mx4Args args_again() {
-  typedef const __attribute__((address_space(4))) Mx4Args *At;
-  At p = (At)__builtin_amdgcn_kernarg_segment_ptr();
-  asm volatile("" : "+s"(p));
-  return *(const Mx4Args *)p;
-}
-
 __device__ __forceinline__ uint32_t lds_at(const char *at) { return (uint32_t)(uintptr_t)(lds_void *)at; }
 
 // Writes to LDS that the compiler does not see: it would wait for every copy in flight before them.

@@ -357,7 +357,7 @@ hipError_t launch_mx4_tile(const Mx4Args &p, bool whole_only, hipStream_t stream
     if (whole_only && (a.rows || whole < (int64_t)grid.x)) {
       Mx4Args b = a;
       b.vec_store = p.vec_store;  // (of 4 elements there)
-      const hipError_t e = launch_mx4_rest(b, stream);
+      const hipError_t e = launch_mx4_rest(b, a.rows ? kFewTiles - 1 : (int64_t)grid.x - whole, stream);
       (void)e;  // the launch's error is the last one
     }
   });

@@ -67,6 +67,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
+// The kernel's arguments, read again for each tile: held in scalar registers through the loop they would spill.
+__device__ __forceinline__ Mx4Args args_again() {
+  typedef const __attribute__((address_space(4))) Mx4Args *At;
+  At p = (At)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const Mx4Args *)p;
+}
+
 // Four results of one row of C, columns n .. n+3 (n < N): activation, rounding, store.
 template <int FMT>
 __device__ __forceinline__ void store_mx4(const Mx4Args &p, const Epilogue &ep, char *row, int64_t n, f32x4 acc) {

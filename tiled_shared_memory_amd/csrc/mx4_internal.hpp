@@ -39,8 +39,9 @@ struct Mx4Args {
 bool mx4_tile_supports(const Mx4Args &p);
 // whole_only: tiles left over from whole rounds of the CUs go to launch_mx4_rest.
 hipError_t launch_mx4_tile(const Mx4Args &p, bool whole_only, hipStream_t stream);
-// The 256 x 256 tiles that whole_rounds leaves of a launch (tiles_m, tiles_n, z0 and nz set), as 128 x 128 ones.
-hipError_t launch_mx4_rest(const Mx4Args &a, hipStream_t stream);
+// The 256 x 256 tiles that whole_rounds leaves of a launch (tiles_m, tiles_n, z0 and nz set), at most `tiles`, in
+// smaller ones.
+hipError_t launch_mx4_rest(const Mx4Args &a, int64_t tiles, hipStream_t stream);
 // CUs of the current device (gemm_api.hip).
 int device_cus();
 
