@@ -107,10 +107,10 @@ __device__ __forceinline__ void find_group(const Args &p, int lane, int &t, int 
 // 2048, 64 tiles: 27.7 against 17.3).
 // (cus = 0: every tile stays.)
 constexpr int kFewTiles = 72;
-__host__ __device__ inline int64_t whole_rounds(int64_t tiles, int64_t cus) {
+__host__ __device__ inline int64_t whole_rounds(int64_t tiles, int64_t cus, int64_t few = kFewTiles) {
   if (!cus) return tiles;
   const int64_t left = tiles % cus;
-  return left < kFewTiles ? tiles - left : tiles;
+  return left < few ? tiles - left : tiles;
 }
 
 // Tile rows per group of the 256-tiles' order: 4 from 32 tile rows up, else 8 (as the 16-bit kernel).
@@ -141,10 +141,10 @@ __device__ __forceinline__ int tiles_of(const Args &p) {
 // grouped tile order, the grid regrouped per XCD.  Grouped calls number only
 // the tiles that hold rows, so the real work spreads evenly over the XCDs;
 // false: nothing to do.  WHOLE: only the tiles of whole_rounds.
-template <int BM, bool WHOLE = false, class Args>
+template <int BM, bool WHOLE = false, int FEW = kFewTiles, class Args>
 __device__ __forceinline__ bool tile_of(const Args &p, int group_m, int64_t &z, int &tm, int &tn) {
   int V = tiles_of<BM>(p);
-  if (WHOLE) V = (int)whole_rounds(V, p.cus);
+  if (WHOLE) V = (int)whole_rounds(V, p.cus, FEW);
   if ((int)blockIdx.x >= V) return false;
   tile_at<BM>(p, xcd_remap(blockIdx.x, V), group_m, z, tm, tn);
   return true;

@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kThreads) void gemm_mx4_block_kernel(Mx4Args p) {
   int64_t z;
   if constexpr (REST) {
     constexpr int S = 256 / T;
-    const int all = tiles_of<256>(p), pid = (int)whole_rounds(all, p.cus) + (int)(blockIdx.x / (S * S));
+    const int all = tiles_of<256>(p), pid = (int)whole_rounds(all, p.cus, kFewMx4Tiles) + (int)(blockIdx.x / (S * S));
     if (pid >= all) return;  // uniform
     tile_at<256>(p, pid, tile_group(p), z, tm, tn);
     tm = S * tm + (int)blockIdx.x / S % S;
@@ -205,24 +205,17 @@ hipError_t block_t(const Mx4Args &p, hipStream_t stream) {
   });
 }
 
-template <int T>
-hipError_t rest_t(const Mx4Args &a, int64_t tiles, hipStream_t stream) {
-  const dim3 grid((unsigned)(tiles * (256 / T) * (256 / T))), block(kThreads);
-  if (a.fmt == FMT_F32)
-    hipLaunchKernelGGL((gemm_mx4_block_kernel<T, FMT_F32, 2, true>), grid, block, 0, stream, a);
-  else if (a.fmt == FMT_F16)
-    hipLaunchKernelGGL((gemm_mx4_block_kernel<T, FMT_F16, 2, true>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((gemm_mx4_block_kernel<T, FMT_BF16, 2, true>), grid, block, 0, stream, a);
-  return hipPeekAtLastError();
-}
-
 }  // namespace
 
-// Up to 32 tiles as 64-tiles, two per CU (whole products, in us, 64-tiles | 128-tiles: 4112 x 4096 x 4096, 16 tiles left,
-// 48 | 55; 4608 rows, 32 left, 56 | 58; 5120 rows, 64 left, 71 | 64; counts in device memory are not known here).
 hipError_t launch_mx4_rest(const Mx4Args &a, int64_t tiles, hipStream_t stream) {
-  return tiles <= 32 ? rest_t<64>(a, tiles, stream) : rest_t<128>(a, tiles, stream);
+  const dim3 grid((unsigned)(tiles * 16)), block(kThreads);
+  if (a.fmt == FMT_F32)
+    hipLaunchKernelGGL((gemm_mx4_block_kernel<64, FMT_F32, 2, true>), grid, block, 0, stream, a);
+  else if (a.fmt == FMT_F16)
+    hipLaunchKernelGGL((gemm_mx4_block_kernel<64, FMT_F16, 2, true>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((gemm_mx4_block_kernel<64, FMT_BF16, 2, true>), grid, block, 0, stream, a);
+  return hipPeekAtLastError();
 }
 
 hipError_t launch_mx4_block(const Mx4Args &p, int tile, hipStream_t stream) {

@@ -161,7 +161,7 @@ template <int FMT>
 __global__ __launch_bounds__(256, 1) void gemm_mx4_tile_kernel(Mx4Args p) {
   int tm, tn;
   int64_t z;
-  if (!tile_of<BM, true>(p, tile_group(p), z, tm, tn)) return;  // uniform
+  if (!tile_of<BM, true, kFewMx4Tiles>(p, tile_group(p), z, tm, tn)) return;  // uniform
   Ctx c;
   c.lane = threadIdx.x & 63;
   c.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -343,7 +343,7 @@ hipError_t launch_mx4_tile(const Mx4Args &p, bool whole_only, hipStream_t stream
   q.vec_store = (uintptr_t)p.C % 4 == 0 && p.ldc * es % 4 == 0 && p.strideC * es % 4 == 0;
   return over_tiles(q, BM, BN, 256, [&](const Mx4Args &a, dim3 grid) {
     // without counts the host knows the tiles of whole rounds
-    const int64_t whole = a.rows ? (int64_t)grid.x : whole_rounds(grid.x, a.cus);
+    const int64_t whole = a.rows ? (int64_t)grid.x : whole_rounds(grid.x, a.cus, kFewMx4Tiles);
     if (whole) {
       const dim3 g((unsigned)whole);
       if (a.fmt == FMT_F32)
@@ -357,7 +357,7 @@ hipError_t launch_mx4_tile(const Mx4Args &p, bool whole_only, hipStream_t stream
     if (whole_only && (a.rows || whole < (int64_t)grid.x)) {
       Mx4Args b = a;
       b.vec_store = p.vec_store;  // (of 4 elements there)
-      const hipError_t e = launch_mx4_rest(b, a.rows ? kFewTiles - 1 : (int64_t)grid.x - whole, stream);
+      const hipError_t e = launch_mx4_rest(b, a.rows ? kFewMx4Tiles - 1 : (int64_t)grid.x - whole, stream);
       (void)e;  // the launch's error is the last one
     }
   });

@@ -142,14 +142,17 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
   p.slope = act == TSM_ACT_LEAKY_RELU ? slope : 0.f;
   p.vec_store = (uintptr_t)C % (uintptr_t)(4 * es) == 0 && ldc % 4 == 0 && strideC % 4 == 0;
 
-  // 64-tiles up to 128 of 128 x 128 and up to 64 rows.
+  // 64-tiles while there are at most 128 of 128 x 128, those while one round of the CUs does them, then 256-tiles (us, 64 |
+  // 128 | 256):
+  //   1024 x 1024 x 4096   10.4 | 18.6 | 25.1     1024 x 2048 x 4096   16.0 | 18.9 | 25.2     2000 x 2000 x 2001   27 | 18
+  //   2048 x 2048 x 4096   27.7 | 20.7 | 25.3     2304 x 2048 x 4096   32.8 | 35.6 | 25.4     256 x 16384 x 4096   35 | 25 | 30
+  // and for up to 64 rows: 64 x 16384 x 8192   25.0 | 35.3.
   const int64_t tiles128 = ((M + 127) / 128) * ((N + 127) / 128), tiles64 = ((M + 63) / 64) * ((N + 63) / 64);
-  const bool small = tiles128 * batch <= 128 || (M <= 64 && tiles64 * 512 <= 0xffffffffLL);
+  const int64_t all128 = tiles128 > ((int64_t)1 << 40) / batch ? (int64_t)1 << 40 : tiles128 * batch;
+  const bool small = all128 <= 128 || (M <= 64 && tiles64 * 512 <= 0xffffffffLL);
   call->kernel = small ? Mx4Kernel::Block64 : Mx4Kernel::Block128;
   if ((small ? tiles64 : tiles128) * 512 > 0xffffffffLL) return fail(TSM_ERROR_NOT_SUPPORTED, "tile grid too large");
-  const bool half = M <= 128 && tiles128 * batch <= 256;  // 256-tiles half empty, and a round of 128-tiles does it
-  const int64_t tiles256 = ((M + 255) / 256) * ((N + 255) / 256) * batch;
-  if (M > 64 && !half && tiles256 >= kFewTiles && mx4_tile_supports(p)) call->kernel = Mx4Kernel::Tile;
+  if (M > 64 && all128 > 256 && mx4_tile_supports(p)) call->kernel = Mx4Kernel::Tile;
   const Mx4Few few = mx4_few_plan(p);
   if (few.use_stream) call->kernel = Mx4Kernel::Stream;
   // TSM_GEMM_KERNEL=<name> forces a variant (tests and tuning); names of other

@@ -28,6 +28,11 @@ __device__ __forceinline__ f32x16 mfma_mx4_32(u32x4 a, uint32_t sa, u32x4 b, uin
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(va, vb, c, 4, 4, O, (int)sa, O, (int)sb);
 }
 
+// Fewer than this many 256-tiles left over from whole rounds of the CUs run as 64-tiles in a second launch (whole
+// products, in us, two launches | another round: 4112 x 4096 x 4096, 16 tiles left, 51 | 59; 4608 rows, 32 left, 56.5 |
+// 59.5; 5120 rows, 64 left, 71 | 59.9).
+constexpr int kFewMx4Tiles = 33;
+
 // f(0) .. f(N - 1) with constants.
 template <int I>
 struct Const {
