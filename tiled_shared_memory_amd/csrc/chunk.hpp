@@ -14,6 +14,15 @@ struct Chunk {
 #pragma unroll
     for (int i = 0; i < V; ++i) raw[i] = *(const Raw16 *)(x + (c * V + i) * 16);
   }
+  // the same of what is read once (non-temporal)
+  __device__ __forceinline__ void load_once(const char *x, int64_t c) {
+    typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const u32x4_any v = __builtin_nontemporal_load((const u32x4_any *)(x + (c * V + i) * 16));
+      raw[i] = Raw16{{v[0], v[1], v[2], v[3]}};
+    }
+  }
   // the first n elements at x, zeros behind them
   __device__ __forceinline__ void load_part(const char *x, int64_t c, int n) {
     uint32_t w[8];
