@@ -397,6 +397,79 @@ def test_activations_of_few_rows(M, K, pad, fmt):
             check_product(c[0, :m].masked_fill(nan, 0), want.masked_fill(nan, 0), mag.masked_fill(nan, 0), K, fmt)
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,pad", [(1, 16, 128, 0), (7, 33, 1024, 1), (15, 4099, 1152, 0), (16, 20011, 2048, 0),
+                                       (16, 16400, 4224, 1), (17, 32, 1024, 0), (31, 10001, 1152, 1),
+                                       (32, 4100, 8320, 0), (33, 31, 128, 1), (48, 9000, 1280, 0), (63, 1, 4096, 0),
+                                       (64, 8193, 640, 1)])
+def test_few_rows(monkeypatch, M, N, K, pad, out):
+    """The streaming kernel, forced: every width of its tiles, more tiles than workgroups, rows that end inside a tile,
+    K that ends inside a step or a turn of the ring; codes and scales of NaN behind the operands' rows."""
+    import torch
+
+    monkeypatch.setenv("TSM_GEMM_KERNEL", "mx4_stream")
+    g = gen(M * 5 + N + K)
+    say(f"[gpu] mx4 few rows {M}x{N}x{K}+{pad} {out}")
+    a, sa, va = operand(M, K, 16 * pad, 4 * pad, g)
+    b, sb, vb = operand(N, K, 48 * pad, 8 * pad, g, 112, 124)
+    buf = torch.full((M + 1, N + 3 * pad), 77.0, dtype=dtypes()[out], device="cuda")
+    tsm.matmul_mx4(a, sa, b.t(), sb, out=buf[:M, :N], activation="relu")
+    check_product(buf[:M, :N], *ref.product(va, vb, "relu"), K, out)
+    assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
+
+
+@pytest.mark.parametrize("G,M,N,K", [(1, 4, 70, 256), (65, 5, 40, 384), (600, 3, 48, 256), (1100, 1, 16, 128),
+                                     (70, 20, 64, 1152), (9, 64, 100, 2048)])
+def test_few_rows_in_many_groups(G, M, N, K):
+    """Groups in several launches of the streaming kernel, many of them without rows, counts below 0 and above M, rows
+    past the counts left as they are; and the same problems as a batch."""
+    import torch
+
+    g = gen(G + M)
+    say(f"[gpu] mx4 few rows in {G} groups {M}x{N}x{K}")
+    a, sa, va = (t.reshape(G, M, -1) for t in operand(G * M, K, 0, 0, g))
+    b, sb, vb = (t.reshape(G, N, -1) for t in operand(G * N, K, 0, 0, g, 112, 124))
+    plain = tsm.matmul_mx4(a, sa, b.transpose(1, 2), sb)
+    assert tsm.tsm_gemm_mx4_kernel_name(M, N, K, a, K // 2, M * K // 2, sa, K // 32, M * K // 32, b, K // 2,
+                                        N * K // 2, sb, K // 32, N * K // 32, plain, N, M * N, G, None,
+                                        0) == "mx4_stream"
+    check_product(plain, *ref.product(va, vb), K, "f32")
+    for share in (0.0, 0.3, 1.0):
+        n = torch.randint(-1, M + 2, (G,), generator=g, device="cuda", dtype=torch.int32)
+        rows = torch.where(torch.rand(G, generator=g, device="cuda") < share, n, 0).to(torch.int32)
+        c = torch.full((G, M, N), 55.0, device="cuda")
+        tsm.matmul_mx4(a, sa, b.transpose(1, 2), sb, rows=rows, out=c)
+        own = torch.arange(M, device="cuda")[None, :] < rows[:, None]
+        assert torch.equal(c[own], plain[own]) and (c[~own] == 55.0).all()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams at once, of one weight, each with its own workspace, and quantisations beside them."""
+    import torch
+
+    g = gen(21)
+    N, K = 4096, 4096
+    w, ws = tsm.quantize_mx4(torch.randn((N, K), generator=g, device="cuda"))
+    xs = [torch.randn((m, K), generator=g, device="cuda") for m in (2, 300, 700, 1)]
+    say("[gpu] mx4 two calls at once")
+    want = [tsm.matmul_mx4(x, None, w.t(), ws) for x in xs]
+    codes = [tsm.quantize_mx4(x) for x in xs]
+    rooms = [tsm.mx4_workspace_for(x) for x in xs]
+    outs = [torch.empty_like(t) for t in want]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(6):
+        for i, x in enumerate(xs):
+            tsm.matmul_mx4(x, None, w.t(), ws, out=outs[i], workspace=rooms[i], stream=streams[i % 2])
+            got.append((i, tsm.quantize_mx4(x, stream=streams[(i + 1) % 2])))
+    torch.cuda.synchronize()
+    for o, t in zip(outs, want):
+        assert torch.equal(o, t)
+    for i, (q, s) in got:
+        assert torch.equal(q, codes[i][0]) and torch.equal(s, codes[i][1])
+
+
 def test_empty_sums_and_sizes():
     import torch
 
