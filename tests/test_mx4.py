@@ -433,7 +433,8 @@ def test_few_rows_in_many_groups(G, M, N, K):
     assert tsm.tsm_gemm_mx4_kernel_name(M, N, K, a, K // 2, M * K // 2, sa, K // 32, M * K // 32, b, K // 2,
                                         N * K // 2, sb, K // 32, N * K // 32, plain, N, M * N, G, None,
                                         0) == "mx4_stream"
-    check_product(plain, *ref.product(va, vb), K, "f32")
+    for z in range(G):
+        check_product(plain[z], *ref.product(va[z], vb[z]), K, "f32")
     for share in (0.0, 0.3, 1.0):
         n = torch.randint(-1, M + 2, (G,), generator=g, device="cuda", dtype=torch.int32)
         rows = torch.where(torch.rand(G, generator=g, device="cuda") < share, n, 0).to(torch.int32)
