@@ -646,12 +646,13 @@ def route_tokens(logits, topk, *, score="softmax", bias=None, groups=1, top_grou
 
     Not recorded for autograd: the gradient of ``logits`` is ``route_tokens_backward``.
     """
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         _bad("logits must be 2-D")
-    f = _wants("logits", logits, _FLOATS)
+    x, ldx, _, f = _float_rows("logits", logits, shape, 1)
     if score not in _SCORES:
         _bad(f"unknown score {score!r}")
-    tokens, experts = logits.shape
+    tokens, experts = shape
     if bias is not None:
         _wants("bias", bias, (TSM_F32,), (experts,))
         _packed("bias", bias)
@@ -664,7 +665,7 @@ def route_tokens(logits, topk, *, score="softmax", bias=None, groups=1, top_grou
     _packed("ids", ids)
     _packed("weights", weights)
     _launch("moe_route", stream, (logits, bias, ids, weights),
-            (tokens, experts, topk, logits.data_ptr(), _rows_ld("logits", logits), f, _SCORES[score], _at(bias),
+            (tokens, experts, topk, x, ldx, f, _SCORES[score], _at(bias),
              groups, groups if top_groups is None else top_groups, group_best, bool(renormalize), factor,
              ids.data_ptr(), weights.data_ptr()))
     return ids, weights
@@ -674,22 +675,24 @@ def route_tokens_backward(dweights, logits, ids, *, score="softmax", renormalize
                           stream=None):
     """The gradient of ``route_tokens``' ``logits``, in their format, from ``dweights`` (float32, tokens x topk): what
     ``combine_tokens_backward`` gives.  ``ids`` are the chosen experts; they, and the bias, take no gradient."""
-    if logits.dim() != 2:
+    shape, chosen = logits.shape, ids.shape
+    if len(shape) != 2:
         _bad("logits must be 2-D")
-    f = _wants("logits", logits, _FLOATS)
+    x, ldx, _, f = _float_rows("logits", logits, shape, 1)
     if score not in _SCORES:
         _bad(f"unknown score {score!r}")
-    if ids.dim() != 2 or ids.shape[0] != logits.shape[0]:
-        _bad(f"ids must be 2-D with {logits.shape[0]} rows")
+    if len(chosen) != 2 or chosen[0] != shape[0]:
+        _bad(f"ids must be 2-D with {shape[0]} rows")
     _wants("ids", ids, (TSM_I32,))
-    _wants("dweights", dweights, (TSM_F32,), ids.shape)
+    _wants("dweights", dweights, (TSM_F32,), chosen)
     _packed("ids", ids)
     _packed("dweights", dweights)
     if out is None:
-        out = _new(logits, logits.shape, logits.dtype, stream)
-    _wants("out", out, (f,), logits.shape)
+        out = _new(logits, shape, logits.dtype, stream)
+    dx, lddx, _, g = _float_rows("out", out, shape, 1)
+    if g != f:
+        _bad(f"out has dtype {out.dtype}")
     _launch("moe_route_backward", stream, (logits, out, ids, dweights),
-            (logits.shape[0], logits.shape[1], ids.shape[1], dweights.data_ptr(), logits.data_ptr(),
-             _rows_ld("logits", logits), f, ids.data_ptr(), _SCORES[score], bool(renormalize), factor, out.data_ptr(),
-             _rows_ld("out", out)))
+            (*shape, chosen[1], dweights.data_ptr(), x, ldx, f, ids.data_ptr(), _SCORES[score], bool(renormalize),
+             factor, dx, lddx))
     return out
