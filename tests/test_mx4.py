@@ -244,6 +244,40 @@ def test_large_tiles_of_half_slabs_and_odd_columns(monkeypatch, M, N, K, pad, ou
     assert (buf == 77.0).all()
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,pad", [(130, 200, 128 * n, 0) for n in range(1, 20)]
+                         + [(1, 1, 128, 0), (64, 64, 256, 0), (65, 127, 1152, 1), (129, 257, 4224, 1), (1000, 70, 640, 1)])
+@pytest.mark.parametrize("T", [64, 128])
+def test_middle_tiles(monkeypatch, T, M, N, K, pad, out):
+    """The kernels with a ring of copies, forced: every count of slabs in and after a turn of the ring, a last one of
+    half its elements, ragged M and N, results at odd addresses, a batch and grouped counts; scales of NaN and codes
+    behind the operands' rows."""
+    import torch
+
+    monkeypatch.setenv("TSM_GEMM_KERNEL", f"mx4_ring_{T}x{T}x256")
+    g = gen(M + N * 3 + K + T)
+    dt = dtypes()[out]
+    say(f"[gpu] mx4 middle tiles {T} {M}x{N}x{K}+{pad} {out}")
+    a, sa, va = operand(M, K, 16 * pad, 4 * pad, g)
+    b, sb, vb = operand(N, K, 48 * pad, 8 * pad, g, 112, 124)
+    buf = torch.full(((M + 1) * (N + 3 * pad) + 1,), 77.0, dtype=dt, device="cuda")
+    c = buf[pad:].as_strided((M, N), (N + 3 * pad, 1))
+    tsm.matmul_mx4(a, sa, b.t(), sb, out=c, activation="leaky_relu", slope=0.25)
+    check_product(c, *ref.product(va, vb, "leaky_relu", 0.25), K, out, 2.0 ** -24)
+    c.fill_(77.0)
+    assert (buf == 77.0).all()
+    a3, sa3, _ = (t.reshape(5, M, -1) for t in operand(5 * M, K, 0, 0, g))
+    b3, sb3, _ = (t.reshape(5, N, -1) for t in operand(5 * N, K, 0, 0, g, 112, 124))
+    plain = tsm.matmul_mx4(a3, sa3, b3.transpose(1, 2), sb3, out_dtype=dt)
+    for z in range(5):
+        check_product(plain[z], *ref.product(ref.values(a3[z], sa3[z], K), ref.values(b3[z], sb3[z], K)), K, out)
+    rows = torch.tensor([M, 0, M // 2, M + 5, -1], dtype=torch.int32, device="cuda")
+    c = torch.full((5, M, N), 55.0, dtype=dt, device="cuda")
+    tsm.matmul_mx4(a3, sa3, b3.transpose(1, 2), sb3, rows=rows, out=c)
+    for z, m in enumerate([M, 0, M // 2, M, 0]):
+        assert torch.equal(c[z, :m], plain[z, :m]) and (c[z, m:] == 55.0).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(4352, 4096, 256), (4100, 4360, 512), (2200, 2304, 768)])
 def test_tiles_past_whole_rounds(M, N, K):
     """A few 256-tiles more than one per CU (272, 306), or fewer than a round: the two launches together write every

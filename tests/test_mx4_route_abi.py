@@ -62,7 +62,9 @@ def test_an_unknown_variant_is_refused(monkeypatch):
     refused(gemm, {}, 1, "mx4_nothing")
 
 
-BLOCK64, BLOCK128, TILE, STREAM = ("mx4_block_64x64x256", "mx4_block_128x128x256", "mx4_tile_256x256x256", "mx4_stream")
+BLOCK64, BLOCK128, RING64, RING128, TILE, STREAM = (
+    "mx4_block_64x64x256", "mx4_block_128x128x256", "mx4_ring_64x64x256", "mx4_ring_128x128x256",
+    "mx4_tile_256x256x256", "mx4_stream")
 
 
 def name_of(M, N, K, batch=1, lda=None, ldb=None, a=1 << 20, fmt=tsm.TSM_BF16, ldc=None, lds=None, rows=None):
@@ -74,29 +76,29 @@ def name_of(M, N, K, batch=1, lda=None, ldb=None, a=1 << 20, fmt=tsm.TSM_BF16, l
 
 @pytest.mark.parametrize("M,N,K,kw,want", [
     (1, 8192, 8192, {}, STREAM), (32, 128000, 4096, {}, STREAM), (33, 8192, 8192, {}, STREAM),
-    (64, 8192, 8192, {}, STREAM), (64, 8256, 8192, {}, BLOCK64), (64, 512, 8192, dict(batch=16), STREAM),
-    (64, 512, 8192, dict(batch=17), BLOCK64), (16, 64, 128, dict(batch=600, rows=1 << 24), STREAM),
+    (64, 8192, 8192, {}, STREAM), (64, 8256, 8192, {}, RING64), (64, 512, 8192, dict(batch=16), STREAM),
+    (64, 512, 8192, dict(batch=17), RING64), (16, 64, 128, dict(batch=600, rows=1 << 24), STREAM),
     (16, 8192, 8160, {}, BLOCK64), (16, 8192, 8192, dict(a=(1 << 20) + 8), BLOCK64),
     (16, 8192, 8192, dict(lda=4104), BLOCK64), (16, 8192, 8192, dict(lds=258), BLOCK64),
-    (65, 8192, 8192, {}, BLOCK64), (1024, 2048, 4096, {}, BLOCK64), (1025, 2048, 4096, {}, BLOCK128),
-    (2048, 2048, 4096, {}, BLOCK128), (2049, 2048, 4096, {}, TILE), (256, 16384, 4096, {}, BLOCK128),
+    (65, 8192, 8192, {}, RING64), (1024, 2048, 4096, {}, RING64), (1025, 2048, 4096, {}, RING128),
+    (1024, 2048, 4064, {}, BLOCK64), (1025, 2048, 4096, dict(lds=130), BLOCK128), (65, 8192, 8192, dict(a=1048577), BLOCK64),
+    (2048, 2048, 4096, {}, RING128), (2049, 2048, 4096, {}, TILE), (256, 16384, 4096, {}, RING128),
     (257, 16384, 4096, {}, TILE), (2304, 2048, 4224, {}, TILE), (2304, 2048, 4097, {}, BLOCK128),
     (2304, 2047, 4096, dict(ldc=2051), TILE), (2304, 2048, 4096, dict(lda=2056), BLOCK128),
-    (256, 256, 4096, dict(batch=65), TILE), (256, 256, 4096, dict(batch=64), BLOCK128),
+    (256, 256, 4096, dict(batch=65), TILE), (256, 256, 4096, dict(batch=64), RING128),
     (1 << 21, 1 << 12, 256, {}, TILE), (2304, 2048, 4096, dict(lda=1 << 22), TILE),  # 255 * 2^22 + 2048 bytes are below 2^30
     (2304, 2048, 4096, dict(lda=1 << 23), BLOCK128),
-    (2304, 2048, 4096, dict(ldc=1 << 23), BLOCK128), (5, 2**31 - 1, 256, {}, BLOCK64)])
+    (2304, 2048, 4096, dict(ldc=1 << 23), BLOCK128), (5, 2**29, 256, {}, RING128),
+    (5, 2**31 - 1, 256, {}, None)])  # more tiles than a grid may have work-items
 def test_variants(M, N, K, kw, want):
     """Which kernel multiplies what: few rows, the borders of the tiles' sizes, what the large tiles and the streaming
     kernel need, and that nothing needs more than the general kernels."""
-    if want is BLOCK64 and N > 1 << 30:  # (more 64-tiles than a grid holds work-items: refused)
-        assert name_of(M, N, K, **kw) in (BLOCK64, None)
-        return
     assert name_of(M, N, K, **kw) == want
 
 
 @pytest.mark.parametrize("name,M,N,K,kw", [
     (STREAM, 65, 512, 512, {}), (STREAM, 16, 512, 520, {}), (STREAM, 16, 512, 512, dict(lda=264)),
+    (RING64, 300, 300, 320, {}), (RING128, 300, 300, 512, dict(ldb=1 << 23)), (RING128, 30, 30, 512, dict(lds=18)),
     (TILE, 300, 300, 320, {}), (TILE, 300, 300, 512, dict(lds=18)), (TILE, 300, 300, 512, dict(a=(1 << 20) + 4)),
     (TILE, 300, 300, 512, dict(ldb=1 << 23))])
 def test_a_variant_that_cannot_run_the_problem_is_refused(monkeypatch, name, M, N, K, kw):

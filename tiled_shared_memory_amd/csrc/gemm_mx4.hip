@@ -26,9 +26,8 @@ constexpr int BK = 128;         // bytes of codes per slab and row
 constexpr int BB = BK / 16;     // blocks of them
 constexpr int PITCH = BK + 16;  // LDS row pitch, so that a fragment read's rows do not all start on one bank
 
-// D: slabs in flight in registers (even: the LDS buffers alternate).  REST: the
-// workgroups take the parts of the 256-tiles that whole_rounds leaves.
-template <int T, int FMT, int D, bool REST = false>
+// D: slabs in flight in registers (even: the LDS buffers alternate).
+template <int T, int FMT, int D>
 __global__ __launch_bounds__(kThreads) void gemm_mx4_block_kernel(Mx4Args p) {
   constexpr int W = T / 2, NB = W / 16;      // wave tile, 16 x 16 blocks per dimension
   constexpr int RP = kThreads / BB;          // rows per pass (64)
@@ -42,19 +41,9 @@ __global__ __launch_bounds__(kThreads) void gemm_mx4_block_kernel(Mx4Args p) {
   const int team = wave >> 2, wm = (wave >> 1) & 1, wn = wave & 1;
   int tm, tn;
   int64_t z;
-  if constexpr (REST) {
-    constexpr int S = 256 / T;
-    const int all = tiles_of<256>(p), pid = (int)whole_rounds(all, p.cus, kFewMx4Tiles) + (int)(blockIdx.x / (S * S));
-    if (pid >= all) return;  // uniform
-    tile_at<256>(p, pid, tile_group(p), z, tm, tn);
-    tm = S * tm + (int)blockIdx.x / S % S;
-    tn = S * tn + (int)blockIdx.x % S;
-  } else {
-    if (!tile_of<T>(p, 8, z, tm, tn)) return;  // uniform
-  }
+  if (!tile_of<T>(p, 8, z, tm, tn)) return;  // uniform
   const int64_t m0 = (int64_t)tm * T, n0 = (int64_t)tn * T;
   const int64_t M = valid_rows(p, z);
-  if (REST && (m0 >= M || n0 >= p.N)) return;  // uniform
 
   constexpr int H = NB / 2;
   const int row0 = tid / BB, chunk = tid % BB, kc = chunk * 16;
@@ -206,17 +195,6 @@ hipError_t block_t(const Mx4Args &p, hipStream_t stream) {
 }
 
 }  // namespace
-
-hipError_t launch_mx4_rest(const Mx4Args &a, int64_t tiles, hipStream_t stream) {
-  const dim3 grid((unsigned)(tiles * 16)), block(kThreads);
-  if (a.fmt == FMT_F32)
-    hipLaunchKernelGGL((gemm_mx4_block_kernel<64, FMT_F32, 2, true>), grid, block, 0, stream, a);
-  else if (a.fmt == FMT_F16)
-    hipLaunchKernelGGL((gemm_mx4_block_kernel<64, FMT_F16, 2, true>), grid, block, 0, stream, a);
-  else
-    hipLaunchKernelGGL((gemm_mx4_block_kernel<64, FMT_BF16, 2, true>), grid, block, 0, stream, a);
-  return hipPeekAtLastError();
-}
 
 hipError_t launch_mx4_block(const Mx4Args &p, int tile, hipStream_t stream) {
   return tile == 128 ? block_t<128, 2>(p, stream) : block_t<64, 2>(p, stream);

@@ -21,6 +21,10 @@ const char *mx4_name(Mx4Kernel k) {
       return "mx4_block_64x64x256";
     case Mx4Kernel::Tile:
       return "mx4_tile_256x256x256";
+    case Mx4Kernel::Ring128:
+      return "mx4_ring_128x128x256";
+    case Mx4Kernel::Ring64:
+      return "mx4_ring_64x64x256";
     case Mx4Kernel::Stream:
       return "mx4_stream";
     default:
@@ -142,17 +146,21 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
   p.slope = act == TSM_ACT_LEAKY_RELU ? slope : 0.f;
   p.vec_store = (uintptr_t)C % (uintptr_t)(4 * es) == 0 && ldc % 4 == 0 && strideC % 4 == 0;
 
-  // 64-tiles while there are at most 128 of 128 x 128, those while one round of the CUs does them, then 256-tiles (us, 64 |
+  // 64-tiles while there are at most 128 of 128 x 128, those while one round of the CUs does them, then 256-tiles; the
+  // first two with direct copies where the operands are aligned, else through registers (us, general 64 | 128 | direct 64 |
   // 128 | 256):
-  //   1024 x 1024 x 4096   10.4 | 18.6 | 25.1     1024 x 2048 x 4096   16.0 | 18.9 | 25.2     2000 x 2000 x 2001   27 | 18
-  //   2048 x 2048 x 4096   27.7 | 20.7 | 25.3     2304 x 2048 x 4096   32.8 | 35.6 | 25.4     256 x 16384 x 4096   35 | 25 | 30
-  // and for up to 64 rows: 64 x 16384 x 8192   25.0 | 35.3.
+  //    512 x 4096 x 4096   16.1 |      | 14.8 | 15.8              256 x 8192 x 8192   33.7 |      | 34.5 | 35.2
+  //   1024 x 2048 x 4096   15.8 | 18.9 | 14.3 | 15.9 | 25.2      1024 x 4096 x 4096        | 20.1 | 24.8 | 18.5
+  //   2048 x 2048 x 4096   27.7 | 19.6 | 24.5 | 17.5 | 25.3      2304 x 2048 x 4096   32.8 | 35.6 |      |      | 25.4
+  //   256 x 16384 x 4096   35   | 24.7 |      |      | 29.6      2000 x 2000 x 2001   27   | 17.9
+  // and for up to 64 rows: 64 x 16384 x 8192   25.0 | 35.3 | 24.1 | 33.0.
   const int64_t tiles128 = ((M + 127) / 128) * ((N + 127) / 128), tiles64 = ((M + 63) / 64) * ((N + 63) / 64);
   const int64_t all128 = tiles128 > ((int64_t)1 << 40) / batch ? (int64_t)1 << 40 : tiles128 * batch;
-  const bool small = all128 <= 128 || (M <= 64 && tiles64 * 512 <= 0xffffffffLL);
-  call->kernel = small ? Mx4Kernel::Block64 : Mx4Kernel::Block128;
+  const bool small = all128 <= 128 || (M <= 64 && tiles64 * 512 <= 0xffffffffLL), direct = mx4_tile_supports(p);
+  call->kernel = direct ? (small ? Mx4Kernel::Ring64 : Mx4Kernel::Ring128)
+                        : (small ? Mx4Kernel::Block64 : Mx4Kernel::Block128);
   if ((small ? tiles64 : tiles128) * 512 > 0xffffffffLL) return fail(TSM_ERROR_NOT_SUPPORTED, "tile grid too large");
-  if (M > 64 && all128 > 256 && mx4_tile_supports(p)) call->kernel = Mx4Kernel::Tile;
+  if (M > 64 && all128 > 256 && direct) call->kernel = Mx4Kernel::Tile;
   const Mx4Few few = mx4_few_plan(p);
   if (few.use_stream) call->kernel = Mx4Kernel::Stream;
   // TSM_GEMM_KERNEL=<name> forces a variant (tests and tuning); names of other
@@ -160,11 +168,12 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
   const char *force = getenv("TSM_GEMM_KERNEL");
   if (force && strncmp(force, "mx4_", 4) == 0) {
     Mx4Kernel want = Mx4Kernel::None;
-    for (Mx4Kernel k : {Mx4Kernel::Block128, Mx4Kernel::Block64, Mx4Kernel::Tile, Mx4Kernel::Stream})
+    for (Mx4Kernel k : {Mx4Kernel::Block128, Mx4Kernel::Block64, Mx4Kernel::Ring128, Mx4Kernel::Ring64, Mx4Kernel::Tile,
+                        Mx4Kernel::Stream})
       if (strcmp(force, mx4_name(k)) == 0) want = k;
     if (want == Mx4Kernel::None) return fail(TSM_ERROR_INVALID_VALUE, "TSM_GEMM_KERNEL=%s names no kernel", force);
-    if ((want == Mx4Kernel::Block64 && tiles64 * 512 > 0xffffffffLL) ||
-        (want == Mx4Kernel::Tile && !mx4_tile_supports(p)) || (want == Mx4Kernel::Stream && !few.can_stream))
+    if (((want == Mx4Kernel::Block64 || want == Mx4Kernel::Ring64) && tiles64 * 512 > 0xffffffffLL) ||
+        ((want == Mx4Kernel::Tile || want == Mx4Kernel::Ring128 || want == Mx4Kernel::Ring64) && !direct) || (want == Mx4Kernel::Stream && !few.can_stream))
       return fail(TSM_ERROR_NOT_SUPPORTED, "TSM_GEMM_KERNEL=%s cannot run this problem", force);
     call->kernel = want;
     call->forced = true;
@@ -184,6 +193,10 @@ int mx4_run(const Call &c, void *stream) {
       return launched(launch_mx4_block(c.p, 128, s));
     case Mx4Kernel::Block64:
       return launched(launch_mx4_block(c.p, 64, s));
+    case Mx4Kernel::Ring128:
+      return launched(launch_mx4_ring(c.p, 128, s));
+    case Mx4Kernel::Ring64:
+      return launched(launch_mx4_ring(c.p, 64, s));
     case Mx4Kernel::Tile:
       return launched(launch_mx4_tile(c.p, !c.forced, s));
     case Mx4Kernel::Stream:

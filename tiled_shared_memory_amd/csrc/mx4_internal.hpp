@@ -35,6 +35,8 @@ struct Mx4Args {
   int32_t cus;      // 256 x 256 tiles: CUs, one tile each per round (0: no second launch)
 };
 
+// tile: 64 or 128; for operands that mx4_tile_supports takes.
+hipError_t launch_mx4_ring(const Mx4Args &p, int tile, hipStream_t stream);
 // 256 x 256 tiles: see mx4_tile_supports for what they need.
 bool mx4_tile_supports(const Mx4Args &p);
 // whole_only: tiles left over from whole rounds of the CUs go to launch_mx4_rest.
@@ -45,7 +47,7 @@ hipError_t launch_mx4_rest(const Mx4Args &a, int64_t tiles, hipStream_t stream);
 // CUs of the current device (gemm_api.hip).
 int device_cus();
 
-enum class Mx4Kernel { None, Block128, Block64, Tile, Stream };
+enum class Mx4Kernel { None, Block128, Block64, Ring128, Ring64, Tile, Stream };
 // Few rows (up to 64): what the problem allows, and the rule's choice.
 struct Mx4Few {
   bool can_stream = false, use_stream = false;
