@@ -88,7 +88,7 @@ def name_of(M, N, K, batch=1, lda=None, ldb=None, a=1 << 20, fmt=tsm.TSM_BF16, l
     (256, 256, 4096, dict(batch=65), TILE), (256, 256, 4096, dict(batch=64), RING128),
     (1 << 21, 1 << 12, 256, {}, TILE), (2304, 2048, 4096, dict(lda=1 << 22), TILE),  # 255 * 2^22 + 2048 bytes are below 2^30
     (2304, 2048, 4096, dict(lda=1 << 23), BLOCK128),
-    (2304, 2048, 4096, dict(ldc=1 << 23), BLOCK128), (5, 2**29, 256, {}, RING128),
+    (2304, 2048, 4096, dict(ldc=1 << 23), BLOCK128), (5, 2**29, 256, {}, BLOCK128),
     (5, 2**31 - 1, 256, {}, None)])  # more tiles than a grid may have work-items
 def test_variants(M, N, K, kw, want):
     """Which kernel multiplies what: few rows, the borders of the tiles' sizes, what the large tiles and the streaming
