@@ -353,10 +353,16 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs &a, const char *r
   }
 }
 
+// Place in LDS of expert e's bias: a token's lanes read their i-th ones beside each other.
+template <int L, int V>
+__device__ __forceinline__ int bias_at(int e) {
+  return e % V * L + e / V;
+}
+
 // The order by keys in float64 of a token's experts that may be among the chosen: bits `within` of each lane's, up to L
 // in the token, `before` of them in the lanes before.  All of a wave's lanes come here, also those of tokens that do not
 // ask for it.
-template <int FMT, int L>
+template <int FMT, int L, int V>
 __device__ __forceinline__ void order_exactly(const RouteArgs &a, const char *row, const float *bias, bool asked,
                                               uint32_t within, int before, int around, int e0, double *keys, int *ids,
                                               int *chosen, float *logit) {
@@ -379,7 +385,7 @@ __device__ __forceinline__ void order_exactly(const RouteArgs &a, const char *ro
   const int e = held ? ids[l] : 0;
   const float x = elem_f32<FMT>(elem_bits<FMT>(row, e));
   const double d = exp(a.sigmoid ? -(double)x : x - top);
-  const double key = (a.sigmoid ? 1.0 / (1.0 + d) : d / sum) + (double)bias[e];
+  const double key = (a.sigmoid ? 1.0 / (1.0 + d) : d / sum) + (double)bias[bias_at<L, V>(e)];
   if (held) keys[l] = key;
   wave_sync();
   if (held) {
@@ -523,8 +529,8 @@ template <int FMT, int L, int V>
 __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
   constexpr int kTokens = kThreads / L;
   __shared__ double keys[4][L * V < 64 ? 64 : L * V];  // of the choice in float64: a wave's
-  __shared__ float bias_of[L * V];         // -inf for NaN
-  __shared__ Choice list[kTokens][8];
+  __shared__ float bias_of[L * V];         // -inf for NaN; in the order of bias_at
+  __shared__ Choice list[kTokens][9];      // (8; the rows of a wave's tokens on different banks)
   __shared__ double near_keys[kTokens][L];
   __shared__ int near_ids[kTokens][L];
   __shared__ int chosen[kTokens][8];
@@ -534,7 +540,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
   if (a.bias) {
     for (int i = threadIdx.x; i < a.experts; i += kThreads) {
       const float b = a.bias[i];
-      bias_of[i] = b == b ? b : -kInf;
+      bias_of[bias_at<L, V>(i)] = b == b ? b : -kInf;
     }
     __syncthreads();
   }
@@ -567,7 +573,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
         float g[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float s = score_of(a.sigmoid, x[i], top, by) + (scored ? bias_of[e0 + i] : 0.f);
+          const float s = score_of(a.sigmoid, x[i], top, by) + (scored ? bias_of[i * L + l] : 0.f);
           g[i] = x[i] > -kInf ? s : -kInf;
           if (scored) key[i] = ordered(g[i]);
         }
@@ -680,7 +686,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
       c.x = elem_f32<FMT>(elem_bits<FMT>(row, c.e));
       c.key = c.x;
       if (scored) {
-        c.bias = bias_of[c.e];
+        c.bias = bias_of[bias_at<L, V>(c.e)];
         c.key = score_of(a.sigmoid, c.x, top, by) + c.bias;
       }
       list[slot][l] = c;
@@ -717,13 +723,13 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
           if (ordered(list[slot][j].key) == least) lx = list[slot][j].x, lb = list[slot][j].bias;
         for (uint32_t rest = within & ~taken; rest; rest &= rest - 1) {
           const int e = e0 + __builtin_ctz(rest);
-          unclear |= elem_f32<FMT>(elem_bits<FMT>(row, e)) != lx || bias_of[e] != lb;
+          unclear |= elem_f32<FMT>(elem_bits<FMT>(row, e)) != lx || bias_of[bias_at<L, V>(e)] != lb;
         }
       }
       unclear = row_ballot<L>(unclear) != 0;
       open |= unclear && around > L;
       if (__ballot(unclear && !open))
-        order_exactly<FMT, L>(a, row, bias_of, unclear && around <= L, within, row_scan<L>(own) - own, around, e0,
+        order_exactly<FMT, L, V>(a, row, bias_of, unclear && around <= L, within, row_scan<L>(own) - own, around, e0,
                               near_keys[slot], near_ids[slot], chosen[slot], logit[slot]);
     }
     wave_sync();
