@@ -13,6 +13,11 @@
 // one read gives a lane all of an operand's scales of a slab and the matrix
 // instruction picks the block's byte.
 //
+// Measured (us): 1000 x 1500 x 777 with float32 out 11.5; 2000 x 2000 x 2001 17.9; 4000 x
+// 5000 x 3001 93-113, 1.1-1.3 PFLOP/s.  Rows at odd addresses cost most: a 16-byte load of
+// 64 lanes there takes 72 cycles of L1, of rows at 4 bytes 20, and L1 is busy all the time
+// (at 16 bytes 4000 x 5000 x 3008 takes 85).
+//
 // Any sizes and any alignment, as there: rows past M or N read the last row (their
 // products are never stored), and the codes past K are shifted out of the last
 // vectors, so they are zeros in both operands.

@@ -9,6 +9,12 @@
 //
 // The fragments are those of the 256-tiles (gemm_mx4_tile.hip): a lane takes blocks
 // 4h .. 4h + 3 of a slab's eight (h = lane / 32), whose scales are one word.
+//
+// Measured (us, bf16 out): 128 x 8192 x 8192 21.1, 512 x 4096 x 4096 14.5 (T = 64); 512 x
+// 8192 x 8192 33.9, 2048 x 2048 x 4096 17.8, 1.9 PFLOP/s (T = 128).  The MFMAs are busy for
+// 6-17% of the cycles: a CU receives 30 bytes a ns from L2 whatever the ring's depth (8
+// stages were no faster than 4), 7.7 TB/s over the chip, and only tiles that reuse more
+// per byte (256 x 256, or these with K split between workgroups) would need less.
 #include "lds_ring.hpp"
 #include "mx4_common.hpp"
 

@@ -21,6 +21,13 @@
 // in the four sub-slices, in both operands, and the matrix instruction picks the
 // byte.
 //
+// Measured: 8192 x 8192 x 8192 227-250 us, 4.4-4.8 PFLOP/s, MFMAs busy for 61% of the
+// cycles.  Power bounds it: codes of zeros take 94 us for 4096 x 4096 x 16384 where
+// Gaussian ones take 119, a unit of K costs the same at every size (5.1 PFLOP/s), and
+// what fills the gaps between tiles gains nothing (workgroups that stay and request the
+// next tile's first slabs before they store, as they are or started one after another:
+// 248-251 where these take 248).  Fewer rounds: 4096 x 4096 x 4096 37 us.
+//
 // K's last slab, which may hold half of its elements, comes first, so that its zeros
 // and its scales are the prologue's business and the loop has no branch for them.
 #include "lds_ring.hpp"

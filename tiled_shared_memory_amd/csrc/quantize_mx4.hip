@@ -6,6 +6,9 @@
 // conversion instruction divides and rounds in one step, with the scale of E = 0,
 // 2^-127, given as that subnormal number.  A block with a NaN or an infinity gets
 // E = 255 and codes of 0.
+//
+// Bound by memory: 16384 x 4096 bf16 29.4 us (5.8 TB/s), back 27-31 (5.7-6.4); columns of
+// 1500 x 8195 float32 14.5 (3.8: 792 workgroups, 3 per CU), back 12.7 (4.3).
 #include "mx4_codes.hpp"
 #include "mx4_internal.hpp"
 
