@@ -109,6 +109,35 @@ def test_near_ties(score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,G,top", [(8, 2, 1, 1), (8, 8, 1, 1), (16, 4, 4, 2), (16, 8, 8, 5), (60, 8, 1, 1),
+                                       (64, 8, 8, 3), (128, 8, 8, 4), (128, 8, 1, 1), (256, 8, 8, 4), (256, 7, 1, 1),
+                                       (512, 8, 16, 4)])
+@pytest.mark.parametrize("near", [3, 9, 40])
+def test_some_near_ties(E, k, G, top, near, score):
+    """Tokens some of whose experts, inside the choice, at its border and past it, and in groups at theirs, have keys
+    nearer than float32 holds: fewer than the lanes of a token, and more."""
+    import torch
+
+    g = gen(E + near)
+    T = 700
+    x = torch.randn((1, E), generator=g, device="cuda").expand(T, E)
+    s = ref.scores(x[:1].double(), score)[0]
+    bias = 0.2 * torch.randn(E, generator=g, device="cuda")
+    key = s + bias
+    at = key.argsort(descending=True)
+    lo = max(0, min(k, E) - (near + 1) // 2)
+    close = at[lo:lo + near]
+    bias[close] = (key[close[:1]] - s[close]).float()  # equal to within a rounding of the bias
+    step = torch.randint(-1, 2, (T, E), generator=g, device="cuda").double() * 2.0 ** -23
+    x = (x.double() + step).float()
+    say(f"[gpu] route some near ties {E} {k} {G} {near} {score}")
+    ids, w = tsm.route_tokens(x, k, score=score, bias=bias, groups=G, top_groups=top)
+    want = ref.choose(x.double(), k, score, bias, G, top, 2)
+    assert torch.equal(ids.long(), want), (ids.long() != want).nonzero()[:4].tolist()
+    check_weights(w, ids, x.double(), score, True, 1.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_far_logits(score):
     """Logits far from 0: weights neither overflow nor vanish where they are renormalised."""
     import torch
