@@ -27,7 +27,7 @@
 // ones, so they neither underflow nor overflow.
 //
 // What bounds it is the arithmetic: 65536 x 256 float32 with sigmoid scores, a bias and
-// 4 of 8 groups takes 37-44 us, 1140 vector instructions per wave (four tokens), which
+// 4 of 8 groups takes 35-41 us, 1140 vector instructions per wave (four tokens), which
 // keep the SIMDs busy for 70% of its cycles; 20 us of it are the bias and the groups
 // (scores of every expert, near ties).  The logits alone would take 14 us from memory.
 // The gradient of the same, 18.5 us, moves its 113 MB at 6.1 TB/s.
@@ -84,7 +84,9 @@ __device__ __forceinline__ float across(float v) {
 }
 template <int STEP>
 __device__ __forceinline__ double across(double v) {
-  return __shfl_xor(v, 1 << STEP, 64);
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)across<STEP>((int)(uint32_t)b), hi = (uint32_t)across<STEP>((int)(uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 // f(the value r lanes before, around the token's lanes, and r) for the multiples of `apart` (a power of two) below L.
 template <int L, class T, class F>
@@ -201,6 +203,7 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, T *keys, T e
     if (g >= a.groups) continue;
     T b1 = none, b2 = none;
     int at = g % size;
+#pragma unroll 4
     for (int i = 0; i < size; ++i) {
       const T k = keys[g * size + at];
       at = at + 1 == size ? 0 : at + 1;
@@ -345,18 +348,17 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs &a, const char *r
     // of the lanes that hold it, the lowest expert
     int e = m == best ? at : a.experts;
     steps<6>([&](auto s) {
-      const int o = __shfl_xor(e, 1 << s.value, 64);
+      const int o = across<s.value>(e);
       e = o < e ? o : e;
     });
     if (lane == 0) {
       chosen[j] = best > none ? e : -1;
-      if (best > none) {
-        logit[j] = elem_f32<FMT>(elem_bits<FMT>(row, e));
-        keys[e] = none;
-      }
+      if (best > none) keys[e] = none;
     }
     wave_sync();
   }
+  if (lane < a.topk && chosen[lane] >= 0) logit[lane] = elem_f32<FMT>(elem_bits<FMT>(row, chosen[lane]));
+  wave_sync();
 }
 
 // Place in LDS of expert e's bias: a token's lanes read their i-th ones beside each other.
