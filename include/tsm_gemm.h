@@ -503,7 +503,8 @@ int gemm_mx4_grouped(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t 
 
 /*
  * gemm_mx4_float_a -- mx4_quantize of activations X (TSM_ROW, format xdtype) and
- * their product with B in one call: the same bits as the two calls.
+ * their product with B in one call: the codes and scales of mx4_quantize; the
+ * kernel, and with it the order of the sums, may be another than gemm_mx4's.
  *   rows      : NULL (a strided batch, strideX = 0 shares X), or counts as
  *               gemm_mx4_grouped takes them.
  *   workspace : DEVICE memory of gemm_mx4_float_a_workspace_bytes(M, K, batch)

@@ -368,8 +368,8 @@ def test_batches_and_groups(M, N, K):
 @pytest.mark.parametrize("M,N,K", [(1, 300, 4096), (1, 64, 33), (5, 100, 777), (16, 512, 2048), (64, 256, 512),
                                    (500, 512, 1024)])
 def test_product_of_activations(M, N, K, fmt):
-    """Activations quantised within the call: the bits of the two calls, with and without a workspace, in a batch, with
-    a shared operand and with counts."""
+    """Activations quantised within the call: the products of their codes, with and without a workspace, in a batch,
+    with a shared operand and with counts."""
     import torch
 
     g = gen(M + N + K)
