@@ -478,6 +478,43 @@ def test_few_rows_in_many_groups(G, M, N, K):
         assert torch.equal(c[own], plain[own]) and (c[~own] == 55.0).all()
 
 
+@pytest.mark.parametrize("G,M,N,K", [(2, 1, 300, 1024), (5, 1, 64, 512), (3, 7, 130, 640), (40, 16, 256, 256),
+                                     (9, 5, 33, 77)])
+def test_a_weight_that_problems_share(G, M, N, K):
+    """Problems of one weight, whose rows follow each other or not: codes and activations, padded, with counts, and
+    one matrix of activations for all."""
+    import torch
+
+    g = gen(G * M + N)
+    say(f"[gpu] mx4 shared weight {G} {M}x{N}x{K}")
+    kb, nb = (K + 1) // 2, (K + 31) // 32
+    a, sa, va = operand(G * M, K, 0, 0, g)
+    b, sb, vb = operand(N, K, 0, 0, g, 112, 124)
+    want, mag = ref.product(va, vb)
+    far = torch.full((G, M + 1, kb + 16), 0xFF, dtype=torch.uint8, device="cuda")
+    far[:, :M, :kb] = a.view(G, M, kb)
+    far_s = torch.full((G, M + 2, nb + 4), 0xFF, dtype=torch.uint8, device="cuda")
+    far_s[:, :M, :nb] = sa.view(G, M, nb)
+    buf = torch.full((G, M + 1, N + 5), 77.0, device="cuda")
+    for q in (a.view(G, M, kb), far[:, :M, :kb]):
+        for s in (sa.view(G, M, nb), far_s[:, :M, :nb]):
+            for c in (torch.full((G, M, N), 9.0, device="cuda"), buf[:, :M, :N]):
+                c.fill_(9.0)
+                tsm.matmul_mx4(q, s, b.t(), sb, columns=K, out=c)
+                check_product(c.reshape(G * M, N), want, mag, K, "f32")
+    assert (buf[:, M] == 77.0).all() and (buf[:, :, N:] == 77.0).all()
+    rows = torch.tensor([M - 1] + [M] * (G - 1), dtype=torch.int32, device="cuda")
+    c = torch.full((G, M, N), 55.0, device="cuda")
+    tsm.matmul_mx4(a.view(G, M, kb), sa.view(G, M, nb), b.t(), sb, columns=K, rows=rows, out=c)
+    assert (c[0, M - 1] == 55.0).all()
+    own = torch.arange(M, device="cuda")[None, :] < rows[:, None]
+    check_product(c[own], want[own.view(-1)], mag[own.view(-1)], K, "f32")
+    x = torch.randn((G, M + 1, K + 3), generator=g, device="cuda")
+    for v in (x[:, :M, :K].contiguous(), x[:, :M, :K], x[:1, :M, :K].expand(G, M, K)):
+        want, mag = ref.product(ref.values(*tsm.quantize_mx4(v.reshape(G * M, K)), K), vb)
+        check_product(tsm.matmul_mx4(v, None, b.t(), sb).view(G * M, N), want, mag, K, "f32")
+
+
 def test_two_calls_at_once():
     """Calls on two streams at once, of one weight, each with its own workspace, and quantisations beside them."""
     import torch

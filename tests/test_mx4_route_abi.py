@@ -67,11 +67,12 @@ BLOCK64, BLOCK128, RING64, RING128, TILE, STREAM = (
     "mx4_tile_256x256x256", "mx4_stream")
 
 
-def name_of(M, N, K, batch=1, lda=None, ldb=None, a=1 << 20, fmt=tsm.TSM_BF16, ldc=None, lds=None, rows=None):
+def name_of(M, N, K, batch=1, lda=None, ldb=None, a=1 << 20, fmt=tsm.TSM_BF16, ldc=None, lds=None, rows=None,
+            shared=False):
     kb, nb = (K + 1) // 2, (K + 31) // 32
     lda, ldb, lds, ldc = lda or kb, ldb or kb, lds or nb, ldc or N
-    return tsm.tsm_gemm_mx4_kernel_name(M, N, K, a, lda, M * lda, 1 << 21, lds, M * lds, 1 << 22, ldb, N * ldb, 1 << 23,
-                                        lds, N * lds, 1 << 45, ldc, M * ldc, batch, rows, fmt)
+    return tsm.tsm_gemm_mx4_kernel_name(M, N, K, a, lda, M * lda, 1 << 21, lds, M * lds, 1 << 22, ldb, 0 if shared else N * ldb,
+                                        1 << 23, lds, 0 if shared else N * lds, 1 << 45, ldc, M * ldc, batch, rows, fmt)
 
 
 @pytest.mark.parametrize("M,N,K,kw,want", [
@@ -89,6 +90,9 @@ def name_of(M, N, K, batch=1, lda=None, ldb=None, a=1 << 20, fmt=tsm.TSM_BF16, l
     (1 << 21, 1 << 12, 256, {}, TILE), (2304, 2048, 4096, dict(lda=1 << 22), TILE),  # 255 * 2^22 + 2048 bytes are below 2^30
     (2304, 2048, 4096, dict(lda=1 << 23), BLOCK128),
     (2304, 2048, 4096, dict(ldc=1 << 23), BLOCK128), (5, 2**29, 256, {}, BLOCK128),
+    (1, 4096, 4096, dict(batch=65, shared=True), RING64), (1, 4096, 4096, dict(batch=64, shared=True), STREAM),
+    (16, 4096, 4096, dict(batch=256, shared=True), TILE), (16, 4096, 4096, dict(batch=256), STREAM),
+    (16, 64, 128, dict(batch=600, rows=1 << 24, shared=True), STREAM),
     (5, 2**31 - 1, 256, {}, None)])  # more tiles than a grid may have work-items
 def test_variants(M, N, K, kw, want):
     """Which kernel multiplies what: few rows, the borders of the tiles' sizes, what the large tiles and the streaming

@@ -116,6 +116,19 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
     for (int i = 0; i < 4; ++i)
       if (ranges_overlap(C, c_bytes, in[i], bytes[i])) return fail(TSM_ERROR_INVALID_VALUE, "C overlaps %s", names[i]);
   }
+  // Problems that share B and whose rows follow each other in A and C are one of all rows: B is read for all of them at
+  // once (64 of 16 x 4096 x 4096: 18 us, one by one 76).
+  if (batch > 1 && !rows && strideB == 0 && stride_sb == 0 && K > 0 && batch <= 0x7fffffffLL / M) {
+    const int64_t kb = mx4_code_bytes(K), nb = mx4_blocks(K);
+    const bool one = M == 1;
+    if ((one ? strideA >= kb : strideA == M * lda) && (one ? stride_sa >= nb : stride_sa == M * ld_sa) &&
+        (one || strideC == M * ldc)) {
+      if (one) lda = strideA, ld_sa = stride_sa, ldc = strideC;
+      M *= batch;
+      batch = 1;
+      strideA = stride_sa = strideC = 0;
+    }
+  }
   const int64_t es = fmt_bytes(out_dtype);
   Mx4Args &p = call->p;
   p = Mx4Args{};
@@ -372,10 +385,11 @@ int gemm_mx4_float_a(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx
                 B, ldb, strideB, scale_b, ld_sb, stride_sb, C, ldc, strideC, batch, rows, false, out_dtype, activation,
                 slope, &c);
   if (st != TSM_SUCCESS) return st;
-  if (c.kernel == Mx4Kernel::Stream && !c.forced && mx4_rows_supports(c.p)) {
+  // (problems that mx4_plan made one have to lie so in X too)
+  const bool alike = c.p.M == M || (M == 1 ? strideX > 0 : strideX == M * ldx);
+  if (c.kernel == Mx4Kernel::Stream && !c.forced && alike && mx4_rows_supports(c.p)) {
     c.p.X = X;
-    c.p.ldx = ldx;
-    c.p.strideX = strideX;
+    c.p.ldx = c.p.M != M && M == 1 ? strideX : ldx;
     return launched(launch_mx4_rows(c.p, xdtype, (hipStream_t)stream));
   }
   if (K > 0) {

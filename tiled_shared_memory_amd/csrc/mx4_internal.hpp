@@ -17,7 +17,7 @@ struct Mx4Args {
   const uint8_t *SA, *SB;   // scale bytes
   void *C;
   const void *X;            // few rows: activations to quantise, in A's place
-  int64_t ldx, strideX;
+  int64_t ldx;
   int64_t M, N, K;          // K in elements
   int64_t kb, nb;           // bytes of codes and of scales per row
   int64_t lda, ldb, ldsa, ldsb, ldc;  // bytes; of C elements
