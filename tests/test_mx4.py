@@ -266,6 +266,8 @@ def test_middle_tiles(monkeypatch, T, M, N, K, pad, out):
     check_product(c, *ref.product(va, vb, "leaky_relu", 0.25), K, out, 2.0 ** -24)
     c.fill_(77.0)
     assert (buf == 77.0).all()
+    if (M, T) == (130, 64):  # enough tiles for the shorter ring
+        M, N = 700, 520
     a3, sa3, _ = (t.reshape(5, M, -1) for t in operand(5 * M, K, 0, 0, g))
     b3, sb3, _ = (t.reshape(5, N, -1) for t in operand(5 * N, K, 0, 0, g, 112, 124))
     plain = tsm.matmul_mx4(a3, sa3, b3.transpose(1, 2), sb3, out_dtype=dt)

@@ -5,16 +5,21 @@
 // Four waves own a quarter of the tile each.  Slabs of 256 elements (128 bytes of a row)
 // and their scales go global -> LDS with direct copies on a ring of D stages, D - 1
 // slabs ahead: what bounds a tile that has a CU to itself is the way of a slab from
-// memory, so as many of them as LDS holds are under way.
+// memory, so as many of them as LDS holds are under way.  Where there is room for it two
+// slabs, 256 neighbouring bytes of each row, are requested together, which memory serves
+// faster (256 x 8192 x 8192 29 us, one at a time 34.2; T = 128 has room for one ahead
+// so, 42 against 35).
 //
 // The fragments are those of the 256-tiles (gemm_mx4_tile.hip): a lane takes blocks
 // 4h .. 4h + 3 of a slab's eight (h = lane / 32), whose scales are one word.
 //
-// Measured (us, bf16 out): 128 x 8192 x 8192 21.1, 512 x 4096 x 4096 14.5 (T = 64); 512 x
-// 8192 x 8192 33.9, 2048 x 2048 x 4096 17.8, 1.9 PFLOP/s (T = 128).  The MFMAs are busy for
-// 6-17% of the cycles: a CU receives 30 bytes a ns from L2 whatever the ring's depth (8
-// stages were no faster than 4), 7.7 TB/s over the chip, and only tiles that reuse more
-// per byte (256 x 256, or these with K split between workgroups) would need less.
+// Each sub-slice's fragments are read while the one before is multiplied; that alone
+// gains nothing here.  Measured (us, bf16 out): 128 x 8192 x 8192 18.9, 256 x 8192 x 8192
+// 29 (T = 64); 512 x 8192 x 8192 35, 2048 x 2048 x 4096 17.8, 1.9 PFLOP/s (T = 128).  With
+// operands from the Infinity Cache these are 14.0, 22.3, 28.5: the rest is memory, which
+// serves 128 or 256 bytes of a row at a time.  The MFMAs are busy for 6-17% of the cycles:
+// only tiles that reuse more per byte (256 x 256, or these with K split between workgroups)
+// would take fewer bytes.
 #include "lds_ring.hpp"
 #include "mx4_common.hpp"
 
@@ -41,6 +46,8 @@ __device__ __forceinline__ void ring(const Mx4Args &p) {
   constexpr int L = T / 32;              // wave-loads (1 KiB: 8 rows) per wave, operand and slab
   constexpr int S = T / 64;              // wave-loads of scales (256 bytes: 32 rows) per wave and slab
   constexpr int N = 2 * L + S;
+  // slabs are requested two at a time (not by tiles that come after whole rounds: 4112 x 4096 x 4096 48 us, was 46)
+  constexpr bool PAIR = T == 64 && !REST;
   constexpr int CODES = T * BK, BYTES = 2 * CODES + 2 * T * 8;  // of an operand, of a stage
   // an array each: a read waits for the copies into its array, as the compiler sees to it
   __shared__ __attribute__((aligned(1024))) char s0[BYTES], s1[BYTES], s2[BYTES], s3[BYTES], s4[BYTES], s5[BYTES],
@@ -89,22 +96,29 @@ __device__ __forceinline__ void ring(const Mx4Args &p) {
   auto stage = [&](int d) -> char * {
     return d == 0 ? s0 : d == 1 ? s1 : d == 2 ? s2 : d == 3 ? s3 : d == 4 ? s4 : d == 5 ? s5 : d == 6 ? s6 : s7;
   };
-  // Slab j into stage d.  Chunks past K, and slabs past the end, copy zeros without touching memory (their scales too).
-  auto fetch = [&](int j, int d) {
+  // Slab j into stage d: part 0 A's codes, 1 B's, 2 the scales.  Chunks past K, and slabs past the end, copy zeros without
+  // touching memory (their scales too).
+  auto fetch = [&](int j, int d, auto part) {
     const int left = j < nk ? (int)(p.kb - (int64_t)j * BK) : 0, at = left ? j * BK : 0;
     asm volatile("" : "+s"(codes_at), "+s"(scales_at));  // (an address in a register for every copy would spill)
+    if constexpr (part.value == 0) {
 #pragma unroll
-    for (int i = 0; i < L; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(stage(d) + codes_at + i * 1024), 16,
-                                               chunk[i] < left ? offa[i] : kOutside, at, 0, 0);
+      for (int i = 0; i < L; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)(stage(d) + codes_at + i * 1024), 16,
+                                                 chunk[i] < left ? offa[i] : kOutside, at, 0, 0);
+    }
+    if constexpr (part.value == 1) {
 #pragma unroll
-    for (int i = 0; i < L; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(stage(d) + CODES + codes_at + i * 1024), 16,
-                                               chunk[i] < left ? offb[i] : kOutside, at, 0, 0);
+      for (int i = 0; i < L; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)(stage(d) + CODES + codes_at + i * 1024), 16,
+                                                 chunk[i] < left ? offb[i] : kOutside, at, 0, 0);
+    }
+    if constexpr (part.value == 2) {
 #pragma unroll
-    for (int i = 0; i < S; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(stage(d) + scales_at + i * 256), 4,
-                                               half * 64 < left ? offs[i] : kOutside, at / 16, 0, 0);
+      for (int i = 0; i < S; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)(stage(d) + scales_at + i * 256), 4,
+                                                 half * 64 < left ? offs[i] : kOutside, at / 16, 0, 0);
+    }
   };
 
   f32x16 acc[NB][NB];
@@ -113,42 +127,89 @@ __device__ __forceinline__ void ring(const Mx4Args &p) {
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x16{};
   const int r32 = lane & 31;
-  unrolled<D - 1>([&](auto d) { fetch(d.value, d.value); });
-  auto multiply = [&](int j, auto d) {  // slab j in stage d
-    // it is here, and every wave is past its reads of the one before, whose stage is refilled
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N * (D - 2)) : "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    fetch(j + D - 1, (d.value + D - 1) % D);
-    const char *const s = stage(d.value);
-    uint32_t ea[NB], eb[NB];
+  // fragments of two sub-slices, scales of two slabs (zeros before the first)
+  u32x4 fa[2][NB], fb[2][NB];
+  uint32_t ea[2][NB], eb[2][NB];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      int at = lane * 4;
-      asm("" : "+v"(at));
-      ea[i] = *reinterpret_cast<const uint32_t *>(s + 2 * CODES + (wm * NB + i) * 256 + at);
-      eb[i] = *reinterpret_cast<const uint32_t *>(s + 2 * CODES + T * 8 + (wn * NB + i) * 256 + at);
-    }
+  for (int i = 0; i < NB; ++i) fa[1][i] = fb[1][i] = u32x4{}, ea[1][i] = eb[1][i] = 0;
+  // (B, A): a lane's accumulator holds groups of 4 consecutive columns of one row of C
+  auto multiply = [&](auto u, const uint32_t(&sa)[NB], const uint32_t(&sb)[NB]) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+        acc[i][k] = mfma_mx4_32<u.value>(fb[u.value & 1][k], sb[k], fa[u.value & 1][i], sa[i], acc[i][k]);
+  };
+  // Slab j in stage d: each sub-slice's fragments are read, and a part of slab j + D - 1 requested, while the one before
+  // is multiplied.
+  auto slab = [&](int j, auto d) {
+    const char *const s = stage(d.value);
     unrolled<4>([&](auto u) {
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (u.value == 0) {
+        // it is here, and every wave is past its reads of the one before, whose stage is refilled.  (A pair's copies go out
+        // in any order, so its first slab waits for both.)
+        constexpr int newer = PAIR && d.value % 2 == 0 ? N * (D - 4) : N * (D - 2);
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(newer) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+      }
+      // (opaque offsets: a read that the compiler can tell apart from a stage's first copy makes it wait for every copy)
       int at = r32 * BK + swz<2>(r32, 4 * half + u.value) * 16;
       asm("" : "+v"(at));
-      u32x4 fa[NB], fb[NB];
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
-        fa[i] = *reinterpret_cast<const u32x4 *>(s + (wm * W + i * 32) * BK + at);
-        fb[i] = *reinterpret_cast<const u32x4 *>(s + CODES + (wn * W + i * 32) * BK + at);
+        fa[u.value & 1][i] = *reinterpret_cast<const u32x4 *>(s + (wm * W + i * 32) * BK + at);
+        fb[u.value & 1][i] = *reinterpret_cast<const u32x4 *>(s + CODES + (wn * W + i * 32) * BK + at);
       }
-      // (B, A): a lane's accumulator holds groups of 4 consecutive columns of one row of C
+      if constexpr (u.value == 0) {
+        int es = lane * 4;
+        asm("" : "+v"(es));
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < NB; ++i) {
+          ea[d.value & 1][i] = *reinterpret_cast<const uint32_t *>(s + 2 * CODES + (wm * NB + i) * 256 + es);
+          eb[d.value & 1][i] = *reinterpret_cast<const uint32_t *>(s + 2 * CODES + T * 8 + (wn * NB + i) * 256 + es);
+        }
+      }
+      if constexpr (u.value < 3 && PAIR && d.value % 2 == 0) fetch(j + D - 2, (d.value + D - 2) % D, u);
+      if constexpr (u.value < 3 && !(PAIR && d.value % 2)) fetch(j + D - 1, (d.value + D - 1) % D, u);
+      constexpr int e = (u.value == 0 ? d.value + 1 : d.value) & 1;
+      multiply(Const<(u.value + 3) % 4>{}, ea[e], eb[e]);
+      if constexpr (NB == 2) {
 #pragma unroll
-        for (int k = 0; k < NB; ++k) acc[i][k] = mfma_mx4_32<u.value>(fb[k], eb[k], fa[i], ea[i], acc[i][k]);
+        for (int i = 0; i < 4; ++i) {
+          __builtin_amdgcn_sched_group_barrier(SG_MFMA, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(SG_DS_READ, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(SG_VMEM_READ, 1, 0);
+        }
+      }
     });
   };
+  if constexpr (PAIR) {
+    unrolled<D / 2 - 1>([&](auto d) {
+      unrolled<3>([&](auto part) {
+        fetch(2 * d.value, 2 * d.value, part);
+        fetch(2 * d.value + 1, 2 * d.value + 1, part);
+      });
+    });
+  } else {
+    unrolled<D - 1>([&](auto d) { unrolled<3>([&](auto part) { fetch(d.value, d.value, part); }); });
+  }
   // (no branch within a turn of the ring: where ways meet the compiler waits for what either has left under way)
   int j = 0;
-  for (; j + D <= nk; j += D) unrolled<D>([&](auto d) { multiply(j + d.value, d); });
-  last_turn<D>(j, nk, multiply);
+  for (; j + D <= nk; j += D) unrolled<D>([&](auto d) { slab(j + d.value, d); });
+  last_turn<D>(j, nk, slab);
+  {
+    uint32_t sa[NB], sb[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) sa[i] = nk & 1 ? ea[0][i] : ea[1][i], sb[i] = nk & 1 ? eb[0][i] : eb[1][i];
+    multiply(Const<3>{}, sa, sb);
+    // (here, by all lanes, and not where only those with rows to store are left)
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int k = 0; k < NB; ++k) asm volatile("" : "+a"(acc[i][k]));
+  }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the copies of zeros past the end
   const Epilogue ep{p.act, p.slope, false};
 #pragma unroll
@@ -199,8 +260,12 @@ hipError_t launch_mx4_rest(const Mx4Args &a, int64_t tiles, hipStream_t stream) 
   return hipPeekAtLastError();
 }
 
+// Rings of 8 stages where every tile has a CU to itself, of 4 where two share one (us, 8 | 4: 128 x 8192 x 8192, 256 tiles,
+// 18.9 | 20.5; 256 x 8192 x 8192, 512 tiles, 33.5 | 28.5).
 hipError_t launch_mx4_ring(const Mx4Args &p, int tile, hipStream_t stream) {
-  return tile == 128 ? ring_t<128, 4>(p, stream) : ring_t<64, 4>(p, stream);
+  if (tile == 128) return ring_t<128, 4>(p, stream);
+  const int64_t tiles = ((p.M + 63) / 64) * ((p.N + 63) / 64);
+  return p.batch <= 256 && tiles * p.batch <= 256 ? ring_t<64, 8>(p, stream) : ring_t<64, 4>(p, stream);
 }
 
 }  // namespace tsm

@@ -162,11 +162,11 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
   // 64-tiles while there are at most 128 of 128 x 128, those while one round of the CUs does them, then 256-tiles; the
   // first two with direct copies where the operands are aligned, else through registers (us, general 64 | 128 | direct 64 |
   // 128 | 256):
-  //    512 x 4096 x 4096   16.1 |      | 14.8 | 15.8              256 x 8192 x 8192   33.7 |      | 34.5 | 35.2
-  //   1024 x 2048 x 4096   15.8 | 18.9 | 14.3 | 15.9 | 25.2      1024 x 4096 x 4096        | 20.1 | 24.8 | 18.5
-  //   2048 x 2048 x 4096   27.7 | 19.6 | 24.5 | 17.5 | 25.3      2304 x 2048 x 4096   32.8 | 35.6 |      |      | 25.4
-  //   256 x 16384 x 4096   35   | 24.7 |      |      | 29.6      2000 x 2000 x 2001   27   | 17.9
-  // and for up to 64 rows: 64 x 16384 x 8192   25.0 | 35.3 | 24.1 | 33.0.
+  //    512 x 4096 x 4096   16.1 |      | 13.7 | 15.8              256 x 8192 x 8192   33.7 |      | 30.3 | 34.0 | 50
+  //   1024 x 2048 x 4096   15.8 | 18.9 | 13.9 | 16.1 | 25.2      1024 x 2560 x 4096        |      | 21.3 | 16.4 | 25
+  //   2048 x 2048 x 4096   27.7 | 19.6 | 24.4 | 17.9 | 25.5      2048 x 2304 x 4096   32.8 | 35.6 | 32.5 | 29.9 | 25.2
+  //   256 x 16384 x 4096   35   | 24.7 | 32.6 | 22.0 | 29.6      2000 x 2000 x 2001   27   | 17.9
+  // and for up to 64 rows: 64 x 16384 x 8192   25.0 | 35.3 | 22.5 | 33.0.
   const int64_t tiles128 = ((M + 127) / 128) * ((N + 127) / 128), tiles64 = ((M + 63) / 64) * ((N + 63) / 64);
   const int64_t all128 = tiles128 > ((int64_t)1 << 40) / batch ? (int64_t)1 << 40 : tiles128 * batch;
   const bool small = all128 <= 128 || (M <= 64 && tiles64 * 512 <= 0xffffffffLL), direct = mx4_tile_supports(p);
