@@ -42,7 +42,8 @@ def check_weights(w, ids, x, score, renormalize, factor):
 # experts, topk, groups, top_groups, group_best
 LAYOUTS = [(1, 1, 1, 1, 1), (8, 2, 1, 1, 1), (8, 8, 1, 1, 1), (16, 4, 4, 2, 2), (17, 3, 1, 1, 1), (60, 4, 1, 1, 1),
            (60, 6, 12, 5, 2), (64, 8, 8, 3, 1), (64, 64, 1, 1, 1), (66, 5, 33, 20, 2), (128, 8, 64, 9, 2),
-           (130, 10, 1, 1, 1), (160, 6, 8, 3, 1), (256, 8, 8, 4, 2), (256, 8, 1, 1, 1), (256, 33, 4, 3, 2),
+           (130, 10, 1, 1, 1), (160, 6, 8, 3, 1), (160, 6, 8, 3, 2), (6, 2, 3, 2, 2), (45, 7, 9, 4, 2), (100, 8, 4, 2, 2), (33, 8, 3, 2, 1),
+           (500, 8, 4, 2, 2), (256, 8, 8, 4, 2), (256, 8, 1, 1, 1), (256, 33, 4, 3, 2),
            (384, 8, 1, 1, 1), (500, 7, 4, 2, 2), (512, 16, 16, 9, 2), (512, 64, 2, 1, 1)]
 
 
@@ -111,7 +112,7 @@ def test_near_ties(score):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,k,G,top", [(8, 2, 1, 1), (8, 8, 1, 1), (16, 4, 4, 2), (16, 8, 8, 5), (60, 8, 1, 1),
                                        (64, 8, 8, 3), (128, 8, 8, 4), (128, 8, 1, 1), (256, 8, 8, 4), (256, 7, 1, 1),
-                                       (512, 8, 16, 4)])
+                                       (512, 8, 16, 4), (160, 6, 8, 3), (100, 8, 4, 2), (500, 8, 4, 2)])
 @pytest.mark.parametrize("near", [3, 9, 40])
 def test_some_near_ties(E, k, G, top, near, score):
     """Tokens some of whose experts, inside the choice, at its border and past it, and in groups at theirs, have keys

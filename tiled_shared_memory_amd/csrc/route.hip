@@ -6,16 +6,16 @@
 //   groups  the top_groups with the largest sum of their `best` largest keys
 //   weight  factor * s_e, renormalised over the chosen: factor * s_e / sum of their s
 //
-// L lanes hold a token's row, each the experts l V .. l V + V - 1; a wave works on
-// 64 / L tokens.
+// L lanes hold a token's row, each up to V experts that follow each other; a wave works
+// on 64 / L tokens.
 //
 // Up to 8 choices (route8_kernel): each lane sorts its keys, the lanes' lists of 8 are
 // merged pairwise (element i against the partner's 7 - i, then three exchanges), and
 // the k-th of the result is the smallest key that is chosen.  The lanes list the
 // experts that reach it, and up to 8 lanes order those and weigh them: about as much
 // work as two rounds of searching the largest key, which it replaces.
-// More choices, and groups that lanes cannot share out evenly (route_kernel): one
-// after another, the largest key of each lane, of the L lanes, the first lane that
+// More choices, and groups for which the lanes are too few (route_kernel): one after
+// another, the largest key of each lane, of the L lanes, the first lane that
 // holds it.
 //
 // A choice is made by the exact keys.  Keys computed in float32 are off by a
@@ -148,12 +148,12 @@ __device__ __forceinline__ RouteArgs args_again() {
   return *(const RouteArgs *)p;
 }
 
-// A lane's V logits of a token's row, -inf past the last expert.
+// A lane's logits of a token's row, from expert e0: n of its V, -inf behind them.
 template <int FMT, int L, int V>
-__device__ __forceinline__ void load_row(float (&x)[V], const RouteArgs &a, int64_t t, int e0) {
+__device__ __forceinline__ void load_row(float (&x)[V], const RouteArgs &a, int64_t t, int e0, int n) {
   const char *p = (const char *)a.logits + t * a.ld * fmt_bytes(FMT);
   constexpr int N = Vec<FMT>::N;
-  if (V % N == 0 && a.experts == L * V) {  // uniform (gfx950 takes vectors at any alignment of the element)
+  if (V % N == 0 && a.experts == L * V) {  // uniform: n = V (gfx950 takes vectors at any alignment of the element)
 #pragma unroll
     for (int h = 0; h < V / N; ++h) {
       Vec<FMT> v;
@@ -164,7 +164,7 @@ __device__ __forceinline__ void load_row(float (&x)[V], const RouteArgs &a, int6
     return;
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = e0 + i < a.experts ? elem_f32<FMT>(elem_bits<FMT>(p, e0 + i)) : -kInf;
+  for (int i = 0; i < V; ++i) x[i] = i < n ? elem_f32<FMT>(elem_bits<FMT>(p, e0 + i)) : -kInf;
 }
 
 // The largest logit and the sum of exp(x - largest) of a token's row.
@@ -361,18 +361,24 @@ __device__ __forceinline__ void choose_exactly(const RouteArgs &a, const char *r
   wave_sync();
 }
 
-// Place in LDS of expert e's bias: a token's lanes read their i-th ones beside each other.
-template <int L, int V>
-__device__ __forceinline__ int bias_at(int e) {
-  return e % V * L + e / V;
+// An expert of a lane's i-th place, and the place in LDS of its bias: a token's lanes read their i-th ones beside each
+// other.
+struct Pick {
+  int both;  // bias place << 16 | expert
+  __device__ __forceinline__ int expert() const { return both & 0xffff; }
+  __device__ __forceinline__ int place() const { return both >> 16; }
+};
+template <int L>
+__device__ __forceinline__ Pick pick(int e0, int i) {
+  return Pick{(i * L + (int)(threadIdx.x % L)) << 16 | (e0 + i)};
 }
 
 // The order by keys in float64 of a token's experts that may be among the chosen: bits `within` of each lane's, up to L
 // in the token, `before` of them in the lanes before.  All of a wave's lanes come here, also those of tokens that do not
 // ask for it.
-template <int FMT, int L, int V>
+template <int FMT, int L>
 __device__ __forceinline__ void order_exactly(const RouteArgs &a, const char *row, const float *bias, bool asked,
-                                              uint32_t within, int before, int around, int e0, double *keys, int *ids,
+                                              uint32_t within, int before, int around, int e0, double *keys, Pick *ids,
                                               int *chosen, float *logit) {
   const int l = threadIdx.x % L;
   double top = -(double)kInf, sum = 0;
@@ -387,18 +393,19 @@ __device__ __forceinline__ void order_exactly(const RouteArgs &a, const char *ro
     sum = row_sum<L>(sum);
   }
   if (asked)
-    for (; within; within &= within - 1) ids[before++] = e0 + __builtin_ctz(within);
+    for (; within; within &= within - 1) ids[before++] = pick<L>(e0, __builtin_ctz(within));
   wave_sync();
   const bool held = asked && l < around;
-  const int e = held ? ids[l] : 0;
+  const Pick own = held ? ids[l] : Pick{0};
+  const int e = own.expert();
   const float x = elem_f32<FMT>(elem_bits<FMT>(row, e));
   const double d = exp(a.sigmoid ? -(double)x : x - top);
-  const double key = (a.sigmoid ? 1.0 / (1.0 + d) : d / sum) + (double)bias[bias_at<L, V>(e)];
+  const double key = (a.sigmoid ? 1.0 / (1.0 + d) : d / sum) + (double)bias[own.place()];
   if (held) keys[l] = key;
   wave_sync();
   if (held) {
     int rank = 0;
-    for (int j = 0; j < around; ++j) rank += keys[j] > key || (keys[j] == key && ids[j] < e);
+    for (int j = 0; j < around; ++j) rank += keys[j] > key || (keys[j] == key && ids[j].expert() < e);
     if (rank < a.topk) {
       chosen[rank] = e;
       logit[rank] = x;
@@ -530,25 +537,34 @@ __device__ __forceinline__ void largest8(int (&best)[8], const int (&key)[V]) {
 
 struct Choice {
   float key, x, bias;
-  int e;
+  Pick e;
 };
 
 template <int FMT, int L, int V>
 __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
   constexpr int kTokens = kThreads / L;
   __shared__ double keys[4][L * V < 64 ? 64 : L * V];  // of the choice in float64: a wave's
-  __shared__ float bias_of[L * V];         // -inf for NaN; in the order of bias_at
+  __shared__ float bias_of[L * V];         // -inf for NaN; by places
   __shared__ Choice list[kTokens][9];      // (8; the rows of a wave's tokens on different banks)
   __shared__ double near_keys[kTokens][L];
-  __shared__ int near_ids[kTokens][L];
+  __shared__ Pick near_ids[kTokens][L];
   __shared__ int chosen[kTokens][8];
   __shared__ float logit[kTokens][8];
   RouteArgs a = first;
-  const int slot = threadIdx.x / L, l = threadIdx.x % L, e0 = l * V;
+  const int slot = threadIdx.x / L, l = threadIdx.x % L;
+  // Each group's experts on lanes of its own (a power of two): lane l has n from e0.
+  auto first_of = [&](int lane) { return (lane >> a.shift) * a.size + (lane & ((1 << a.shift) - 1)) * a.per; };
+  auto count_of = [&](int lane) {
+    const int in = (lane & ((1 << a.shift) - 1)) * a.per, left = a.experts - first_of(lane);
+    const int n = a.size - in < a.per ? a.size - in : a.per;
+    return n < left ? n : left;  // (0 and less: none)
+  };
+  const int e0 = first_of(l);
   if (a.bias) {
-    for (int i = threadIdx.x; i < a.experts; i += kThreads) {
-      const float b = a.bias[i];
-      bias_of[bias_at<L, V>(i)] = b == b ? b : -kInf;
+    for (int i = threadIdx.x; i < L * V; i += kThreads) {
+      if (i / L >= count_of(i % L)) continue;
+      const float b = a.bias[first_of(i % L) + i / L];
+      bias_of[i] = b == b ? b : -kInf;
     }
     __syncthreads();
   }
@@ -562,7 +578,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
     float top = 0.f, sum = 1.f, by = 1.f, error;
     {
       float x[V];
-      load_row<FMT, L>(x, a, held ? t : a.tokens - 1, e0);
+      load_row<FMT, L>(x, a, held ? t : a.tokens - 1, e0, count_of(l));
       // a NaN is above +inf or below -inf in this order
       int hi, lo;
 #pragma unroll
@@ -593,7 +609,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
             b2 = __builtin_amdgcn_fmed3f(b1, b2, g[i]);
             b1 = g[i] > b1 ? g[i] : b1;
           }
-          const int lanes = a.experts / a.groups / V;  // of a group: a power of two
+          const int lanes = 1 << a.shift;  // of a group
           steps<log2_of(L)>([&](auto s) {
             if ((1 << s.value) < lanes) {
               const float o1 = across<s.value>(b1), o2 = across<s.value>(b2);
@@ -624,7 +640,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
         int b1 = key[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) b1 = key[i] > b1 ? key[i] : b1;
-        const int lanes = a.experts / a.groups / V;
+        const int lanes = 1 << a.shift;
         steps<log2_of(L)>([&](auto s) {
           if ((1 << s.value) < lanes) {
             const int o = across<s.value>(b1);
@@ -682,19 +698,19 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
       upto = row_scan<L>(count);
     }
     const uint32_t taken = mine;
-    for (int at = upto - count; mine; mine &= mine - 1) list[slot][at++].e = e0 + __builtin_ctz(mine);
+    for (int at = upto - count; mine; mine &= mine - 1) list[slot][at++].e = pick<L>(e0, __builtin_ctz(mine));
     wave_sync();
     const int n = total < a.topk ? total : a.topk;
 
     // lane j orders the j-th of the list
-    Choice c{-kInf, 0.f, 0.f, -1};
+    Choice c{-kInf, 0.f, 0.f, {0}};
     const char *const row = (const char *)a.logits + (held ? t : a.tokens - 1) * a.ld * fmt_bytes(FMT);
     if (l < n) {
       c.e = list[slot][l].e;
-      c.x = elem_f32<FMT>(elem_bits<FMT>(row, c.e));
+      c.x = elem_f32<FMT>(elem_bits<FMT>(row, c.e.expert()));
       c.key = c.x;
       if (scored) {
-        c.bias = bias_of[bias_at<L, V>(c.e)];
+        c.bias = bias_of[c.e.place()];
         c.key = score_of(a.sigmoid, c.x, top, by) + c.bias;
       }
       list[slot][l] = c;
@@ -707,12 +723,12 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
     for (int j = 0; j < a.topk; ++j) {
       const Choice o = list[slot][j];
       const bool other = j < n && j != l;
-      rank += other && (o.key > c.key || (o.key == c.key && o.e < c.e));
+      rank += other && (o.key > c.key || (o.key == c.key && o.e.expert() < c.e.expert()));
       // (equal logits and biases make equal keys, whatever they round to)
       close |= other && fabsf(o.key - c.key) <= tolerance && (o.x != c.x || o.bias != c.bias);
     }
     if (l < n) {
-      chosen[slot][rank] = c.e;
+      chosen[slot][rank] = c.e.expert();
       logit[slot][rank] = c.x;
     }
     if (scored) {
@@ -730,14 +746,14 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
         for (int j = 0; j < n; ++j)
           if (ordered(list[slot][j].key) == least) lx = list[slot][j].x, lb = list[slot][j].bias;
         for (uint32_t rest = within & ~taken; rest; rest &= rest - 1) {
-          const int e = e0 + __builtin_ctz(rest);
-          unclear |= elem_f32<FMT>(elem_bits<FMT>(row, e)) != lx || bias_of[bias_at<L, V>(e)] != lb;
+          const int i = __builtin_ctz(rest);
+          unclear |= elem_f32<FMT>(elem_bits<FMT>(row, e0 + i)) != lx || bias_of[i * L + l] != lb;
         }
       }
       unclear = row_ballot<L>(unclear) != 0;
       open |= unclear && around > L;
       if (__ballot(unclear && !open))
-        order_exactly<FMT, L, V>(a, row, bias_of, unclear && around <= L, within, row_scan<L>(own) - own, around, e0,
+        order_exactly<FMT, L>(a, row, bias_of, unclear && around <= L, within, row_scan<L>(own) - own, around, e0,
                               near_keys[slot], near_ids[slot], chosen[slot], logit[slot]);
     }
     wave_sync();
@@ -761,7 +777,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs first) {
   const int64_t t = a.t0 + (int64_t)blockIdx.x * kTokens + slot;
   const bool held = t < a.tokens;
   float x[V], bias[V] = {}, top = 0.f, sum = 1.f;
-  load_row<FMT, L>(x, a, held ? t : a.tokens - 1, e0);
+  load_row<FMT, L>(x, a, held ? t : a.tokens - 1, e0, a.experts - e0);
   if (a.bias) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -912,11 +928,22 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteArgs a) {
   }
 }
 
-// Whether lanes of V experts share out the groups evenly, a power of two lanes each.
-bool even_groups(const RouteArgs &a, int V) {
-  if (a.top_groups == a.groups) return true;
-  const int size = a.experts / a.groups, lanes = size / V;
-  return size % V == 0 && (lanes & (lanes - 1)) == 0;
+// Places a row on L lanes of up to V experts, where groups are chosen each on lanes of its own, a power of two of them;
+// false: they do not hold it.
+bool place(RouteArgs &a, int L, int V) {
+  if (a.experts > L * V) return false;
+  int lanes = L;
+  a.size = a.experts;
+  a.per = V;
+  if (a.top_groups < a.groups) {
+    while (lanes > 0 && L / lanes < a.groups) lanes /= 2;
+    if (lanes == 0) return false;
+    a.size = a.experts / a.groups;
+    a.per = (a.size + lanes - 1) / lanes;
+  }
+  a.shift = 0;
+  while (1 << a.shift < lanes) ++a.shift;
+  return a.per <= V;
 }
 
 // f(arguments, workgroups) over launches of 2^23 workgroups at most (work-items below 2^32).
@@ -959,17 +986,18 @@ hipError_t backward(const RouteArgs &base, hipStream_t stream) {
 
 template <int FMT>
 hipError_t route_fmt(const RouteArgs &a, hipStream_t stream) {
-  const int E = a.experts, V = E <= 8 ? 1 : E <= 16 ? 2 : E <= 64 ? 8 : 16;
+  const int E = a.experts;
   // The fewest lanes that hold a row in 16 experts each: what is done for each lane's list is done for fewer (65536 tokens,
   // us, 16 | 8 lanes: 8 experts 11.2 | 6.5, 64 14.8 | 9.7, 128 16.9 | 13.0).  Of 32 experts a lane's own work takes over
   // (16 | 8 lanes of 256 experts: 65536 tokens 24.3 | 20.9, with a bias 34.8 | 37; 64 tokens in groups 7.1 | 9.6).
-  if (a.topk <= 8 && even_groups(a, V)) {
-    if (E <= 8) return route8<FMT, 8, 1>(a, stream);
-    if (E <= 16) return route8<FMT, 8, 2>(a, stream);
-    if (E <= 64) return route8<FMT, 8, 8>(a, stream);
-    if (E <= 128) return route8<FMT, 8, 16>(a, stream);
-    if (E <= 256) return route8<FMT, 16, 16>(a, stream);
-    return route8<FMT, 32, 16>(a, stream);
+  if (a.topk <= 8) {
+    RouteArgs b = a;
+    if (place(b, 8, 1)) return route8<FMT, 8, 1>(b, stream);
+    if (place(b, 8, 2)) return route8<FMT, 8, 2>(b, stream);
+    if (place(b, 8, 8)) return route8<FMT, 8, 8>(b, stream);
+    if (place(b, 8, 16)) return route8<FMT, 8, 16>(b, stream);
+    if (place(b, 16, 16)) return route8<FMT, 16, 16>(b, stream);
+    if (place(b, 32, 16)) return route8<FMT, 32, 16>(b, stream);
   }
   if (E <= 16) return route_any<FMT, 16, 1>(a, stream);
   if (E <= 64) return route_any<FMT, 16, 4>(a, stream);

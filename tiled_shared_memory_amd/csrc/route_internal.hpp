@@ -25,6 +25,7 @@ struct RouteArgs {
   int32_t sigmoid, renormalize;
   float factor;
   int64_t t0;          // first token of this launch
+  int32_t size, shift, per;  // route8_kernel: 2^shift lanes hold `size` experts, `per` each
 };
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
 hipError_t launch_route_backward(const RouteArgs &a, hipStream_t stream);
