@@ -280,6 +280,41 @@ def test_middle_tiles(monkeypatch, T, M, N, K, pad, out):
         assert torch.equal(c[z, :m], plain[z, :m]) and (c[z, m:] == 55.0).all()
 
 
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K,pq,ps", [(1, 1, 1, 0, 0), (3, 70, 2, 1, 1), (65, 5, 31, 0, 3), (64, 64, 32, 2, 0),
+                                         (10, 129, 33, 3, 2), (130, 7, 255, 0, 0), (70, 200, 256, 1, 1),
+                                         (129, 65, 257, 2, 3), (33, 300, 511, 5, 0), (200, 100, 513, 0, 1),
+                                         (257, 130, 769, 1, 2), (64, 128, 1000, 0, 0), (66, 67, 1023, 3, 1),
+                                         (100, 31, 1281, 2, 2), (140, 260, 2047, 1, 0), (1, 500, 4097, 0, 3),
+                                         (300, 33, 3333, 7, 5), (128, 64, 8190, 0, 0), (40, 40, 10001, 1, 1)])
+@pytest.mark.parametrize("T", [64, 128])
+def test_odd_rows(monkeypatch, T, M, N, K, pq, ps, out):
+    """The general kernel, forced: rows at any address, K that ends anywhere in a slab, a batch and grouped counts;
+    scales of NaN, and codes, behind the rows and in an odd K's last half byte."""
+    import torch
+
+    monkeypatch.setenv("TSM_GEMM_KERNEL", f"mx4_block_{T}x{T}x256")
+    g = gen(M + N * 3 + K + T)
+    dt = dtypes()[out]
+    say(f"[gpu] mx4 odd rows {T} {M}x{N}x{K}+{pq},{ps} {out}")
+    a, sa, va = operand(M, K, pq, ps, g)
+    b, sb, vb = operand(N, K, pq + 1, ps + 2, g, 112, 124)
+    buf = torch.full((M + 1, N + 3), 77.0, dtype=dt, device="cuda")
+    tsm.matmul_mx4(a, sa, b.t(), sb, columns=K, out=buf[:M, :N], activation="leaky_relu", slope=0.25)
+    check_product(buf[:M, :N], *ref.product(va, vb, "leaky_relu", 0.25), K, out, 2.0 ** -24)
+    assert (buf[M] == 77.0).all() and (buf[:, N:] == 77.0).all()
+    a3, sa3, va3 = (t.reshape(5, M, -1) for t in operand(5 * M, K, 0, 0, g))
+    b3, sb3, vb3 = (t.reshape(5, N, -1) for t in operand(5 * N, K, 0, 0, g, 112, 124))
+    plain = tsm.matmul_mx4(a3, sa3, b3.transpose(1, 2), sb3, columns=K, out_dtype=dt)
+    for z in range(5):
+        check_product(plain[z], *ref.product(va3[z], vb3[z]), K, out)
+    rows = torch.tensor([M, 0, M // 2, M + 5, -1], dtype=torch.int32, device="cuda")
+    c = torch.full((5, M, N), 55.0, dtype=dt, device="cuda")
+    tsm.matmul_mx4(a3, sa3, b3.transpose(1, 2), sb3, columns=K, rows=rows, out=c)
+    for z, m in enumerate([M, 0, M // 2, M, 0]):
+        assert torch.equal(c[z, :m], plain[z, :m]) and (c[z, m:] == 55.0).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(4352, 4096, 256), (4100, 4360, 512), (2200, 2304, 768)])
 def test_tiles_past_whole_rounds(M, N, K):
     """A few 256-tiles more than one per CU (272, 306), or fewer than a round: the two launches together write every
