@@ -489,10 +489,6 @@ def _uint8():
     return _UINT8[0]
 
 
-def _group_stride(t, groups):
-    return t.stride(0) if t.dim() == 3 and groups > 1 else 0
-
-
 def _group_rows(rows, groups):
     if rows is not None:
         _wants("rows", rows, (TSM_I32,), (groups,))
@@ -507,28 +503,34 @@ def quantize_mx4(x, *, rows=None, out=None, scale=None, stream=None):
     With ``rows`` (int32, one count per matrix of a 3-D ``x``, on the GPU) only the first rows of each are read and
     written.  A block with a NaN or an infinity becomes one of NaN.
     """
-    if x.dim() not in (2, 3):
+    shape, f = x.shape, (_FORMATS or _formats()).get(x.dtype)
+    d = len(shape)
+    if d not in (2, 3):
         _bad("x must be 2-D or 3-D")
-    f = _wants("x", x, _FLOATS)
-    R, C = x.shape[-2], x.shape[-1]
-    G = x.shape[0] if x.dim() == 3 else 1
-    q_shape, s_shape = (*x.shape[:-1], (C + 1) // 2), (*x.shape[:-1], (C + 31) // 32)
+    if f not in _FLOATS:
+        _bad(f"x has dtype {x.dtype}")
+    R, C, G = shape[-2], shape[-1], shape[0] if d == 3 else 1
+    q_shape, s_shape = (R, (C + 1) // 2), (R, (C + 31) // 32)
+    if d == 3:
+        q_shape, s_shape = (G, *q_shape), (G, *s_shape)
     if out is None:
         out = _new(x, q_shape, "uint8", stream)
     if scale is None:
         scale = _new(x, s_shape, "uint8", stream)
     codes, scales = _u8_rows("out", out, q_shape, G), _u8_rows("scale", scale, s_shape, G)
-    _group_rows(rows, G)
+    if rows is not None:
+        _group_rows(rows, G)
+    st = x.stride()
     layout, ldx = TSM_ROW, max(1, C)
-    if x.numel():
-        if C == 1 or x.stride(-1) == 1:
-            ldx = x.stride(-2) if R > 1 else max(1, C)
-        elif R == 1 or x.stride(-2) == 1:
-            layout, ldx = TSM_COL, x.stride(-1)
-        else:
-            _bad("x must be row- or column-major in its last two dims")
+    if C == 1 or st[-1] == 1:
+        if R > 1 and C:
+            ldx = st[-2]
+    elif R == 1 or st[-2] == 1:
+        layout, ldx = TSM_COL, st[-1]
+    elif x.numel():
+        _bad("x must be row- or column-major in its last two dims")
     _launch("mx4_quantize", stream, (x, out, scale, rows),
-            (R, C, x.data_ptr(), ldx, layout, _group_stride(x, G), f, *codes, *scales, _at(rows), G))
+            (R, C, x.data_ptr(), ldx, layout, st[0] if G > 1 else 0, f, *codes, *scales, _at(rows), G))
     return out, scale
 
 
@@ -539,19 +541,24 @@ def dequantize_mx4(codes, scales, *, columns=None, rows=None, out=None, out_dtyp
     ``columns`` elements a row: where neither it nor ``out`` says, two per byte of codes.  ``rows`` as for
     ``quantize_mx4``.
     """
-    if codes.dim() not in (2, 3):
+    held = codes.shape
+    d = len(held)
+    if d not in (2, 3):
         _bad("codes must be 2-D or 3-D")
-    C = columns if columns is not None else out.shape[-1] if out is not None else 2 * codes.shape[-1]
-    shape = (*codes.shape[:-1], C)
-    G = codes.shape[0] if codes.dim() == 3 else 1
+    C = columns if columns is not None else out.shape[-1] if out is not None else 2 * held[-1]
+    R, G = held[-2], held[0] if d == 3 else 1
+    shape, q_shape, s_shape = (R, C), (R, (C + 1) // 2), (R, (C + 31) // 32)
+    if d == 3:
+        shape, q_shape, s_shape = (G, *shape), (G, *q_shape), (G, *s_shape)
     if out is None:
         out = _new(codes, shape, out_dtype or "float32", stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         _bad(f"out has dtype {out.dtype}, out_dtype is {out_dtype}")
-    q, e = _u8_rows("codes", codes, (*shape[:-1], (C + 1) // 2), G), _u8_rows("scales", scales, (*shape[:-1], (C + 31) // 32), G)
+    q, e = _u8_rows("codes", codes, q_shape, G), _u8_rows("scales", scales, s_shape, G)
     y, ldy, sy, f = _float_rows("out", out, shape, G)
-    _group_rows(rows, G)
-    _launch("mx4_dequantize", stream, (codes, scales, out, rows), (shape[-2], C, *q, *e, y, ldy, sy, f, _at(rows), G))
+    if rows is not None:
+        _group_rows(rows, G)
+    _launch("mx4_dequantize", stream, (codes, scales, out, rows), (R, C, *q, *e, y, ldy, sy, f, _at(rows), G))
     return out
 
 
@@ -580,17 +587,18 @@ def matmul_mx4(a, scale_a, b, scale_b, *, columns=None, rows=None, out=None, out
     floats = scale_a is None
     K = sha[-1] if floats else 2 * sha[-1] if columns is None else columns
     M, KB, NB, N = sha[-2], (K + 1) // 2, (K + 31) // 32, shb[-1]
+    ba, bb = (sha[0] if da == 3 else 1), (shb[0] if db == 3 else 1)
     if floats:
-        x, ldx, sx, fx = _float_rows("a", a, sha, sha[0])
+        x, ldx, sx, fx = _float_rows("a", a, sha, ba)
         if columns is not None and K != columns:
             _bad(f"columns is {columns}, a has {K}")
     else:
-        codes = (*_u8_rows("a", a, (*sha[:-1], KB), sha[0]), *_u8_rows("scale_a", scale_a, (*sha[:-1], NB), sha[0]))
+        codes = (*_u8_rows("a", a, (ba, M, KB) if da == 3 else (M, KB), ba),
+                 *_u8_rows("scale_a", scale_a, (ba, M, NB) if da == 3 else (M, NB), ba))
     if b.dtype is not _uint8():
         _bad(f"b has dtype {b.dtype}, torch.uint8 wanted")
     if shb[-2] != KB:
         _bad(f"inner sizes differ: {KB} bytes of codes vs {shb[-2]}")
-    ba, bb = (sha[0] if da == 3 else 1), (shb[0] if db == 3 else 1)
     if ba != bb and ba != 1 and bb != 1:
         _bad(f"batch sizes differ: {ba} vs {bb}")
     batch = ba if bb == 1 else bb
