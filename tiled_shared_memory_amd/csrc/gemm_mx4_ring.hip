@@ -46,7 +46,8 @@ __device__ __forceinline__ void ring(const Mx4Args &p) {
   constexpr int L = T / 32;              // wave-loads (1 KiB: 8 rows) per wave, operand and slab
   constexpr int S = T / 64;              // wave-loads of scales (256 bytes: 32 rows) per wave and slab
   constexpr int N = 2 * L + S;
-  // slabs are requested two at a time (not by tiles that come after whole rounds: 4112 x 4096 x 4096 48 us, was 46)
+  // slabs are requested two at a time (not by tiles that come after whole rounds: 4112 x 4096 x 4096 48 us,
+  // one at a time 46)
   constexpr bool PAIR = T == 64 && !REST;
   constexpr int CODES = T * BK, BYTES = 2 * CODES + 2 * T * 8;  // of an operand, of a stage
   // an array each: a read waits for the copies into its array, as the compiler sees to it
