@@ -1,0 +1,42 @@
+"""The router's choice on the GPU where float32 keys do not decide it, against float64."""
+
+import math
+
+import pytest
+
+import mx4_ref as ref
+from gpu_util import say
+from mx4_ref import dtypes
+
+import tiled_shared_memory_amd as tsm
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    import torch
+
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(5, 4), (8, 8), (33, 6), (60, 8), (64, 5), (100, 8), (129, 7), (255, 8), (300, 8), (500, 3),
+                                 (60, 12), (500, 20)])
+@pytest.mark.parametrize("fmt", ["f32", "bf16"])
+def test_biases_of_the_lowest_value(E, k, score, fmt):
+    """Experts masked by a bias of float32's lowest value, fewer left than are chosen: the masked ones follow, the lowest
+    index first, and none that has a logit of -inf, nor a number past the last expert."""
+    import torch
+
+    g = gen(E + k)
+    x = torch.randn((67, E), generator=g, device="cuda").to(dtypes()[fmt])
+    x[5, : E // 2] = -math.inf
+    x[66, 1] = -math.inf
+    for left in (0, 1, k - 1, k):
+        bias = torch.full((E,), torch.finfo(torch.float32).min, device="cuda")
+        at = torch.randperm(E, generator=g, device="cuda")[:left]
+        bias[at] = 0.1 * torch.randn(left, generator=g, device="cuda")
+        say(f"[gpu] route biases of the lowest value {E} {k} {score} {fmt} {left}")
+        ids, w = tsm.route_tokens(x, k, score=score, bias=bias)
+        assert torch.equal(ids.long(), ref.choose(x.double(), k, score, bias))
+        assert torch.isfinite(w).all()

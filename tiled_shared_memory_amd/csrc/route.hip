@@ -33,6 +33,7 @@
 // The gradient of the same, 18.5 us, moves its 113 MB at 6.1 TB/s.
 #include "elems.hpp"
 #include "route_internal.hpp"
+#include "route_keys.hpp"
 
 namespace tsm {
 namespace {
@@ -50,8 +51,7 @@ constexpr float kInf = __builtin_inff();
 __device__ __forceinline__ float score_error(bool sigmoid, float largest) {
   return sigmoid ? 0x1p-21f : 0x1p-18f * largest;
 }
-// Two keys, and two groups' sums, that may be in the other order.
-__device__ __forceinline__ float key_error(float error, float key) { return 2 * error + 0x1p-22f * fabsf(key); }
+// Two groups' sums that may be in the other order.
 __device__ __forceinline__ float group_error(float error, float sum) { return 4 * error + 0x1p-21f * fabsf(sum); }
 
 // ---- lanes of a token ----
@@ -480,14 +480,6 @@ __device__ __forceinline__ void weigh(const RouteArgs &a, float top, float sum, 
 }
 
 // ---- up to 8 choices ----
-// Floats in the order of their values as whole numbers (-0 as 0), and back.
-__device__ __forceinline__ int ordered(float f) {
-  const int b = __builtin_bit_cast(int, f + 0.f);
-  return b ^ (b >> 31 & 0x7fffffff);
-}
-__device__ __forceinline__ float of_ordered(int i) { return __builtin_bit_cast(float, i ^ (i >> 31 & 0x7fffffff)); }
-constexpr int kNone = -0x7f800001;  // -inf
-
 __device__ __forceinline__ void exchange(int &a, int &b) {  // the larger to a
   const int m = a > b ? a : b;
   b = a > b ? b : a;
@@ -733,8 +725,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
     }
     if (scored) {
       // those that are not chosen but as near to the last chosen one as keys may be off
-      const float f = of_ordered(least);
-      const int near = all ? least : ordered(f - key_error(error, f));
+      const int near = all ? least : near_limit(least, error);
       uint32_t within = 0;
 #pragma unroll
       for (int i = V - 1; i >= 0; --i) within = within + within + (key[i] >= near);

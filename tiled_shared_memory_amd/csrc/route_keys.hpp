@@ -1,0 +1,28 @@
+// What the expert router decides from float32 keys, and what it leaves to float64: plain arithmetic, for the kernels and
+// for programs on the host.
+#pragma once
+
+#include <stdint.h>
+
+namespace tsm {
+
+// Floats in the order of their values as whole numbers (-0 as 0), and back.
+constexpr int ordered(float f) {
+  const int b = __builtin_bit_cast(int, f + 0.f);
+  return b ^ (b >> 31 & 0x7fffffff);
+}
+constexpr float of_ordered(int i) { return __builtin_bit_cast(float, i ^ (i >> 31 & 0x7fffffff)); }
+constexpr int kNone = -0x7f800001;  // -inf: the key of what may not be chosen, and of places without an expert
+
+// How far two float32 keys may lie apart and be in the other order, where a score is off by `error` (score_error).
+constexpr float key_error(float error, float key) { return 2 * error + 0x1p-22f * __builtin_fabsf(key); }
+
+// The least key that may be as large as the smallest chosen one: that one at most, and above kNone, since places without
+// an expert hold it (from a key of float32's lowest value the difference is -inf, from an infinite one NaN).
+constexpr int near_limit(int least, float error) {
+  const float f = of_ordered(least);
+  const int near = ordered(f - key_error(error, f));
+  return near > least ? least : near > kNone ? near : kNone + 1;
+}
+
+}  // namespace tsm
