@@ -40,3 +40,26 @@ def test_biases_of_the_lowest_value(E, k, score, fmt):
         ids, w = tsm.route_tokens(x, k, score=score, bias=bias)
         assert torch.equal(ids.long(), ref.choose(x.double(), k, score, bias))
         assert torch.isfinite(w).all()
+
+
+@pytest.mark.parametrize("E,k,G,top,nbest", [(480, 12, 2, 1, 2), (480, 9, 2, 1, 1), (510, 16, 2, 1, 1), (390, 64, 2, 1, 2),
+                                             (504, 8, 3, 1, 2), (453, 4, 3, 2, 2), (483, 20, 3, 2, 1), (511, 6, 7, 3, 2),
+                                             (512, 9, 2, 1, 2), (495, 5, 33, 17, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "bias"])
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+def test_the_last_expert_of_large_groups(E, k, G, top, nbest, score, biased, fmt):
+    """The first and the last expert of every group in its turn the best of a token."""
+    import torch
+
+    g = gen(E + k)
+    T = 8 * G
+    x = torch.randn((T, E), generator=g, device="cuda")
+    t, n = torch.arange(T, device="cuda"), E // G
+    x[t, t % G * n + t // G % 2 * (n - 1)] += 9
+    x[:, E - 1] += 4 * (t % 3 == 0)
+    x = x.to(dtypes()[fmt])
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda") if biased else None
+    say(f"[gpu] route last experts {E} {k} {G} {top} {nbest} {score} {biased} {fmt}")
+    ids, _ = tsm.route_tokens(x, k, score=score, bias=bias, groups=G, top_groups=top, group_best=nbest)
+    assert torch.equal(ids.long(), ref.choose(x.double(), k, score, bias, G, top, nbest))

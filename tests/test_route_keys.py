@@ -15,6 +15,7 @@ extern "C" {
 int c_none() { return tsm::kNone; }
 int c_ordered(float f) { return tsm::ordered(f); }
 int c_near_limit(int least, float error) { return tsm::near_limit(least, error); }
+int c_group_of(int e, int size) { return (int)tsm::group_of(e, tsm::group_magic(size)); }
 }
 """
 
@@ -42,3 +43,9 @@ def test_near_keys_are_keys_of_experts(keys):
             near = keys.c_near_limit(least, error)
             assert keys.c_none() < near <= least, (key, error)
     assert keys.c_near_limit(keys.c_ordered(1.0), 0.0) == keys.c_ordered(1 - 2.0 ** -22)
+
+
+def test_the_group_of_every_expert(keys):
+    """Of every layout of up to 512 experts."""
+    wrong = [(size, e) for size in range(1, 513) for e in range(512) if keys.c_group_of(e, size) != e // size]
+    assert not wrong, f"{len(wrong)}: {wrong[:8]}"

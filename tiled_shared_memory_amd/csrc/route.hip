@@ -265,10 +265,10 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const float (&x)[V], 
   }
   if (grouped) {
     const uint64_t kept = best_groups<L>(a, keys, sums ? error : 0.f, &open);
-    const uint32_t size = a.experts / a.groups, magic = (65536u + size - 1) / size;  // e / size for e < 512
+    const uint32_t magic = group_magic(a.experts / a.groups);
 #pragma unroll
     for (int i = 0; i < V; ++i)  // (past the last expert any: no key)
-      if (!((kept >> (((uint32_t)(e0 + i) * magic >> 16) & 63)) & 1)) key[i] = -kInf;
+      if (!((kept >> (group_of(e0 + i, magic) & 63)) & 1)) key[i] = -kInf;
   }
   float last = 0.f;
   const int rounds = a.topk + (scored ? 1 : 0);

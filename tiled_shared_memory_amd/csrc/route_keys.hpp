@@ -25,4 +25,9 @@ constexpr int near_limit(int least, float error) {
   return near > least ? least : near > kNone ? near : kNone + 1;
 }
 
+// e / size of an expert e < 512, by a product with group_magic(size).  Exact: size * magic passes 2^20 by less than size,
+// and e times that stays below 2^20.
+constexpr uint32_t group_magic(uint32_t size) { return ((1u << 20) + size - 1) / size; }
+constexpr uint32_t group_of(uint32_t e, uint32_t magic) { return e * magic >> 20; }
+
 }  // namespace tsm
