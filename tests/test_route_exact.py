@@ -63,3 +63,29 @@ def test_the_last_expert_of_large_groups(E, k, G, top, nbest, score, biased, fmt
     say(f"[gpu] route last experts {E} {k} {G} {top} {nbest} {score} {biased} {fmt}")
     ids, _ = tsm.route_tokens(x, k, score=score, bias=bias, groups=G, top_groups=top, group_best=nbest)
     assert torch.equal(ids.long(), ref.choose(x.double(), k, score, bias, G, top, nbest))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [1.0, 16.0, 1000.0, 30000.0])
+@pytest.mark.parametrize("E,k,G,top", [(256, 8, 8, 3), (160, 6, 8, 4), (60, 4, 12, 5), (512, 8, 16, 7), (256, 16, 8, 3),
+                                       (240, 12, 6, 2), (512, 10, 64, 20)])
+def test_groups_whose_biases_cancel(E, k, G, top, size, score):
+    """Groups of one expert with a large bias and one with as large a one below zero: their sums are as near as those
+    biases' roundings leave them, far nearer than the keys' own."""
+    import torch
+
+    g = gen(E + G)
+    T, n = 500, E // G
+    for turn in range(4):
+        x = torch.randn((1, E), generator=g, device="cuda")
+        s = ref.scores(x.double(), score)[0].view(G, n)
+        bias = torch.full((G, n), -8.0 * size, device="cuda")
+        bias[:, 0] = size * (1 + torch.rand(G, generator=g, device="cuda"))
+        bias[:, 1] = -(bias[:, 0].double() + s[:, 0] + s[:, 1]).float()
+        bias = bias[:, torch.randperm(n, generator=g, device="cuda")].reshape(E)
+        step = min(1.0, size * 2.0 ** -22 * (E if score == "softmax" else 4))  # moves a score by a rounding of its key
+        x = x + step * torch.randn((T, E), generator=g, device="cuda")
+        say(f"[gpu] route cancelling biases {E} {k} {G} {size} {score}")
+        ids, _ = tsm.route_tokens(x, k, score=score, bias=bias, groups=G, top_groups=top, group_best=2)
+        want = ref.choose(x.double(), k, score, bias, G, top, 2)
+        assert torch.equal(ids.long(), want), f"{int((ids.long() != want).any(1).sum())} tokens"

@@ -15,6 +15,10 @@ extern "C" {
 int c_none() { return tsm::kNone; }
 int c_ordered(float f) { return tsm::ordered(f); }
 int c_near_limit(int least, float error) { return tsm::near_limit(least, error); }
+int c_near_groups(float error, float a1, float a2, float b1, float b2) {
+  return tsm::near_sums(b1 + b2, a1 + a2, tsm::group_tolerance(error, a1, a2)) ||
+         tsm::near_sums(a1 + a2, b1 + b2, tsm::group_tolerance(error, b1, b2));
+}
 int c_group_of(int e, int size) { return (int)tsm::group_of(e, tsm::group_magic(size)); }
 }
 """
@@ -29,6 +33,7 @@ def keys(tmp_path_factory):
                    check=True)
     lib = ctypes.CDLL(str(d / "k.so"))
     lib.c_ordered.argtypes = [ctypes.c_float]
+    lib.c_near_groups.argtypes = [ctypes.c_float] * 5
     lib.c_near_limit.argtypes = [ctypes.c_int, ctypes.c_float]
     return lib
 
@@ -49,3 +54,27 @@ def test_the_group_of_every_expert(keys):
     """Of every layout of up to 512 experts."""
     wrong = [(size, e) for size in range(1, 513) for e in range(512) if keys.c_group_of(e, size) != e // size]
     assert not wrong, f"{len(wrong)}: {wrong[:8]}"
+
+
+@pytest.mark.parametrize("size", [0.0, 0.1, 16.0, 1000.0, 1e6, 1e30])
+@pytest.mark.parametrize("error", [2.0 ** -27, 2.0 ** -21])
+def test_groups_in_the_other_order_are_near(keys, size, error):
+    """Two groups' sums of two keys, biases of either sign that all but cancel: where the exact sums are not in the order of
+    the float32 ones, one of the two groups finds the other near."""
+    rng = np.random.default_rng(int(size) + 3)
+    other = 0
+    for _ in range(4000):
+        s = rng.random((2, 2)) * 2.0 ** -8  # exact scores, and float32 ones off by less than `error`
+        s32 = (s + (rng.random((2, 2)) - 0.5) * 1.9 * error).astype(np.float32)
+        b = np.zeros((2, 2), np.float32)
+        b[:, 0] = size * (1 + rng.random(2))
+        b[:, 1] = -(b[:, 0].astype(np.float64) + s.sum(1))  # (the sums are what this rounding leaves, and a little)
+        b[1, 1] = np.float32(b[1, 1] + (rng.random() - 0.5) * 2.0 ** -23)
+        k32 = s32 + b
+        exact, got = (s + b.astype(np.float64)).sum(1), k32[:, 0] + k32[:, 1]
+        assert k32.dtype == got.dtype == np.float32
+        if np.sign(exact[1] - exact[0]) != np.sign(got[1] - got[0]):
+            other += 1
+            assert keys.c_near_groups(error, *map(float, k32.ravel())), (s, b)
+    # (without biases the exact sums are too far apart for it; at 1e30 float64 too holds nothing of the scores)
+    assert other > 20 or size in (0.0, 1e30)

@@ -51,8 +51,6 @@ constexpr float kInf = __builtin_inff();
 __device__ __forceinline__ float score_error(bool sigmoid, float largest) {
   return sigmoid ? 0x1p-21f : 0x1p-18f * largest;
 }
-// Two groups' sums that may be in the other order.
-__device__ __forceinline__ float group_error(float error, float sum) { return 4 * error + 0x1p-21f * fabsf(sum); }
 
 // ---- lanes of a token ----
 template <int N>
@@ -194,12 +192,14 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, T *keys, T e
   const T none = -(T)kInf;
   constexpr int P = (RouteInfo::kMaxGroups + L - 1) / L;
   T of[P];
+  float tolerance[P];
   wave_sync();
   // lane l takes groups l, l + L, ...: their largest keys, from a start of its own (no two lanes on one bank)
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int g = l + p * L;
     of[p] = none;
+    tolerance[p] = 0.f;
     if (g >= a.groups) continue;
     T b1 = none, b2 = none;
     int at = g % size;
@@ -210,7 +210,9 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, T *keys, T e
       b2 = k > b1 ? b1 : (k > b2 ? k : b2);
       b1 = k > b1 ? k : b1;
     }
-    of[p] = a.best > 1 && b2 > none ? b1 + b2 : b1;
+    if (a.best == 1 || !(b2 > none)) b2 = 0;
+    of[p] = b1 + b2;
+    tolerance[p] = group_tolerance((float)error, (float)b1, (float)b2);
   }
   wave_sync();
 #pragma unroll
@@ -226,10 +228,7 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, T *keys, T e
     for (int o = 0; o < a.groups; ++o) {
       const T k = keys[o];
       before += k > of[p] || (k == of[p] && o < g);
-      if (error > 0 && g < a.groups && o != g) {
-        const T d = k > of[p] ? k - of[p] : of[p] - k;
-        *open |= d <= group_error((float)error, (float)k);
-      }
+      if (error > 0 && g < a.groups && o != g) *open |= near_sums((float)k, (float)of[p], tolerance[p]);
     }
     kept |= row_ballot<L>(g < a.groups && before < a.top_groups && of[p] > none) << (p * L % 64);
   }
@@ -610,18 +609,20 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
               b2 = least > rest ? least : rest;
             }
           });
-          if (a.best > 1 && b2 > -kInf) b1 += b2;
+          if (a.best == 1 || !(b2 > -kInf)) b2 = 0.f;
+          const float tolerance = group_tolerance(error, b1, b2);
+          b1 += b2;
           int before = 0;
           bool close = false;
           around_row<L>(b1, lanes, [&](float o, int r) {  // the other groups'
             before += o > b1 || (o == b1 && l >= r);
-            close |= fabsf(o - b1) <= group_error(error, o);
+            close |= near_sums(o, b1, tolerance);
           });
           if (__ballot(close)) {  // it matters between one that is kept and one that is not
             for (int r = lanes; r < L; r += lanes) {
               const float o = __shfl(b1, (l - r) & (L - 1), L);
               const int ob = __shfl(before, (l - r) & (L - 1), L);
-              open |= fabsf(o - b1) <= group_error(error, o) && (ob < a.top_groups) != (before < a.top_groups);
+              open |= near_sums(o, b1, tolerance) && (ob < a.top_groups) != (before < a.top_groups);
             }
           }
 #pragma unroll

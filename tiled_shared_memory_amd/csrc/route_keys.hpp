@@ -17,6 +17,15 @@ constexpr int kNone = -0x7f800001;  // -inf: the key of what may not be chosen, 
 // How far two float32 keys may lie apart and be in the other order, where a score is off by `error` (score_error).
 constexpr float key_error(float error, float key) { return 2 * error + 0x1p-22f * __builtin_fabsf(key); }
 
+// How far a group's sum of keys b1 and b2 (0: of one key) may lie from another's and be in the other order.  Each key is
+// off by `error` and its own rounding, whatever their sum leaves of them, and the sum by one more: 2 error + 2^-23 (|b1| +
+// |b2|) for a group.  Twice that holds for two groups, whichever is the larger one's: of two groups one at least finds the
+// other near.  (And twice the roundings' part, for those of the comparison.)
+constexpr float group_tolerance(float error, float b1, float b2) {
+  return 4 * error + 0x1p-21f * (__builtin_fabsf(b1) + __builtin_fabsf(b2));
+}
+constexpr bool near_sums(float other, float own, float tolerance) { return __builtin_fabsf(other - own) <= tolerance; }
+
 // The least key that may be as large as the smallest chosen one: that one at most, and above kNone, since places without
 // an expert hold it (from a key of float32's lowest value the difference is -inf, from an infinite one NaN).
 constexpr int near_limit(int least, float error) {
