@@ -89,3 +89,31 @@ def test_groups_whose_biases_cancel(E, k, G, top, size, score):
         ids, _ = tsm.route_tokens(x, k, score=score, bias=bias, groups=G, top_groups=top, group_best=2)
         want = ref.choose(x.double(), k, score, bias, G, top, 2)
         assert torch.equal(ids.long(), want), f"{int((ids.long() != want).any(1).sum())} tokens"
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("nbest", [1, 2])
+@pytest.mark.parametrize("E,k,G,top", [(64, 8, 8, 3), (60, 8, 12, 4), (160, 7, 8, 2), (300, 6, 3, 2), (512, 8, 64, 9),
+                                       (64, 12, 8, 2), (160, 33, 8, 3), (504, 20, 3, 2), (512, 64, 16, 5)])
+def test_groups_of_the_lowest_value(E, k, G, top, nbest, score):
+    """Groups masked by biases of float32's lowest value, whose sums pass its range, beside groups out of service and
+    others that a token has no logits for: the masked ones are still chosen before those."""
+    import torch
+
+    g = gen(E + k + G)
+    T, n = 96, E // G
+    low = torch.finfo(torch.float32).min
+    for left in (0, 1, top - 1, top + 1):
+        x = torch.randn((T, G, n), generator=g, device="cuda")
+        x[torch.rand((T, G), generator=g, device="cuda") < 0.4] = -math.inf
+        x[5] = -math.inf
+        bias = torch.full((G, n), low, device="cuda")
+        bias[torch.randperm(G, generator=g, device="cuda")[:left]] = 0.0
+        bias[G // 2, 1:] = low / 2
+        if left:
+            bias[0] = -math.inf
+        x, bias = x.view(T, E), bias.view(E)
+        say(f"[gpu] route groups of the lowest value {E} {k} {G} {top} {nbest} {score} {left}")
+        ids, w = tsm.route_tokens(x, k, score=score, bias=bias, groups=G, top_groups=top, group_best=nbest)
+        assert torch.equal(ids.long(), ref.choose(x.double(), k, score, bias, G, top, nbest))
+        assert torch.isfinite(w).all()

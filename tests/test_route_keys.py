@@ -19,6 +19,8 @@ int c_near_groups(float error, float a1, float a2, float b1, float b2) {
   return tsm::near_sums(b1 + b2, a1 + a2, tsm::group_tolerance(error, a1, a2)) ||
          tsm::near_sums(a1 + a2, b1 + b2, tsm::group_tolerance(error, b1, b2));
 }
+float c_group_sum(float b1, float b2) { return tsm::group_sum(b1, b2); }
+float c_group_tolerance(float error, float b1, float b2) { return tsm::group_tolerance(error, b1, b2); }
 int c_group_of(int e, int size) { return (int)tsm::group_of(e, tsm::group_magic(size)); }
 }
 """
@@ -34,6 +36,8 @@ def keys(tmp_path_factory):
     lib = ctypes.CDLL(str(d / "k.so"))
     lib.c_ordered.argtypes = [ctypes.c_float]
     lib.c_near_groups.argtypes = [ctypes.c_float] * 5
+    lib.c_group_sum.argtypes, lib.c_group_sum.restype = [ctypes.c_float] * 2, ctypes.c_float
+    lib.c_group_tolerance.argtypes, lib.c_group_tolerance.restype = [ctypes.c_float] * 3, ctypes.c_float
     lib.c_near_limit.argtypes = [ctypes.c_int, ctypes.c_float]
     return lib
 
@@ -78,3 +82,18 @@ def test_groups_in_the_other_order_are_near(keys, size, error):
             assert keys.c_near_groups(error, *map(float, k32.ravel())), (s, b)
     # (without biases the exact sums are too far apart for it; at 1e30 float64 too holds nothing of the scores)
     assert other > 20 or size in (0.0, 1e30)
+
+
+def test_sums_past_the_range_of_float32(keys):
+    """A group of experts is one also where its sum passes float32's range (a mask of its lowest value twice); what then
+    reads as equal is near, at a finite distance, and a group of none stays one."""
+    top, f = float(np.finfo(np.float32).max), keys.c_group_sum
+    assert f(-np.inf, 0.0) == -np.inf and f(0.5, 0.25) == 0.75 and f(-top, 0.0) == -top
+    pairs = [(-top, -top), (-top, 0.0), (0.25, -top), (-3e38, -1e38), (-3e38, -0.9e38), (-2e38, -1e38), (0.5, 0.25),
+             (top, 0.0), (top, top), (3e38, 2e38), (top, -top)]
+    for a in pairs:
+        assert np.isfinite(f(*a)), a
+        assert np.isfinite(keys.c_group_tolerance(2.0 ** -21, *a)), a
+        for b in pairs:
+            exact, got = sum(a) - sum(b), np.float64(f(*a)) - np.float64(f(*b))
+            assert np.sign(exact) == np.sign(got) or abs(got) <= keys.c_group_tolerance(2.0 ** -21, *a), (a, b)

@@ -211,7 +211,7 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, T *keys, T e
       b1 = k > b1 ? k : b1;
     }
     if (a.best == 1 || !(b2 > none)) b2 = 0;
-    of[p] = b1 + b2;
+    of[p] = group_sum(b1, b2);
     tolerance[p] = group_tolerance((float)error, (float)b1, (float)b2);
   }
   wave_sync();
@@ -611,7 +611,7 @@ __global__ __launch_bounds__(kThreads) void route8_kernel(RouteArgs first) {
           });
           if (a.best == 1 || !(b2 > -kInf)) b2 = 0.f;
           const float tolerance = group_tolerance(error, b1, b2);
-          b1 += b2;
+          b1 = group_sum(b1, b2);
           int before = 0;
           bool close = false;
           around_row<L>(b1, lanes, [&](float o, int r) {  // the other groups'
