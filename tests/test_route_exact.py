@@ -117,3 +117,57 @@ def test_groups_of_the_lowest_value(E, k, G, top, nbest, score):
         ids, w = tsm.route_tokens(x, k, score=score, bias=bias, groups=G, top_groups=top, group_best=nbest)
         assert torch.equal(ids.long(), ref.choose(x.double(), k, score, bias, G, top, nbest))
         assert torch.isfinite(w).all()
+
+
+def microseconds(call, turns=15):
+    import torch
+
+    call()
+    times = []
+    for _ in range(turns):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        call()
+        end.record()
+        end.synchronize()
+        times.append(start.elapsed_time(end) * 1e3)
+    return sorted(times)[turns // 2]
+
+
+@pytest.mark.parametrize("score,biased", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+@pytest.mark.parametrize("E,k,G,top,pow2", [(60, 4, 12, 5, 16), (45, 7, 9, 4, 16), (33, 8, 3, 2, 4), (160, 6, 5, 2, 8)])
+def test_any_number_of_groups_takes_the_usual_way(E, k, G, top, pow2, score, biased):
+    """Groups that are not a power of two are chosen as quickly as as large ones that are: what fills them up is no near
+    tie, which would have every token decided again in float64 (five times as long)."""
+    import torch
+
+    g = gen(E)
+    say(f"[gpu] route time of {G} groups {score} {biased}")
+    took = []
+    for experts, groups in ((E, G), (E // G * pow2, pow2)):
+        x = torch.randn((65536, experts), generator=g, device="cuda")
+        bias = 0.1 * torch.randn(experts, generator=g, device="cuda") if biased else None
+        ids, w = tsm.route_tokens(x, k, score=score, bias=bias, groups=groups, top_groups=top)
+        took.append(microseconds(lambda: tsm.route_tokens(x, k, score=score, bias=bias, groups=groups, top_groups=top,
+                                                          ids=ids, weights=w)))
+    assert took[0] <= 2 * took[1], took
+
+
+@pytest.mark.parametrize("k", [8, 16])
+@pytest.mark.parametrize("masked", ["logits", "bias"])
+def test_a_group_out_of_service_takes_the_usual_way(k, masked):
+    """A whole group without an expert to choose costs nothing, and its absence shows in no choice."""
+    import torch
+
+    g = gen(k)
+    E, G, top = 256, 8, 4
+    x = torch.randn((65536, E), generator=g, device="cuda")
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    kw = dict(score="sigmoid", groups=G, top_groups=top)
+    say(f"[gpu] route time of a group out of service {k} {masked}")
+    ids, w = tsm.route_tokens(x, k, bias=bias, **kw)
+    usual = microseconds(lambda: tsm.route_tokens(x, k, bias=bias, ids=ids, weights=w, **kw))
+    (x.view(-1, G, E // G) if masked == "logits" else bias.view(1, G, E // G))[:, 3] = -math.inf
+    took = microseconds(lambda: tsm.route_tokens(x, k, bias=bias, ids=ids, weights=w, **kw))
+    assert torch.equal(ids.long(), ref.choose(x.double(), k, "sigmoid", bias, G, top, 2))
+    assert took <= 2 * usual, (took, usual)

@@ -21,6 +21,9 @@ int c_near_groups(float error, float a1, float a2, float b1, float b2) {
 }
 float c_group_sum(float b1, float b2) { return tsm::group_sum(b1, b2); }
 float c_group_tolerance(float error, float b1, float b2) { return tsm::group_tolerance(error, b1, b2); }
+int c_near_sums(float o, float b1, float b2, float error) {
+  return tsm::near_sums(o, tsm::group_sum(b1, b2), tsm::group_tolerance(error, b1, b2));
+}
 int c_group_of(int e, int size) { return (int)tsm::group_of(e, tsm::group_magic(size)); }
 }
 """
@@ -38,6 +41,7 @@ def keys(tmp_path_factory):
     lib.c_near_groups.argtypes = [ctypes.c_float] * 5
     lib.c_group_sum.argtypes, lib.c_group_sum.restype = [ctypes.c_float] * 2, ctypes.c_float
     lib.c_group_tolerance.argtypes, lib.c_group_tolerance.restype = [ctypes.c_float] * 3, ctypes.c_float
+    lib.c_near_sums.argtypes = [ctypes.c_float] * 4
     lib.c_near_limit.argtypes = [ctypes.c_int, ctypes.c_float]
     return lib
 
@@ -97,3 +101,16 @@ def test_sums_past_the_range_of_float32(keys):
         for b in pairs:
             exact, got = sum(a) - sum(b), np.float64(f(*a)) - np.float64(f(*b))
             assert np.sign(exact) == np.sign(got) or abs(got) <= keys.c_group_tolerance(2.0 ** -21, *a), (a, b)
+
+
+def test_a_group_of_none_is_near_nothing(keys):
+    """Groups without an expert to choose (out of service, or only there to fill up a power of two) decide nothing; nor
+    does one of an infinite bias, unless the other has one too."""
+    near, top = keys.c_near_sums, float(np.finfo(np.float32).max)
+    for error in (2.0 ** -27, 2.0 ** -21, 2.0 ** -9):
+        for b1, b2 in ((0.5, 0.25), (1.0, 0.0), (-1e9, 0.0), (1e30, 1.0), (-top, -top), (top, top), (np.inf, 0.0),
+                       (-np.inf, 0.0)):
+            assert not near(-np.inf, b1, b2, error), (b1, b2)
+            assert not near(keys.c_group_sum(b1, b2), -np.inf, 0.0, error), (b1, b2)
+        assert not near(0.5, np.inf, 0.0, error) and not near(keys.c_group_sum(np.inf, 0.0), 0.5, 0.0, error)
+        assert near(0.5, 0.25, 0.25, error)

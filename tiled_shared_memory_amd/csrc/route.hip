@@ -220,6 +220,7 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, T *keys, T e
     if (l + p * L < a.groups) keys[l + p * L] = of[p];
   wave_sync();
   uint64_t kept = 0;
+  bool close = false;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     if (p * L >= a.groups) continue;  // uniform
@@ -228,9 +229,18 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs &a, T *keys, T e
     for (int o = 0; o < a.groups; ++o) {
       const T k = keys[o];
       before += k > of[p] || (k == of[p] && o < g);
-      if (error > 0 && g < a.groups && o != g) *open |= near_sums((float)k, (float)of[p], tolerance[p]);
+      if (error > 0) close |= g < a.groups && o != g && near_sums((float)k, (float)of[p], tolerance[p]);
     }
     kept |= row_ballot<L>(g < a.groups && before < a.top_groups && of[p] > none) << (p * L % 64);
+  }
+  if (error > 0 && __ballot(close)) {  // it matters between one that is kept and one that is not
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int g = l + p * L;
+      if (g >= a.groups) continue;
+      for (int o = 0; o < a.groups; ++o)
+        *open |= ((kept >> o ^ kept >> g) & 1) && near_sums((float)keys[o], (float)of[p], tolerance[p]);
+    }
   }
   wave_sync();
   return kept;

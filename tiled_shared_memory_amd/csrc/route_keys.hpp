@@ -29,9 +29,12 @@ constexpr double group_sum(double b1, double b2) { return b1 + b2; }
 // How far a group's sum of keys b1 and b2 (0: of one key) may lie from another's and be in the other order.  Each key is
 // off by `error` and its own rounding, whatever their sum leaves of them, and the sum by one more: 2 error + 2^-23 (|b1| +
 // |b2|) for a group.  Twice that holds for two groups, whichever is the larger one's: of two groups one at least finds the
-// other near.  (And twice the roundings' part, for those of the comparison.)
+// other near.  (And twice the roundings' part, for those of the comparison.)  Finite for infinite keys too, so that a
+// group of none, -inf, is near nothing.
 constexpr float group_tolerance(float error, float b1, float b2) {
-  return 4 * error + 0x1p-21f * __builtin_fabsf(b1) + 0x1p-21f * __builtin_fabsf(b2);
+  constexpr float top = __FLT_MAX__;
+  const float m1 = __builtin_fabsf(b1), m2 = __builtin_fabsf(b2);
+  return 4 * error + 0x1p-21f * (m1 < top ? m1 : top) + 0x1p-21f * (m2 < top ? m2 : top);
 }
 constexpr bool near_sums(float other, float own, float tolerance) { return __builtin_fabsf(other - own) <= tolerance; }
 
