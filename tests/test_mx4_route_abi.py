@@ -307,3 +307,18 @@ def test_allocations_are_made_on_the_stream_of_the_call(monkeypatch):
             made.clear()
             call()
             assert made == [want] * n
+
+
+@pytest.mark.parametrize("M,N,K,batch", [(1024, 1, 32, (1 << 20) + 1), (1, 1, 32, (1 << 31) - 1), (1, 128, 128, (1 << 30) + 1),
+                                         (16, 2000, 64, 1 << 23)])
+def test_problems_of_one_weight_that_one_grid_cannot_hold_stay_apart(M, N, K, batch):
+    """Joined they would pass a launch's work-items, and be refused; one after another they run."""
+    assert name_of(M * batch, N, K, shared=True) is None
+    assert name_of(M, N, K, batch=batch, shared=True) is not None
+
+
+def test_problems_of_one_weight_up_to_the_limit_run_as_one():
+    """(2^30 rows by 128 columns are 2^23 tiles of 512 work-items, 2^32 in all: one too many.)"""
+    assert name_of(1 << 30, 128, 128) is None
+    assert name_of(8, 128, 128, batch=(1 << 27) - 16, shared=True) == name_of((1 << 30) - 128, 128, 128) != "mx4_stream"
+    assert name_of(8, 128, 128, batch=1 << 27, shared=True) == "mx4_stream"

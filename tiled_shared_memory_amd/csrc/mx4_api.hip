@@ -117,8 +117,9 @@ int mx4_plan(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int
       if (ranges_overlap(C, c_bytes, in[i], bytes[i])) return fail(TSM_ERROR_INVALID_VALUE, "C overlaps %s", names[i]);
   }
   // Problems that share B and whose rows follow each other in A and C are one of all rows: B is read for all of them at
-  // once (64 of 16 x 4096 x 4096: 18 us, one by one 76).
-  if (batch > 1 && !rows && strideB == 0 && stride_sb == 0 && K > 0 && batch <= 0x7fffffffLL / M) {
+  // once (64 of 16 x 4096 x 4096: 18 us, one by one 76).  (Not of more rows than one grid of 128-tiles holds, below.)
+  if (batch > 1 && !rows && strideB == 0 && stride_sb == 0 && K > 0 && batch <= 0x7fffffffLL / M &&
+      (M * batch + 127) / 128 * ((N + 127) / 128) * 512 <= 0xffffffffLL) {
     const int64_t kb = mx4_code_bytes(K), nb = mx4_blocks(K);
     const bool one = M == 1;
     if ((one ? strideA >= kb : strideA == M * lda) && (one ? stride_sa >= nb : stride_sa == M * ld_sa) &&
