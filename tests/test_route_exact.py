@@ -171,3 +171,46 @@ def test_a_group_out_of_service_takes_the_usual_way(k, masked):
     took = microseconds(lambda: tsm.route_tokens(x, k, bias=bias, ids=ids, weights=w, **kw))
     assert torch.equal(ids.long(), ref.choose(x.double(), k, "sigmoid", bias, G, top, 2))
     assert took <= 2 * usual, (took, usual)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("near", [3, 9, 40])
+@pytest.mark.parametrize("E,k,G,top", [(64, 12, 1, 1), (256, 16, 8, 4), (512, 33, 16, 9), (504, 8, 3, 1), (504, 20, 3, 2),
+                                       (130, 64, 1, 1), (512, 64, 64, 30), (60, 4, 12, 5), (16, 9, 4, 3)])
+def test_near_ties_of_many_choices(E, k, G, top, near, score):
+    """Keys that float32 cannot tell apart inside the choice, at its border and past it, of more than 8 choices and of
+    groups that are no power of two."""
+    import torch
+
+    g = gen(E + near)
+    T = 400
+    x = torch.randn((1, E), generator=g, device="cuda").expand(T, E)
+    s = ref.scores(x[:1].double(), score)[0]
+    bias = 0.2 * torch.randn(E, generator=g, device="cuda")
+    key = s + bias
+    close = key.argsort(descending=True)[max(0, k - (near + 1) // 2):][:near]
+    bias[close] = (key[close[:1]] - s[close]).float()
+    x = (x.double() + torch.randint(-1, 2, (T, E), generator=g, device="cuda").double() * 2.0 ** -23).float()
+    say(f"[gpu] route near ties of many choices {E} {k} {G} {near} {score}")
+    for nbest in (1, 2):
+        ids, _ = tsm.route_tokens(x, k, score=score, bias=bias, groups=G, top_groups=top, group_best=nbest)
+        assert torch.equal(ids.long(), ref.choose(x.double(), k, score, bias, G, top, nbest))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,G,top", [(64, 6, 8, 3), (60, 8, 12, 5), (256, 8, 1, 1), (256, 16, 8, 4), (504, 8, 3, 2)])
+def test_infinite_biases(E, k, G, top, score):
+    """Biases of +inf choose their experts first, in the order of their indices; of -1e9 last."""
+    import torch
+
+    g = gen(E + k)
+    x = torch.randn((300, E), generator=g, device="cuda")
+    for share in (0.01, 0.1, 0.9):
+        at = torch.rand(E, generator=g, device="cuda") < share
+        for value in (math.inf, -1e9):
+            bias = torch.where(at, value, 0.1 * torch.randn(E, generator=g, device="cuda"))
+            say(f"[gpu] route infinite biases {E} {k} {G} {score} {share} {value}")
+            for nbest in (1, 2):
+                ids, w = tsm.route_tokens(x, k, score=score, bias=bias, groups=G, top_groups=top, group_best=nbest)
+                assert torch.equal(ids.long(), ref.choose(x.double(), k, score, bias, G, top, nbest))
+                assert torch.isfinite(w).all()
