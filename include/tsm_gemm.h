@@ -451,7 +451,9 @@ int moe_combine_backward(int64_t tokens, int64_t topk, int64_t hidden, const voi
  *   scales : (C + 31) / 32 bytes, one per block of 32 elements: E stands for
  *            2^(E - 127), and 255 for a block of NaN whatever its codes.
  * Leading dimensions and strides of codes and scales are in bytes; neither needs
- * any alignment (rows at multiples of 16 and 4 bytes are faster to read).
+ * any alignment.  The fast kernels of the products need all three: K a multiple of
+ * 128, rows of codes at multiples of 16 bytes, rows of scales at multiples of 4;
+ * every other product runs on the general kernels (mx4_block_*).
  *
  * mx4_quantize -- rows to that form: of each block's largest magnitude m
  *     E := max(0, 127 + floor(log2 m) - 2),   code := nearest to |X| / 2^(E - 127),
@@ -489,7 +491,10 @@ int gemm_mx4(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, con
 
 /* gemm_mx4_strided_batched, gemm_mx4_grouped -- as gemm_i8_strided_batched and
  * gemm_i8_grouped: `batch` products at strides (0 shares an operand), or experts'
- * slabs with row counts in device memory; an activation, in which a NaN stays one. */
+ * slabs with row counts in device memory; an activation, in which a NaN stays one.
+ * A grouped call's kernel is chosen by M, the rows of a slab, since its counts are
+ * known on the GPU only: slabs of thousands of rows run on large tiles however few
+ * of them are filled. */
 int gemm_mx4_strided_batched(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int64_t strideA,
                              const uint8_t *scale_a, int64_t ld_sa, int64_t stride_sa, const uint8_t *B, int64_t ldb,
                              int64_t strideB, const uint8_t *scale_b, int64_t ld_sb, int64_t stride_sb, void *C,
@@ -520,7 +525,10 @@ int gemm_mx4_float_a(int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx
 int64_t gemm_mx4_float_a_workspace_bytes(int64_t M, int64_t K, int64_t batch);
 
 /* tsm_gemm_mx4_kernel_name -- the kernel a gemm_mx4_strided_batched call (rows
- * NULL) or a gemm_mx4_grouped call would launch, or NULL. */
+ * NULL) or a gemm_mx4_grouped call would launch, or NULL.  A gemm_mx4_float_a call
+ * launches the same behind its quantisation, but for one or two rows that mx4_stream
+ * would multiply: those are quantised within the launch of a kernel of its own, which
+ * has no name here (TSM_GEMM_KERNEL=mx4_stream keeps to the two launches). */
 const char *tsm_gemm_mx4_kernel_name(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, int64_t strideA,
                                      const uint8_t *scale_a, int64_t ld_sa, int64_t stride_sa, const uint8_t *B,
                                      int64_t ldb, int64_t strideB, const uint8_t *scale_b, int64_t ld_sb,
@@ -544,7 +552,7 @@ const char *tsm_gemm_mx4_kernel_name(int64_t M, int64_t N, int64_t K, const uint
  *   weights : factor * s_e, or with renormalize factor * s_e over the sum of the
  *             chosen experts' s (finite, however small those are).
  * Equal keys (and sums) go to the lowest index.  The choice is the one of exact
- * scores, up to differences below 2^-50.  An expert whose logit (or bias) is -inf
+ * scores, up to differences of keys below 2^-50 (of keys past 1, 2^-50 of them).  An expert whose logit (or bias) is -inf
  * or NaN is never chosen, and where none is left the id is -1 and the weight 0: a
  * padded token with a row of -inf gets no expert.  A row with a NaN (or, for a
  * softmax, +inf) among its logits gets weights of NaN; its ids are those of its

@@ -20,7 +20,7 @@
 // everything in flight.
 //
 // Measured, bf16 out, weights from memory (a copy reaches 5.1 TB/s on the same card):
-//   16 x 16384 x 8192   17.0 us a call, 4.2 TB/s  (scales in registers, whose copies at
+//   16 x 16384 x 8192   16.0 us a call, 4.5 TB/s  (scales in registers, whose copies at
 //                       the loop's end waited: 21.5; then weights through all caches: 18.3)
 //   8 x 28672 x 8192    26.5 us, 4.7 TB/s     8 x 8192 x 28672   23.0 us, 5.4 TB/s
 //   64 groups of 4 x 2048 x 4096   48.5 us, 5.9 TB/s (part of it from the cache)

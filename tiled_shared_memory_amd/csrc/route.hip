@@ -19,9 +19,13 @@
 // holds it.
 //
 // A choice is made by the exact keys.  Keys computed in float32 are off by a
-// known bound (score_error); where two neighbours in the order, or two groups, lie
-// nearer than that, the token is decided again by a whole wave in float64.  Which
-// experts are chosen is therefore the same whatever exp() rounds to.
+// known bound (score_error; route_keys.hpp has what follows from it); where two
+// neighbours in the order, or a group that is kept and one that is not, lie nearer
+// than that, the token is decided again by a whole wave in float64.  Which experts
+// are chosen is therefore the same whatever exp() rounds to.  (That takes five times
+// as long, so what decides nothing, such as a group without an expert to choose, must
+// not read as near: 65536 x 60 in 12 groups 41 us, 116 with the four groups that fill
+// up its lanes taken for near ones.)
 //
 // Weights of renormalised scores are formed from exp(x - max) over the chosen
 // ones, so they neither underflow nor overflow.
@@ -30,6 +34,8 @@
 // 4 of 8 groups takes 35-41 us, 1140 vector instructions per wave (four tokens), which
 // keep the SIMDs busy for 70% of its cycles; 20 us of it are the bias and the groups
 // (scores of every expert, near ties).  The logits alone would take 14 us from memory.
+// More than 8 choices cost a search of the whole row each: 16 of 65536 x 256 in 4 of 8
+// groups 124 us, 33 without groups 145, 16 of 65536 x 512 132 and in 16 groups 207.
 // The gradient of the same, 18.5 us, moves its 113 MB at 6.1 TB/s.
 #include "elems.hpp"
 #include "route_internal.hpp"
@@ -42,12 +48,12 @@ constexpr int kThreads = 256;
 constexpr float kInf = __builtin_inff();
 
 // How far a float32 score may be from the exact one.  exp of d is off by |d| 1.5 * 2^-24 (the product with log2 e) and
-// 2^-23, relative.
+// 2^-23, relative; of a difference d by another |d| 2^-24.
 //  * A sigmoid s = 1 / (1 + exp(-x)) takes s (1 - s) of that, at most 0.224 / |x| and 1/4 of it, and adds a sum (2^-24)
 //    and a reciprocal (2^-23): below 2^-21.
 //  * A softmax's score takes it whole, relative to itself, and |d| exp(-|d|) < 0.37; the sum's error is that of its
-//    terms in the mean (|d| is at most ln 512 in that mean, plus the logarithm of the largest score's share) and of 37
-//    additions, 32 in a lane and 5 over the lanes; with reciprocal and product below 2^-18 of the largest score.
+//    terms in the mean (|d| is at most ln 512 in that mean, plus the logarithm of the largest score's share) and of 21
+//    additions, 16 in a lane and 5 over the lanes; with reciprocal and product below 2^-18 of the largest score.
 __device__ __forceinline__ float score_error(bool sigmoid, float largest) {
   return sigmoid ? 0x1p-21f : 0x1p-18f * largest;
 }
