@@ -214,3 +214,27 @@ def test_infinite_biases(E, k, G, top, score):
                 ids, w = tsm.route_tokens(x, k, score=score, bias=bias, groups=G, top_groups=top, group_best=nbest)
                 assert torch.equal(ids.long(), ref.choose(x.double(), k, score, bias, G, top, nbest))
                 assert torch.isfinite(w).all()
+
+
+@pytest.mark.parametrize("k", [8, 12])
+@pytest.mark.parametrize("nbest", [1, 2])
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "bias"])
+def test_groups_of_infinite_and_of_the_largest_keys(k, nbest, biased):
+    """Sigmoid scores of logits of +inf, and biases of +inf, beside float32's largest value in groups before them."""
+    import torch
+
+    g = gen(k)
+    E, G, top = 64, 8, 2
+    big = torch.finfo(torch.float32).max
+    x = torch.randn((64, E), generator=g, device="cuda")
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda") if biased else None
+    row = torch.arange(64, device="cuda")
+    for at, value in ((row % 24, big), (row % 24 + 8, big), (row * 7 % E, math.inf), (row * 5 % 40 + 24, math.inf)):
+        if biased:
+            bias[at[:2] if value == big else at[2:4]] = value
+        else:
+            x[row, at] = value
+    say(f"[gpu] route groups of infinite keys {k} {nbest} {biased}")
+    ids, w = tsm.route_tokens(x, k, score="sigmoid", bias=bias, groups=G, top_groups=top, group_best=nbest)
+    assert torch.equal(ids.long(), ref.choose(x.double(), k, "sigmoid", bias, G, top, nbest))
+    assert torch.isfinite(w).all()

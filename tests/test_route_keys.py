@@ -93,6 +93,7 @@ def test_sums_past_the_range_of_float32(keys):
     reads as equal is near, at a finite distance, and a group of none stays one."""
     top, f = float(np.finfo(np.float32).max), keys.c_group_sum
     assert f(-np.inf, 0.0) == -np.inf and f(0.5, 0.25) == 0.75 and f(-top, 0.0) == -top
+    assert f(np.inf, 0.0) == f(np.inf, 1.0) == f(np.inf, np.inf) == f(np.inf, -top) == np.inf > f(top, top)
     pairs = [(-top, -top), (-top, 0.0), (0.25, -top), (-3e38, -1e38), (-3e38, -0.9e38), (-2e38, -1e38), (0.5, 0.25),
              (top, 0.0), (top, top), (3e38, 2e38), (top, -top)]
     for a in pairs:

@@ -17,12 +17,13 @@ constexpr int kNone = -0x7f800001;  // -inf: the key of what may not be chosen, 
 // How far two float32 keys may lie apart and be in the other order, where a score is off by `error` (score_error).
 constexpr float key_error(float error, float key) { return 2 * error + 0x1p-22f * __builtin_fabsf(key); }
 
-// The sum of a group's largest keys (b2 0: of one key; b1 -inf: it has none).  In float32 kept within the range, where
-// it is near (group_tolerance) all that it now equals: of two keys of the lowest value, a mask, it must not become -inf.
+// The sum of a group's largest keys (b2 0: of one key; b1 -inf: it has none).  Of finite keys it is kept within float32's
+// range, where it is near (group_tolerance) all that it now equals: of two keys of the lowest value, a mask, it must not
+// become -inf.
 constexpr float group_sum(float b1, float b2) {
   constexpr float top = __FLT_MAX__;
   const float sum = b1 + b2;
-  return !(b1 >= -top) ? b1 : sum < -top ? -top : sum > top ? top : sum;
+  return !(__builtin_fabsf(b1) <= top) ? b1 : sum < -top ? -top : sum > top ? top : sum;
 }
 constexpr double group_sum(double b1, double b2) { return b1 + b2; }
 
@@ -30,7 +31,7 @@ constexpr double group_sum(double b1, double b2) { return b1 + b2; }
 // off by `error` and its own rounding, whatever their sum leaves of them, and the sum by one more: 2 error + 2^-23 (|b1| +
 // |b2|) for a group.  Twice that holds for two groups, whichever is the larger one's: of two groups one at least finds the
 // other near.  (And twice the roundings' part, for those of the comparison.)  Finite for infinite keys too, so that a
-// group of none, -inf, is near nothing.
+// group of none, or of an infinite key, is near nothing.
 constexpr float group_tolerance(float error, float b1, float b2) {
   constexpr float top = __FLT_MAX__;
   const float m1 = __builtin_fabsf(b1), m2 = __builtin_fabsf(b2);
